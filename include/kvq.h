@@ -85,6 +85,7 @@ typedef enum { KVQ_F16 = 0, KVQ_F32 = 1 } kvq_dtype;
 #define KVQ_DEVERR_SEQ_LEN 0x8u      /* a seq_len above max_seq_len or max_pages * page_size */
 #define KVQ_DEVERR_TIMEOUT 0x10u     /* a bounded wait on a copy ran out (work skipped) */
 #define KVQ_DEVERR_SEQ_ID 0x20u      /* kvq_kvarn_append: a seq_id outside [0, num_seqs) */
+#define KVQ_DEVERR_POSITION 0x80u    /* kvq_norm_rope_write: a position outside [0, max_position) */
 #define KVQ_DEVERR_BOUNDS 0x40u      /* debug build only: a store fell outside the buffer its
                                         arguments describe (skipped); see kvq_debug_build */
 
@@ -193,6 +194,63 @@ kvq_status kvq_cache_read_errors(kvq_cache* cache, uint32_t* flags, int clear, v
  * IEEE round-to-nearest; results are bit-identical to the specification. */
 kvq_status kvq_quantize_write(kvq_cache* cache, const void* k, const void* v,
                               const int32_t* slot_mapping, int num_tokens, int mode, void* stream);
+
+/* ---- Reading back --------------------------------------------------------
+ * The values the cache holds at `slot_mapping`, as dense rows: codes times
+ * their scales in fp32 (NVFP4 code s_b s_t), rounded once to out_dtype; KVarN
+ * rows r_t c_d (scale q + zero) rotated back to the input domain by the
+ * normalised Hadamard transform in fp32.  ([P3]: x^ = q s; [P5] KV 的写入与读取路径.)
+ *  slot_mapping  device int32 [num_tokens]; a negative slot leaves its output
+ *                rows as they were; a slot past the pool does too and sets
+ *                KVQ_DEVERR_SLOT_RANGE.  The same slot may appear twice.
+ *  k_out, v_out  device [num_tokens][num_kv_heads][head_dim], out_dtype,
+ *                16-byte aligned; either may be NULL (that side is not read)
+ * KVarN reads quantized tiles only (an open tile's rows are in the caller's
+ * tail buffer as they were written).  A value outside the fp16 range reads as
+ * infinity at out_dtype KVQ_F16. */
+kvq_status kvq_cache_read(const kvq_cache* cache, const int32_t* slot_mapping, int num_tokens, void* k_out,
+                          void* v_out, int out_dtype, void* stream);
+
+/* ---- Norm, rotation and quantized write in one pass -----------------------
+ * For every token and head, with x the head's row of head_dim values:
+ *   y = x w / sqrt(mean(x^2) + eps)              (y = x where the weight is NULL)
+ *   the first rot_dim values of y are rotated by the token's angles: for pair i
+ *   of rot_dim / 2, (a, b) = values (i, i + rot_dim/2), or (2i, 2i + 1) when
+ *   `interleaved`:  a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i
+ * and the result is rounded once to io_dtype.  Queries go to q_out; keys (from
+ * their rounded rows) and values are quantized into the cache as by
+ * kvq_quantize_write, whose rules for slots hold here too: the slots of one
+ * call are distinct, a negative slot writes nothing to the cache, a slot past
+ * the pool sets KVQ_DEVERR_SLOT_RANGE.  The rotated rows are the correctly
+ * rounded values of the formula (evaluated to about 2^-44 where fp32 does not
+ * settle the rounding).
+ * All pointers are device pointers, 16-byte aligned (positions, slot_mapping: 4). */
+typedef struct {
+  const void* q;      /* io_dtype, token t's heads at q + t * q_stride: [num_q_heads][head_dim] */
+  const void* k;      /* [num_kv_heads][head_dim] at k + t * k_stride */
+  const void* v;      /* likewise; may be NULL without slot_mapping */
+  int64_t q_stride;   /* elements between tokens (a fused projection's row); multiples of 16 bytes */
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* positions;  /* [num_tokens]; one outside [0, max_position) skips its token (its q_out and
+                                k_out rows stay as they were) and sets KVQ_DEVERR_POSITION */
+  const float* cos_sin;      /* [max_position][rot_dim]: rot_dim/2 cosines, then rot_dim/2 sines */
+  const void* q_weight;      /* [head_dim] io_dtype, or NULL: no norm of the queries */
+  const void* k_weight;      /* [head_dim] io_dtype, or NULL: no norm of the keys */
+  const int32_t* slot_mapping; /* [num_tokens], or NULL: the cache is not written */
+  void* q_out;        /* [num_tokens][num_q_heads][head_dim], io_dtype; may be q itself where q is dense */
+  void* k_out;        /* [num_tokens][num_kv_heads][head_dim] rotated keys, or NULL; may be k itself */
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t rot_dim;      /* a multiple of 16, at most head_dim; 0 rotates nothing (positions and cos_sin
+                           are not read and may be NULL) */
+  int32_t max_position; /* rows of cos_sin */
+  int32_t interleaved;
+  float eps;            /* >= 0 */
+} kvq_norm_rope;
+/* KVarN quantizes whole tiles: there slot_mapping must be NULL, and k_out and v
+ * go to kvq_kvarn_append or kvq_quantize_write (else KVQ_ERR_UNSUPPORTED). */
+kvq_status kvq_norm_rope_write(kvq_cache* cache, const kvq_norm_rope* r, int mode, void* stream);
 
 /* Decode plan: how many KV splits per (sequence, kv head), the tokens per
  * split, and the workspace bytes kvq_decode_attention needs for these sizes

@@ -24,6 +24,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE
           "--expt-relaxed-constexpr"]
 PER_FILE = {
     "kvq_write.cu": ["-fmad=false"],
+    "kvq_rope.cu": ["-fmad=false"],
 }
 
 

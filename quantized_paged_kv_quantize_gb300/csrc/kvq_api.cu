@@ -309,6 +309,61 @@ kvq_status kvq_quantize_write(kvq_cache* cache, const void* k, const void* v, co
   return KVQ_OK;
 }
 
+kvq_status kvq_cache_read(const kvq_cache* cache, const int32_t* slot_mapping, int num_tokens, void* k_out,
+                          void* v_out, int out_dtype, void* stream) {
+  kvq_status s = check_cache(cache);
+  if (s) return s;
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
+  if (out_dtype != KVQ_F16 && out_dtype != KVQ_F32) return fail(KVQ_ERR_UNSUPPORTED, "out_dtype %d", out_dtype);
+  if (num_tokens == 0 || (!k_out && !v_out)) return KVQ_OK;
+  if (!slot_mapping || !aligned(slot_mapping, 4))
+    return fail(KVQ_ERR_INVALID_ARG, "slot_mapping must be non-NULL and 4-byte aligned");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(KVQ_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  if (cache->cfg.num_kv_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", cache->cfg.num_kv_heads);
+  cudaError_t e = kvq::launch_cache_read(cache, slot_mapping, num_tokens, k_out, v_out, out_dtype,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_norm_rope_write(kvq_cache* cache, const kvq_norm_rope* r, int mode, void* stream) {
+  kvq_status s = check_cache(cache);
+  if (s) return s;
+  if (mode != cache->cfg.mode)
+    return fail(KVQ_ERR_MODE_MISMATCH, "write mode %d but the cache holds mode %d", mode, cache->cfg.mode);
+  if (!r) return fail(KVQ_ERR_INVALID_ARG, "the argument struct is NULL");
+  const kvq_cache_config& c = cache->cfg;
+  if (r->num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "num_tokens < 0");
+  if (r->num_q_heads <= 0) return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be positive");
+  if (r->rot_dim < 0 || r->rot_dim > c.head_dim || r->rot_dim % 16 != 0)
+    return fail(KVQ_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of 16 in [0, %d]", r->rot_dim, c.head_dim);
+  if (r->rot_dim && r->max_position <= 0) return fail(KVQ_ERR_INVALID_ARG, "max_position must be positive");
+  if (!(r->eps >= 0.0f) || r->eps > 3.0e38f) return fail(KVQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (r->slot_mapping && c.mode == KVQ_KVARN_K4V2_G128)
+    return fail(KVQ_ERR_UNSUPPORTED, "kvarn_k4v2_g128 quantizes whole tiles: take k_out and append it");
+  const long long qd = (long long)r->num_q_heads * c.head_dim, kd = (long long)c.num_kv_heads * c.head_dim;
+  const int per16 = c.io_dtype == KVQ_F16 ? 8 : 4;
+  if (r->q_stride < qd || r->k_stride < kd || (r->slot_mapping && r->v_stride < kd))
+    return fail(KVQ_ERR_INVALID_ARG, "a token stride is smaller than its heads");
+  if (r->q_stride % per16 || r->k_stride % per16 || (r->slot_mapping && r->v_stride % per16))
+    return fail(KVQ_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes");
+  if ((long long)r->num_q_heads + 2 * c.num_kv_heads > 65535)
+    return fail(KVQ_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (r->num_tokens == 0) return KVQ_OK;
+  if (!r->q || !r->k || !r->q_out || (r->slot_mapping && !r->v) || (r->rot_dim && (!r->cos_sin || !r->positions)))
+    return fail(KVQ_ERR_INVALID_ARG, "NULL q, k, v, positions, cos_sin or q_out");
+  if (!aligned(r->q, 16) || !aligned(r->k, 16) || !aligned(r->v, 16) || !aligned(r->cos_sin, 16) ||
+      !aligned(r->q_weight, 16) || !aligned(r->k_weight, 16) || !aligned(r->q_out, 16) || !aligned(r->k_out, 16) ||
+      !aligned(r->positions, 4) || !aligned(r->slot_mapping, 4))
+    return fail(KVQ_ERR_INVALID_ARG, "q, k, v, cos_sin, weights and outputs must be 16-byte aligned");
+  if (!(r->q_out == r->q ? r->q_stride == qd : true) || !(r->k_out == r->k ? r->k_stride == kd : true))
+    return fail(KVQ_ERR_INVALID_ARG, "an output in place of its input needs a dense input");
+  cudaError_t e = kvq::launch_norm_rope_write(cache, *r, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm, rotation and write launch");
+  return KVQ_OK;
+}
+
 kvq_status kvq_tensor_error_stats(const kvq_cache* cache, const void* k, const void* v, const int32_t* slot_mapping,
                                   int num_tokens, kvq_error_stats* dev_stats, void* stream) {
   kvq_status s = check_cache(cache);

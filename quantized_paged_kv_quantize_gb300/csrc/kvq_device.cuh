@@ -499,6 +499,9 @@ __device__ float merge_split_row(const DecodeArgs& a, long long base, int ns, fl
   return lsum > 0.0f ? acc / lsum : 0.0f;
 }
 
+// The span of the pool's (page, kv head) blocks: every store a write kernel makes.
+Span pool_blocks(const kvq_cache* c);
+
 // tcgen05 decode of the 4-bit page modes at head_dim 128 (kvq_decode_umma.cu):
 // whether a cache and query shape take it, its resident CTAs per SM, the pages
 // one split may hold, and the launch (decode only; the caller adds the combine).

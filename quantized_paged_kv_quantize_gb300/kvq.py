@@ -31,7 +31,7 @@ MODES = {
 }
 KVQ_F16, KVQ_F32 = 0, 1
 DEVERR = {0x1: "SLOT_RANGE", 0x2: "PAGE_RANGE", 0x4: "PARTIAL_TILE", 0x8: "SEQ_LEN", 0x10: "TIMEOUT",
-          0x20: "SEQ_ID"}
+          0x20: "SEQ_ID", 0x80: "POSITION"}
 
 EXPORTED = [
     "kvq_last_error", "kvq_version", "kvq_cache_bytes", "kvq_cache_block_bytes", "kvq_cache_alloc",
@@ -41,6 +41,7 @@ EXPORTED = [
     "kvq_kvarn_tail_bytes", "kvq_kvarn_append", "kvq_kvarn_decode_workspace_bytes", "kvq_kvarn_decode_attention",
     "kvq_decode_multi_plan", "kvq_decode_multi_workspace_bytes", "kvq_decode_attention_multi",
     "kvq_debug_build", "kvq_debug_bounds_selftest", "kvq_tensor_error_stats",
+    "kvq_cache_read", "kvq_norm_rope_write",
 ]
 
 
@@ -54,6 +55,17 @@ class CacheConfig(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("mode", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
+class NormRope(ctypes.Structure):
+    """kvq_norm_rope: the arguments of kvq_norm_rope_write."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("slot_mapping", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("max_position", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 def _load():
@@ -88,6 +100,8 @@ def _load():
         "kvq_decode_multi_workspace_bytes": (i32, [vp, i32, i32, i32, i32, ctypes.POINTER(sz)]),
         "kvq_decode_attention_multi": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp, i32, vp, sz,
                                              vp]),
+        "kvq_cache_read": (i32, [vp, vp, i32, vp, vp, i32, vp]),
+        "kvq_norm_rope_write": (i32, [vp, ctypes.POINTER(NormRope), i32, vp]),
         "kvq_kvarn_append": (i32, [vp, vp, vp, vp, vp, i32, vp, i32, vp]),
         "kvq_kvarn_decode_workspace_bytes": (i32, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
         "kvq_kvarn_decode_attention": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, f32, vp, vp, i32, vp, sz, vp]),
@@ -137,6 +151,32 @@ def _dtype_code(dt) -> int:
     if dt in (torch.float32, "f32", KVQ_F32):
         return KVQ_F32
     raise ValueError(f"unsupported dtype {dt}")
+
+
+def _take(t, name: str, cache: "KVCache", dtype, shape, dense: bool = True):
+    """The data pointer of tensor `t`, which must have this dtype and shape
+    (None: any size), lie on the cache's device, and be contiguous -- or, when
+    not `dense`, have contiguous trailing dimensions (a row of a wider tensor)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
+        raise ValueError(f"{name}: shape {tuple(have)}, expected {tuple('*' if w is None else w for w in shape)}")
+    if t.device != cache.pool.device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {cache.pool.device}")
+    if not t.is_contiguous():
+        if dense:
+            raise ValueError(f"{name}: not contiguous")
+        step = 1
+        for size, stride in zip(reversed(have[1:]), reversed(t.stride()[1:])):
+            if size != 1 and stride != step:
+                raise ValueError(f"{name}: the dimensions after the first must be contiguous")
+            step *= size
+    return t.data_ptr()
+
+
+def _io_torch(cache: "KVCache"):
+    return torch.float16 if cache.cfg.io_dtype == KVQ_F16 else torch.float32
 
 
 def make_config(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, mode,
@@ -365,3 +405,55 @@ def kvq_kvarn_decode_attention(cache: KVCache, q, block_table, seq_lens, tail, o
     _check(_lib.kvq_kvarn_decode_attention(cache.handle, _ptr(q), _ptr(block_table), mp, _ptr(seq_lens), B, Hq,
                                            max_seq_len, sm, _ptr(tail), _ptr(out), od, _ptr(workspace), wb,
                                            _stream(stream)))
+
+
+# ---- reading back, and norm + rotation + write in one pass
+def kvq_cache_read(cache: "KVCache", slot_mapping, k_out=None, v_out=None, *, stream=None):
+    """The values the cache holds at `slot_mapping` (int32 [n]): k_out and v_out
+    [n][Hkv][D], both fp16 or both fp32 (either may be None); rows of negative
+    slots stay as they were."""
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("k_out and v_out are both None")
+    n = slot_mapping.shape[0]
+    shape = (n, cache.cfg.num_kv_heads, cache.cfg.head_dim)
+    k = None if k_out is None else _take(k_out, "k_out", cache, out.dtype, shape)
+    v = None if v_out is None else _take(v_out, "v_out", cache, out.dtype, shape)
+    _check(_lib.kvq_cache_read(cache.handle, _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,)), n, k, v,
+                               _dtype_code(out.dtype), _stream(stream)))
+
+
+def kvq_norm_rope_write(cache: "KVCache", q, k, v, positions, cos_sin, q_out, *, slot_mapping=None, k_out=None,
+                        q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, mode=None,
+                        stream=None):
+    """RMS norm (where a weight [D] is given) and rotation of the heads of q
+    [n][Hq][D] and k [n][Hkv][D] by the table row cos_sin[positions[i]] (fp32
+    [max_position][rot_dim]: cosines, then sines; None: no rotation), rounded
+    once into q_out (and k_out); with slot_mapping, k and v [n][Hkv][D] are
+    quantized into the cache.  q, k and v may be slices of one projection's
+    rows (any token stride that is a multiple of 16 bytes)."""
+    c, dt = cache.cfg, _io_torch(cache)
+    n, Hq, D = q.shape[0], q.shape[1], c.head_dim
+    r = NormRope()
+    r.q = _take(q, "q", cache, dt, (n, Hq, D), dense=False)
+    r.k = _take(k, "k", cache, dt, (n, c.num_kv_heads, D), dense=False)
+    r.q_stride, r.k_stride = (t.stride(0) if n > 1 else t.shape[1] * D for t in (q, k))
+    if v is not None:
+        r.v = _take(v, "v", cache, dt, (n, c.num_kv_heads, D), dense=False)
+        r.v_stride = v.stride(0) if n > 1 else c.num_kv_heads * D
+    if cos_sin is not None:
+        r.positions = _take(positions, "positions", cache, torch.int32, (n,))
+        r.cos_sin = _take(cos_sin, "cos_sin", cache, torch.float32, (None, None))
+        r.max_position, r.rot_dim = cos_sin.shape
+    if q_weight is not None:
+        r.q_weight = _take(q_weight, "q_weight", cache, dt, (D,))
+    if k_weight is not None:
+        r.k_weight = _take(k_weight, "k_weight", cache, dt, (D,))
+    if slot_mapping is not None:
+        r.slot_mapping = _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,))
+    r.q_out = _take(q_out, "q_out", cache, dt, (n, Hq, D))
+    if k_out is not None:
+        r.k_out = _take(k_out, "k_out", cache, dt, (n, c.num_kv_heads, D))
+    r.num_tokens, r.num_q_heads, r.interleaved, r.eps = n, Hq, int(interleaved), eps
+    _check(_lib.kvq_norm_rope_write(cache.handle, ctypes.byref(r), cache.mode if mode is None else _mode(mode),
+                                    _stream(stream)))
