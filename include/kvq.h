@@ -86,6 +86,8 @@ typedef enum { KVQ_F16 = 0, KVQ_F32 = 1 } kvq_dtype;
 #define KVQ_DEVERR_TIMEOUT 0x10u     /* a bounded wait on a copy ran out (work skipped) */
 #define KVQ_DEVERR_SEQ_ID 0x20u      /* kvq_kvarn_append: a seq_id outside [0, num_seqs) */
 #define KVQ_DEVERR_POSITION 0x80u    /* kvq_norm_rope_write: a position outside [0, max_position) */
+#define KVQ_DEVERR_QUERY_RANGE 0x100u /* kvq_chunk_attention: cu_q_lens of a sequence not an ascending range of at
+                                        most max_q_len rows of the batch */
 #define KVQ_DEVERR_BOUNDS 0x40u      /* debug build only: a store fell outside the buffer its
                                         arguments describe (skipped); see kvq_debug_build */
 
@@ -311,6 +313,54 @@ kvq_status kvq_decode_attention_multi(const kvq_cache* cache, const void* q, con
                                       int num_q_heads, int max_seq_len, int mode, float softmax_scale,
                                       void* out, int out_dtype, void* workspace, size_t workspace_bytes,
                                       void* stream);
+
+/* ---- Chunk attention -------------------------------------------------------
+ * A batch of chunks of new tokens, of any lengths, over the paged cache that
+ * already holds those tokens: prompts from their first token, chunks of long
+ * prompts, drafted tokens, and single tokens, in one call ([P5] "K 与 V 的量化误差
+ * 进入 attention 的位置不同": A = softmax(QK^T/sqrt(d) + M), O = AV; chunked
+ * prefill and speculative decoding, 使用前仍应确认).  Query i of a sequence's m
+ * queries stands at position p = seq_len - m + i; with s_t = softmax_scale q.k_t,
+ *   logit_cap > 0:  s_t = logit_cap tanh(s_t / logit_cap)
+ *   alibi_slopes:   s_t = s_t - alibi_slopes[head] |p - t|
+ * it attends to the tokens t <= p, with window > 0 only those t > p - window,
+ * and (with prefix_lens) all tokens t < prefix_len, before or after it, inside
+ * the sequence.  A query at a negative position attends to nothing: output 0. */
+typedef struct {
+  float logit_cap;             /* 0: none */
+  int32_t window;              /* 0: none */
+  const float* alibi_slopes;   /* device [num_q_heads], or NULL */
+  const int32_t* prefix_lens;  /* device [num_seqs], or NULL */
+} kvq_attention_options;
+
+/* Plan of a chunk attention: the parts a sequence's token range is split into,
+ * and the workspace bytes the call needs for these sizes (0 with one part).
+ * max_q_len and max_seq_len are host upper bounds of the chunks and of
+ * seq_lens; of `options` (NULL: none) only window and whether prefix_lens is
+ * given matter. */
+kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int num_q_heads, int max_q_len,
+                          int max_seq_len, const kvq_attention_options* options, int* num_splits,
+                          size_t* workspace_bytes);
+
+/*  q            device [total_q][num_q_heads][head_dim], io_dtype of the cache
+ *  cu_q_lens    device int32 [num_seqs + 1]: sequence b's queries are rows
+ *               cu_q_lens[b] .. cu_q_lens[b+1] - 1 (a chunk may be empty; rows of
+ *               no sequence are neither read nor written).  A sequence whose
+ *               entries are not an ascending range of at most max_q_len rows
+ *               inside [0, total_q] is skipped and sets KVQ_DEVERR_QUERY_RANGE.
+ *  out          device [total_q][num_q_heads][head_dim], dtype out_dtype
+ *  options      NULL: none
+ * block_table, max_pages, seq_lens, max_seq_len, mode, softmax_scale and the
+ * workspace are as for kvq_decode_attention, as is the rule for the head group.
+ * A sequence's pages hold its queries' own tokens too (write them first).
+ * KVarN is not supported (KVQ_ERR_UNSUPPORTED): its open tile lies outside the
+ * pages.  A NaN stored as a value (an E4M3 NaN code) may reach the outputs of
+ * every query of its sequence's chunk. */
+kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_q, const int32_t* cu_q_lens,
+                               const int32_t* block_table, int max_pages, const int32_t* seq_lens, int num_seqs,
+                               int num_q_heads, int max_q_len, int max_seq_len, int mode, float softmax_scale,
+                               const kvq_attention_options* options, void* out, int out_dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* ---- KVarN open tiles ---------------------------------------------------
  * [P2] 注意事项: a KVarN tile is exactly one 128-token page, and the backend

@@ -474,6 +474,92 @@ kvq_status kvq_decode_attention_multi(const kvq_cache* cache, const void* q, con
   return KVQ_OK;
 }
 
+// ---- chunk attention
+namespace {
+kvq_status check_chunk(const kvq_cache* cache, int total_q, int num_seqs, int num_q_heads, int max_q_len,
+                       int max_seq_len, const kvq_attention_options* opt) {
+  kvq_status s = check_cache(cache);
+  if (s) return s;
+  const kvq_cache_config& c = cache->cfg;
+  if (c.mode == KVQ_KVARN_K4V2_G128)
+    return fail(KVQ_ERR_UNSUPPORTED, "chunk attention reads 16-token pages; kvarn_k4v2_g128 has its own decode calls");
+  if (total_q < 0 || num_seqs < 0 || max_q_len < 0 || max_seq_len < 0) return fail(KVQ_ERR_INVALID_ARG, "negative size");
+  if (num_q_heads <= 0 || num_q_heads % c.num_kv_heads != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
+                c.num_kv_heads);
+  if (num_q_heads / c.num_kv_heads > 8)
+    return fail(KVQ_ERR_UNSUPPORTED, "GQA group %d > 8", num_q_heads / c.num_kv_heads);
+  if (c.num_kv_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", c.num_kv_heads);
+  if (opt) {
+    if (!(opt->logit_cap >= 0.0f) || opt->logit_cap > 3.0e38f)
+      return fail(KVQ_ERR_INVALID_ARG, "logit_cap must be finite and >= 0");
+    if (opt->window < 0) return fail(KVQ_ERR_INVALID_ARG, "window < 0");
+  }
+  return KVQ_OK;
+}
+}  // namespace
+
+kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int num_q_heads, int max_q_len,
+                          int max_seq_len, const kvq_attention_options* options, int* num_splits,
+                          size_t* workspace_bytes) {
+  kvq_status s = check_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len, options);
+  if (s) return s;
+  const kvq::ChunkPlan p = kvq::plan_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len,
+                                           options ? options->window : 0, options && options->prefix_lens);
+  if (num_splits) *num_splits = p.num_splits;
+  if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
+  return KVQ_OK;
+}
+
+kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_q, const int32_t* cu_q_lens,
+                               const int32_t* block_table, int max_pages, const int32_t* seq_lens, int num_seqs,
+                               int num_q_heads, int max_q_len, int max_seq_len, int mode, float softmax_scale,
+                               const kvq_attention_options* options, void* out, int out_dtype, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (cache && mode != cache->cfg.mode)
+    return fail(KVQ_ERR_MODE_MISMATCH, "attention mode %d but the cache holds mode %d", mode, cache->cfg.mode);
+  kvq_status s = check_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len, options);
+  if (s) return s;
+  bool empty = false;
+  s = check_decode_args(cache, q, block_table, max_pages, seq_lens, total_q == 0 ? 0 : num_seqs, num_q_heads,
+                        max_seq_len, softmax_scale, out, out_dtype, false, nullptr, &empty);
+  if (s || empty) return s;
+  if (!cu_q_lens || !aligned(cu_q_lens, 4))
+    return fail(KVQ_ERR_INVALID_ARG, "cu_q_lens must be non-NULL and 4-byte aligned");
+  if (options && (!aligned(options->alibi_slopes, 4) || !aligned(options->prefix_lens, 4)))
+    return fail(KVQ_ERR_INVALID_ARG, "alibi_slopes and prefix_lens must be 4-byte aligned");
+  kvq::ChunkCall k;
+  k.window = options ? options->window : 0;
+  k.prefix_lens = options ? options->prefix_lens : nullptr;
+  const kvq::ChunkPlan p = kvq::plan_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len, k.window,
+                                           k.prefix_lens != nullptr);
+  if (p.workspace_bytes > 0) {
+    if (!workspace || workspace_bytes < p.workspace_bytes)
+      return fail(KVQ_ERR_CAPACITY, "workspace needs %zu bytes, got %zu", p.workspace_bytes,
+                  workspace ? workspace_bytes : 0);
+    if (!aligned(workspace, 16)) return fail(KVQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  }
+  k.q = q;
+  k.cu_q = cu_q_lens;
+  k.block_table = block_table;
+  k.seq_lens = seq_lens;
+  k.slopes = options ? options->alibi_slopes : nullptr;
+  k.out = out;
+  k.workspace = workspace;
+  k.total_q = total_q;
+  k.num_seqs = num_seqs;
+  k.num_q_heads = num_q_heads;
+  k.max_pages = max_pages;
+  k.max_q_len = max_q_len;
+  k.max_seq_len = max_seq_len;
+  k.out_dtype = out_dtype;
+  k.scale = softmax_scale;
+  k.cap = options ? options->logit_cap : 0.0f;
+  cudaError_t e = kvq::launch_chunk(cache, p, k, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  return KVQ_OK;
+}
+
 // ---- KVarN open tiles
 kvq_status kvq_kvarn_tail_bytes(const kvq_cache* cache, int num_seqs, size_t* bytes) {
   kvq_status s = check_cache(cache);

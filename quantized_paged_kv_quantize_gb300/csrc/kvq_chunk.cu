@@ -1,0 +1,480 @@
+// kvq_chunk.cu -- attention of ragged chunks of new tokens over the packed
+// paged cache (kvq_chunk_attention): the plan, the merge of split token ranges,
+// and the mma.sync kernel that takes fp32 queries or outputs and head_dim 32.
+//
+// For query i of a sequence's m new tokens, at position p = n - m + i:
+//   s_t = scale q . k_t,  s_t = cap tanh(s_t / cap),  s_t -= slope_h |p - t|
+//   o = sum_t softmax(s)_t v_t over t <= p (and t > p - window) or t < prefix
+// k_t, v_t are codes times scales; codes are exact in fp16, so both products
+// run on them and the scales go to the fp32 scores and into P.
+//
+// mma.sync kernel: a CTA of four warps takes 64 rows (query x head of a kv
+// head's group, 16 a warp) and walks over KT-token tiles.  The CTA's threads
+// bring a tile's packed words into registers one tile ahead, write the codes as
+// fp16 rows to shared memory, and each warp multiplies them with its rows:
+// S = Q K^T, online softmax in base 2 with the running maximum and sum in fp32,
+// O += P V with fp32 accumulators.  fp32 queries enter as an fp16 hi + lo pair
+// under a power of two per row, P always does (22 bits of each weight), so the
+// result keeps fp32 grade.  Per-token value scales reach P relative to the
+// largest one met so far (a power of two, moved with the maximum), which
+// keeps P inside fp16 whatever the values' magnitude.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kvq_chunk.cuh"
+#include "kvq_unpack.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16 * kWarps;
+
+template <int D>
+constexpr int kTile = D == 128 ? 32 : 64;  // tokens
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+// x = hi + lo in fp16 (the remainder of the first rounding is exact in fp32)
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  hi = h2_as_u32(h);
+  lo = h2_as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
+}
+// floor(log2 x) of a positive x, kept to exponents whose powers are normal
+__device__ __forceinline__ int exponent(float x) {
+  return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+template <int MODE, int D, bool QF32>
+__global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_constant__ ChunkArgs a) {
+  constexpr int KT = kTile<D>, ST = D + 8;  // smem row stride (halves): 16-byte chunks of 8 rows hit 8 bank groups
+  constexpr int J = D / 8, U = KT * J / kThreads;  // 8-channel units per row; units per thread and side
+  constexpr bool PT = kPerTokenScale<MODE>;
+  __shared__ __align__(16) __half ks[KT * ST], vs[KT * ST];
+  __shared__ float kscale[KT], vscale[KT];
+  __shared__ int vexp_s[2];
+  __shared__ RowTile tile_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  if (warp == 0) {
+    const RowTile t = find_tile(a, blockIdx.x, kRows, blockIdx.x == 0 && kvh == 0 && split == 0);
+    if (lane == 0) tile_s = t;
+  }
+  __syncthreads();
+  const RowTile t = tile_s;
+  if (t.seq < 0) return;
+  const TokenRange tr = token_range(a, t, KT);
+  const int i0 = (int)((long long)tr.tiles * split / a.num_splits);
+  const int i1 = (int)((long long)tr.tiles * (split + 1) / a.num_splits);
+
+  // this thread's rows g, g + 8 of its warp's 16
+  int pos[2], hq[2];
+  long long qrow[2];
+  bool real[2];
+  float slope[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = 16 * warp + g + 8 * u;
+    real[u] = r < t.count;
+    const int rr = t.r0 + (real[u] ? r : 0);
+    pos[u] = t.n - t.m + rr / a.G;
+    hq[u] = kvh * a.G + rr % a.G;
+    qrow[u] = (long long)(t.q0 + rr / a.G) * a.Hq + hq[u];
+    slope[u] = a.slopes ? __ldg(a.slopes + hq[u]) * kLog2e : 0.0f;
+  }
+  const RowSees sees[2] = {row_sees(a, tr, pos[0], real[0]), row_sees(a, tr, pos[1], real[1])};
+
+  // Q as A fragments
+  uint32_t qh[D / 16][4], ql[QF32 ? D / 16 : 1][4];
+  float qfac[2] = {1.0f, 1.0f};
+  if constexpr (QF32) {
+    const float* q = static_cast<const float*>(a.q);
+    float mx[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      for (int d = 2 * tq; d < D; d += 8) {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(q + qrow[u] * D + d));
+        mx[u] = fmaxf(mx[u], fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+      mx[u] = warp_max_xor(mx[u], 1, 2);
+      const int e = mx[u] > 0.0f ? exponent(mx[u]) : 0;
+      mx[u] = pow2(-e);
+      qfac[u] = pow2(e);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int u = f & 1, d = 16 * j + 2 * tq + 8 * (f >> 1);
+        const float2 x = __ldg(reinterpret_cast<const float2*>(q + qrow[u] * D + d));
+        split2(x.x * mx[u], x.y * mx[u], qh[j][f], ql[j][f]);
+      }
+  } else {
+    const __half* q = static_cast<const __half*>(a.q);
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        qh[j][f] = __ldg(reinterpret_cast<const uint32_t*>(q + qrow[f & 1] * D + 16 * j + 2 * tq + 8 * (f >> 1)));
+  }
+
+  float kfac = a.scale, vfac = 1.0f;
+  if constexpr (!PT) {
+    kfac *= *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
+    vfac = *reinterpret_cast<const float*>(a.pool + kHdrVScaleOffset);
+  }
+  const float rcap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+
+  // packed words of tile i: thread's units u = tid + 128 r -> token u / J, channels 8 (u % J) ..
+  Packed8 pk[U], pv[U];
+  float psc = 0.0f;  // per-token scale of token tid % KT, keys for tid < KT, values above
+  auto page_of = [&](int tok) -> int {  // the token's page, -1 past the sequence or out of the pool
+    if (tok >= t.n) return -1;
+    const int pid = __ldg(a.block_table + (long long)t.seq * a.max_pages + (tok >> 4));
+    if (pid < 0 || pid >= a.num_pages) {
+      set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
+      return -1;
+    }
+    return pid;
+  };
+  auto block = [&](int pid) { return a.pool + kHeaderBytes + ((size_t)pid * a.Hkv + kvh) * a.block_bytes; };
+  auto fetch = [&](int i) {
+    const int t0 = tr.tile(i) * KT;
+#pragma unroll
+    for (int r = 0; r < U; ++r) {
+      const int u = tid + kThreads * r, tok = t0 + u / J, j = u % J, pid = page_of(tok);
+      pk[r] = pv[r] = Packed8{make_uint2(0u, 0u), 0u};  // an absent token: zero codes and scales
+      if (pid >= 0) {
+        pk[r] = load_packed8<MODE, D, 0>(block(pid), tok & 15, j);
+        pv[r] = load_packed8<MODE, D, 1>(block(pid), tok & 15, j);
+      }
+    }
+    if constexpr (PT) {
+      psc = 0.0f;
+      if (tid < 2 * KT) {
+        const int tok = t0 + tid % KT, pid = page_of(tok);
+        if (pid >= 0)
+          psc = __ldg(reinterpret_cast<const float*>(block(pid) + (MODE == KVQ_INT4_PER_TOKEN_HEAD ? 16 * D : 32 * D) +
+                                                     (tid < KT ? 0 : 64)) + (tok & 15));
+      }
+    }
+  };
+  // missing pages inside the sequence are not seen
+  auto present = [&](int tok) { return tok < t.n && page_of(tok) >= 0; };
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+  float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
+  int vexp = -100;  // exponent that P is held relative to
+
+  if (i0 < i1) fetch(i0);
+  for (int i = i0; i < i1; ++i) {
+    const int t0 = tr.tile(i) * KT;
+    __syncthreads();  // the previous tile has been read
+    // absent tokens of the tile (past the sequence, missing pages): a flag in the scales' place
+#pragma unroll
+    for (int r = 0; r < U; ++r) {
+      const int u = tid + kThreads * r, tok = u / J, j = u % J;
+      uint32_t h[4];
+      codes8<MODE, 0>(pk[r], tok & 15, h);
+      *reinterpret_cast<uint4*>(ks + tok * ST + 8 * j) = make_uint4(h[0], h[1], h[2], h[3]);
+      codes8<MODE, 1>(pv[r], tok & 15, h);
+      *reinterpret_cast<uint4*>(vs + tok * ST + 8 * j) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    if (tid < 2 * KT) {
+      float* sc = tid < KT ? kscale : vscale;
+      const int k = tid % KT;
+      // an absent token is marked by a negative key scale
+      sc[k] = tid < KT ? (present(t0 + k) ? (PT ? psc : 1.0f) : -1.0f) : (PT ? psc : 1.0f);
+      if constexpr (PT) {
+        if (tid >= KT) {  // whole warps
+          const int e = __reduce_max_sync(kFull, psc > 0.0f ? exponent(psc) : -100);
+          if (lane == 0) vexp_s[(tid - KT) / 32] = e;
+        }
+      }
+    }
+    __syncthreads();
+    if (i + 1 < i1) fetch(i + 1);
+
+    // ---- S = Q K^T
+    float s[KT / 8][4];
+#pragma unroll
+    for (int n = 0; n < KT / 8; ++n) {
+      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 2) {
+        uint32_t b[4];
+        ldsm4(b, ks + (8 * n + (lane & 7)) * ST + 16 * j + 8 * (lane >> 3));
+        mma16816(s[n], qh[j], b[0], b[1]);
+        mma16816(s[n], qh[j + 1], b[2], b[3]);
+        if constexpr (QF32) {
+          mma16816(s[n], ql[j], b[0], b[1]);
+          mma16816(s[n], ql[j + 1], b[2], b[3]);
+        }
+      }
+    }
+
+    // ---- scores in log2 units, the row's maximum
+    const bool masked = !all_see(a, tr, t0, KT);
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < KT / 8; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int u = e >> 1, k = 8 * n + 2 * tq + (e & 1), tok = t0 + k;
+        const float sc = kscale[k];
+        float x = s[n][e] * qfac[u] * (kfac * sc);
+        if (a.cap > 0.0f) x = a.cap * tanhf(x * rcap);
+        x = x * kLog2e;
+        if (a.slopes) x -= slope[u] * fabsf((float)(pos[u] - tok));
+        if (sc < 0.0f || (masked && !sees[u](tok))) x = -INFINITY;
+        s[n][e] = x;
+        mx[u] = fmaxf(mx[u], x);
+      }
+    }
+    const int ve = PT ? (KT == 64 ? max(vexp_s[0], vexp_s[1]) : vexp_s[0]) : vexp;
+    const int vnew = max(vexp, ve);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      mx[u] = fmaxf(warp_max_xor(mx[u], 1, 2), m[u]);
+      const float al = ex2(m[u] - mx[u]);
+      l[u] *= al;
+      const float av = al * (PT ? pow2(max(vexp - vnew, -126)) : 1.0f);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][2 * u] *= av;
+        o[n][2 * u + 1] *= av;
+      }
+      m[u] = mx[u];
+    }
+    vexp = vnew;
+    const float vnorm = PT ? pow2(-vexp) : 1.0f;
+
+    // ---- P (times the value scale), split in fp16, and O += P V
+#pragma unroll
+    for (int j = 0; j < KT / 16; ++j) {
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int n = 2 * j + (f >> 1), u = f & 1;
+        float p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = s[n][2 * u + e];
+          p[e] = ex2(x - m[u]);
+          l[u] += p[e];
+          // a weight of zero stays zero whatever the scale of a token that is not seen
+          if constexpr (PT) p[e] = x == -INFINITY ? 0.0f : p[e] * (vscale[8 * n + 2 * tq + e] * vnorm);
+        }
+        split2(p[0], p[1], ph[f], pl[f]);
+      }
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        ldsm4_t(b, vs + (16 * j + (lane & 15)) * ST + 16 * n + 8 * (lane >> 4));
+        mma16816(o[2 * n], ph, b[0], b[1]);
+        mma16816(o[2 * n + 1], ph, b[2], b[3]);
+        mma16816(o[2 * n], pl, b[0], b[1]);
+        mma16816(o[2 * n + 1], pl, b[2], b[3]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    l[u] += __shfl_xor_sync(kFull, l[u], 1);
+    l[u] += __shfl_xor_sync(kFull, l[u], 2);
+    if (!real[u]) continue;
+    const float f = PT ? pow2(vexp) : vfac;
+    if (a.num_splits == 1) {
+      const float r = l[u] > 0.0f ? f / l[u] : 0.0f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const long long at = qrow[u] * D + 8 * n + 2 * tq;
+        const float x = l[u] > 0.0f ? o[n][2 * u] * r : 0.0f, y = l[u] > 0.0f ? o[n][2 * u + 1] * r : 0.0f;
+        if (a.out_f32) st_chk(reinterpret_cast<float2*>(static_cast<float*>(a.out) + at), make_float2(x, y), a.out_span, a.pool);
+        else st_chk(reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at), __floats2half2_rn(x, y), a.out_span, a.pool);
+      }
+    } else {
+      const long long pi = qrow[u] * a.num_splits + split;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        st_chk(reinterpret_cast<float2*>(a.ws_o + pi * D + 8 * n + 2 * tq), make_float2(o[n][2 * u] * f, o[n][2 * u + 1] * f),
+               a.ws_span, a.pool);
+      if (tq == 0) st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l[u] > 0.0f ? m[u] : -INFINITY, l[u]),
+                          a.ws_span, a.pool);
+    }
+  }
+}
+
+// Merge of the splits: a warp per row (query x head) of a row tile, D / 32
+// channels a lane.  A split without tokens has m = -inf, and its partial is not
+// read into the sum.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int rows) {
+  constexpr int C = D / 32;
+  __shared__ RowTile tile_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y;
+  pdl_wait_primary();
+  if (warp == 0) {
+    const RowTile t = find_tile(a, blockIdx.x, rows, false);
+    if (lane == 0) tile_s = t;
+  }
+  __syncthreads();
+  const RowTile t = tile_s;
+  if (t.seq < 0) return;
+  for (int r = warp; r < t.count; r += 8) {
+    const int rr = t.r0 + r;
+    const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+    const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
+    const float2 v = lane < a.num_splits ? ml[lane] : make_float2(-INFINITY, 0.0f);  // at most 32 splits
+    const float M = warp_max_xor(v.x, 1, 16);
+    const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
+    float L = v.y * w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+    float acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+    for (int s = 0; s < a.num_splits; ++s) {
+      const float ws = __shfl_sync(kFull, w, s);
+      if (ws == 0.0f) continue;
+      const float* src = a.ws_o + (row * a.num_splits + s) * D + C * lane;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += ws * src[c];
+    }
+    const float f = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float x = L > 0.0f ? acc[c] * f : 0.0f;
+      const long long at = row * D + C * lane + c;
+      if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
+      else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);
+    }
+  }
+}
+
+template <int D, bool QF32>
+cudaError_t launch_mma(int mode, const ChunkArgs& a, dim3 grid, cudaStream_t s) {
+  switch (mode) {
+    case KVQ_FP8_PER_TENSOR: chunk_mma_kernel<KVQ_FP8_PER_TENSOR, D, QF32><<<grid, kThreads, 0, s>>>(a); break;
+    case KVQ_INT8_PER_TOKEN_HEAD: chunk_mma_kernel<KVQ_INT8_PER_TOKEN_HEAD, D, QF32><<<grid, kThreads, 0, s>>>(a); break;
+    case KVQ_FP8_PER_TOKEN_HEAD: chunk_mma_kernel<KVQ_FP8_PER_TOKEN_HEAD, D, QF32><<<grid, kThreads, 0, s>>>(a); break;
+    case KVQ_NVFP4:
+    case KVQ_NVFP4_4OVER6: chunk_mma_kernel<KVQ_NVFP4, D, QF32><<<grid, kThreads, 0, s>>>(a); break;
+    case KVQ_INT4_PER_TOKEN_HEAD: chunk_mma_kernel<KVQ_INT4_PER_TOKEN_HEAD, D, QF32><<<grid, kThreads, 0, s>>>(a); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream) {
+  const dim3 grid((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, rows), a.Hkv);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = c->cfg.head_dim == 128 ? cudaLaunchKernelEx(&cfg, chunk_combine_kernel<128>, a, rows)
+                                         : cudaLaunchKernelEx(&cfg, chunk_combine_kernel<32>, a, rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Row tiles per kv head, splits of their token ranges, workspace.  The lengths
+// are on the device: every tile is taken to see max_seq_len tokens (a window
+// bounds what it sees).  A plan of s splits is estimated at
+//   ceil(units s / slots) waves x (token tiles / s + cost of a CTA)
+// as for the decode kernels; more splits than one are worth their partials'
+// way through memory only where a wave is not full or its last one is ragged.
+ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_heads, int max_q_len, int max_seq_len,
+                     int window, bool has_prefix) {
+  (void)max_q_len;
+  ChunkPlan p;
+  p.rows = kRows;
+  const int D = c->cfg.head_dim, kt = D == 128 ? kTile<128> : kTile<32>;
+  const int G = num_q_heads / c->cfg.num_kv_heads;
+  long long len = max_seq_len;
+  if (window > 0 && !has_prefix) len = std::min<long long>(len, (long long)window + kRows);
+  const long long tiles = (len + kt - 1) / kt;
+  const long long units = chunk_tile_bound(total_q, num_seqs, G, p.rows) * c->cfg.num_kv_heads;
+  const long long slots = 2ll * num_sms();  // CTAs side by side
+  constexpr long long kCost = 6;            // start-up, merge and partials of a CTA, in tiles
+  long long best = -1;
+  for (long long s = 1; s <= 32 && s <= std::max(1ll, tiles); ++s) {
+    const long long cost = (units * s + slots - 1) / slots * ((tiles + s - 1) / s + kCost);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.num_splits = (int)s;
+    }
+  }
+  if (p.num_splits > 1)
+    p.workspace_bytes = (size_t)total_q * num_q_heads * p.num_splits * (D + 2) * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkCall& k, cudaStream_t stream) {
+  ChunkArgs a;
+  a.pool = c->base;
+  a.q = k.q;
+  a.cu_q = k.cu_q;
+  a.block_table = k.block_table;
+  a.seq_lens = k.seq_lens;
+  a.prefix_lens = k.prefix_lens;
+  a.slopes = k.slopes;
+  a.out = k.out;
+  const int D = c->cfg.head_dim;
+  const size_t rows = (size_t)k.total_q * k.num_q_heads;
+  a.ws_o = static_cast<float*>(k.workspace);
+  a.ws_ml = plan.num_splits > 1 ? a.ws_o + rows * plan.num_splits * D : nullptr;
+  a.total_q = k.total_q;
+  a.B = k.num_seqs;
+  a.Hq = k.num_q_heads;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.num_pages = c->cfg.num_pages;
+  a.max_pages = k.max_pages;
+  a.max_q_len = k.max_q_len;
+  a.max_seq_len = k.max_seq_len;
+  a.window = k.window;
+  a.num_splits = plan.num_splits;
+  a.out_f32 = k.out_dtype == KVQ_F32;
+  a.scale = k.scale;
+  a.cap = k.cap;
+  a.block_bytes = c->block_bytes;
+  uint8_t* o = static_cast<uint8_t*>(k.out);
+  a.out_span = Span{o, o + rows * D * (a.out_f32 ? 4 : 2)};
+  uint8_t* w = static_cast<uint8_t*>(k.workspace);
+  a.ws_span = Span{w, w ? w + plan.workspace_bytes : nullptr};
+  const dim3 grid((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, kRows), a.Hkv, a.num_splits);
+  const bool qf32 = c->cfg.io_dtype == KVQ_F32;
+  const int mode = c->cfg.mode;
+  cudaError_t e = D == 128 ? (qf32 ? launch_mma<128, true>(mode, a, grid, stream) : launch_mma<128, false>(mode, a, grid, stream))
+                : D == 32  ? (qf32 ? launch_mma<32, true>(mode, a, grid, stream) : launch_mma<32, false>(mode, a, grid, stream))
+                           : cudaErrorInvalidValue;
+  if (e != cudaSuccess || a.num_splits == 1) return e;
+  return launch_chunk_combine(c, a, kRows, stream);
+}
+
+}  // namespace kvq

@@ -51,6 +51,28 @@ cudaError_t launch_cache_read(const kvq_cache* c, const int32_t* slots, int num_
                               int out_dtype, cudaStream_t stream);
 cudaError_t launch_norm_rope_write(const kvq_cache* c, const kvq_norm_rope& r, cudaStream_t stream);
 
+// Chunk attention (kvq_chunk.cu).
+struct ChunkPlan {
+  int rows = 0;        // (query, head) rows of a CTA
+  int num_splits = 1;  // parts of a row tile's token range
+  size_t workspace_bytes = 0;
+};
+struct ChunkCall {
+  const void* q;
+  const int32_t* cu_q;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* prefix_lens;
+  const float* slopes;
+  void* out;
+  void* workspace;
+  int total_q, num_seqs, num_q_heads, max_pages, max_q_len, max_seq_len, window, out_dtype;
+  float scale, cap;
+};
+ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_heads, int max_q_len, int max_seq_len,
+                     int window, bool has_prefix);
+cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkCall& k, cudaStream_t stream);
+
 // num_seqs counts sequences; each has num_queries query rows (multi-query decode).
 DecodePlan plan_decode(const kvq_cache* c, int num_seqs, int num_q_heads, int max_seq_len, int num_queries = 1);
 cudaError_t launch_decode(const kvq_cache* c, const DecodePlan& plan, const void* q, const int32_t* block_table,

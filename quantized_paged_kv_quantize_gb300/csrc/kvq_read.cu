@@ -14,6 +14,7 @@
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_unpack.cuh"
 
 namespace kvq {
 namespace {
@@ -49,83 +50,17 @@ __device__ __forceinline__ void store8<float>(float* p, const float* f, const Sp
   st_chk(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]), span, pool);
 }
 
-__device__ __forceinline__ void half2_to_f32(const uint32_t* h, float* f) {
+// Codes (exact in fp16) times their scale, rounded once in fp32.
+template <int MODE, int SIDE>
+__device__ __forceinline__ void values(const Packed8& p, int off, float st, float* f) {
+  uint32_t h[4];
+  codes8<MODE, SIDE>(p, off, h);
+  const float s = kPerTokenScale<MODE> ? __uint_as_float(p.scale) : st;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 t = __half22float2(u32_as_h2(h[i]));
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-
-// One lane's share of a stored row: the payload words of its eight channels
-// and their scale (the per-token fp32 scale, or the E4M3 block scale's byte).
-struct Packed {
-  uint2 code;
-  uint32_t scale;
-};
-
-template <int MODE, int D, int SIDE>
-__device__ __forceinline__ Packed load_packed(const uint8_t* blk, int off, int j) {
-  constexpr int P = 16;
-  Packed p{make_uint2(0u, 0u), 0u};
-  if constexpr (MODE == KVQ_FP8_PER_TENSOR || MODE == KVQ_INT8_PER_TOKEN_HEAD || MODE == KVQ_FP8_PER_TOKEN_HEAD) {
-    p.code = __ldg(reinterpret_cast<const uint2*>(blk + SIDE * P * D + off * D + kVec * j));
-    if constexpr (MODE != KVQ_FP8_PER_TENSOR)
-      p.scale = __ldg(reinterpret_cast<const uint32_t*>(blk + 2 * P * D + SIDE * 4 * P + 4 * off));
-  } else {
-    if constexpr (SIDE == 0)
-      p.code.x = __ldg(reinterpret_cast<const uint32_t*>(blk + off * (D / 2) + kVec / 2 * j));
-    else
-      p.code = __ldg(reinterpret_cast<const uint2*>(blk + P * D / 2 + (off >> 1) * D + kVec * j));
-    if constexpr (MODE == KVQ_INT4_PER_TOKEN_HEAD)
-      p.scale = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D + SIDE * 4 * P + 4 * off));
-    else
-      p.scale = __ldg(blk + P * D + SIDE * (P * D / 16) + off * (D / 16) + (kVec * j) / 16);
-  }
-  return p;
-}
-
-template <int MODE, int SIDE>
-__device__ __forceinline__ void values(const Packed& p, int off, float st, float* f) {
-  if constexpr (MODE == KVQ_INT8_PER_TOKEN_HEAD) {
-    const float s = __uint_as_float(p.scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = (float)(int8_t)((i < 4 ? p.code.x : p.code.y) >> (8 * (i & 3))) * s;
-  } else if constexpr (MODE == KVQ_FP8_PER_TENSOR || MODE == KVQ_FP8_PER_TOKEN_HEAD) {
-    const float s = MODE == KVQ_FP8_PER_TENSOR ? st : __uint_as_float(p.scale);
-    const uint32_t h[4] = {e4m3x2_to_f16x2(p.code.x & 0xFFFFu), e4m3x2_to_f16x2(p.code.x >> 16),
-                           e4m3x2_to_f16x2(p.code.y & 0xFFFFu), e4m3x2_to_f16x2(p.code.y >> 16)};
-    half2_to_f32(h, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= s;
-  } else if constexpr (MODE == KVQ_NVFP4) {
-    uint32_t w = p.code.x;
-    if constexpr (SIDE == 1) {  // byte d of the pair row: this token's nibble of eight bytes -> four bytes of pairs
-      const int sh = 4 * (off & 1);
-      const uint32_t a = (p.code.x >> sh) & 0x0F0F0F0Fu, b = (p.code.y >> sh) & 0x0F0F0F0Fu;
-      const uint32_t even = prmt(a, b, 0x6420u), odd = prmt(a, b, 0x7531u);
-      w = even | (odd << 4);
-    }
-    uint32_t h[4];
-    e2m1x8_to_f16x2x4(w, h);
-    half2_to_f32(h, f);
-    const float sb = e4m3_to_f32(p.scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * sb * st;  // code times block scale is exact
-  } else {  // INT4
-    const float s = __uint_as_float(p.scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t n;  // the code in the top four bits
-      if constexpr (SIDE == 0) {  // key word: even channels in nibbles 0..3, odd in 4..7
-        n = p.code.x << (28 - 4 * ((i & 1) ? 4 + i / 2 : i / 2));
-      } else {  // value words of four channels: the even token's in the low half-word
-        n = (i < 4 ? p.code.x : p.code.y) << (28 - 4 * (i & 3) - 16 * (off & 1));
-      }
-      f[i] = (float)((int32_t)n >> 28) * s;
-    }
+    f[2 * i] = t.x * s;
+    f[2 * i + 1] = t.y * s;
   }
 }
 
@@ -149,13 +84,13 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_consta
   }
   const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.Hkv, h0 + a.heads_per_cta);
   for (int hb = h0; hb < h1; hb += kInFlight) {
-    Packed pk[kInFlight], pv[kInFlight];
+    Packed8 pk[kInFlight], pv[kInFlight];
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {
       const int h = min(hb + r, h1 - 1);
       const uint8_t* blk = a.pool + kHeaderBytes + ((size_t)page * a.Hkv + h) * a.block_bytes;
-      if (a.k) pk[r] = load_packed<MODE, D, 0>(blk, off, j);
-      if (a.v) pv[r] = load_packed<MODE, D, 1>(blk, off, j);
+      if (a.k) pk[r] = load_packed8<MODE, D, 0>(blk, off, j);
+      if (a.v) pv[r] = load_packed8<MODE, D, 1>(blk, off, j);
     }
 #pragma unroll
     for (int r = 0; r < kInFlight; ++r) {

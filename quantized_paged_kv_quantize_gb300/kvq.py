@@ -31,7 +31,7 @@ MODES = {
 }
 KVQ_F16, KVQ_F32 = 0, 1
 DEVERR = {0x1: "SLOT_RANGE", 0x2: "PAGE_RANGE", 0x4: "PARTIAL_TILE", 0x8: "SEQ_LEN", 0x10: "TIMEOUT",
-          0x20: "SEQ_ID", 0x80: "POSITION"}
+          0x20: "SEQ_ID", 0x80: "POSITION", 0x100: "QUERY_RANGE"}
 
 EXPORTED = [
     "kvq_last_error", "kvq_version", "kvq_cache_bytes", "kvq_cache_block_bytes", "kvq_cache_alloc",
@@ -41,7 +41,7 @@ EXPORTED = [
     "kvq_kvarn_tail_bytes", "kvq_kvarn_append", "kvq_kvarn_decode_workspace_bytes", "kvq_kvarn_decode_attention",
     "kvq_decode_multi_plan", "kvq_decode_multi_workspace_bytes", "kvq_decode_attention_multi",
     "kvq_debug_build", "kvq_debug_bounds_selftest", "kvq_tensor_error_stats",
-    "kvq_cache_read", "kvq_norm_rope_write",
+    "kvq_cache_read", "kvq_norm_rope_write", "kvq_chunk_plan", "kvq_chunk_attention",
 ]
 
 
@@ -66,6 +66,12 @@ class NormRope(ctypes.Structure):
                 ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
                 ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("max_position", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class AttentionOptions(ctypes.Structure):
+    """kvq_attention_options of kvq_chunk_attention."""
+    _fields_ = [("logit_cap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
 def _load():
@@ -102,6 +108,10 @@ def _load():
                                              vp]),
         "kvq_cache_read": (i32, [vp, vp, i32, vp, vp, i32, vp]),
         "kvq_norm_rope_write": (i32, [vp, ctypes.POINTER(NormRope), i32, vp]),
+        "kvq_chunk_plan": (i32, [vp, i32, i32, i32, i32, i32, ctypes.POINTER(AttentionOptions), ctypes.POINTER(i32),
+                                 ctypes.POINTER(sz)]),
+        "kvq_chunk_attention": (i32, [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32,
+                                      ctypes.POINTER(AttentionOptions), vp, i32, vp, sz, vp]),
         "kvq_kvarn_append": (i32, [vp, vp, vp, vp, vp, i32, vp, i32, vp]),
         "kvq_kvarn_decode_workspace_bytes": (i32, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
         "kvq_kvarn_decode_attention": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, f32, vp, vp, i32, vp, sz, vp]),
@@ -457,3 +467,39 @@ def kvq_norm_rope_write(cache: "KVCache", q, k, v, positions, cos_sin, q_out, *,
     r.num_tokens, r.num_q_heads, r.interleaved, r.eps = n, Hq, int(interleaved), eps
     _check(_lib.kvq_norm_rope_write(cache.handle, ctypes.byref(r), cache.mode if mode is None else _mode(mode),
                                     _stream(stream)))
+
+
+# ---- chunk attention
+def kvq_chunk_plan(cache: "KVCache", total_q: int, num_seqs: int, num_q_heads: int, *, max_q_len: int,
+                   max_seq_len: int, window: int = 0, has_prefix: bool = False):
+    """(parts of a token range, rows of q in all, workspace bytes) of a kvq_chunk_attention call of these sizes."""
+    ns, ws = ctypes.c_int(), ctypes.c_size_t()
+    opt = AttentionOptions(0.0, window, None, 1 if has_prefix else None)  # the plan reads only whether it is given
+    _check(_lib.kvq_chunk_plan(cache.handle, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len,
+                               ctypes.byref(opt), ctypes.byref(ns), ctypes.byref(ws)))
+    return ns.value, total_q, ws.value
+
+
+def kvq_chunk_attention(cache: "KVCache", q, cu_q_lens, block_table, seq_lens, out, *, max_q_len: int,
+                        max_seq_len: int, softmax_scale: Optional[float] = None, logit_cap: float = 0.0,
+                        alibi_slopes=None, window: int = 0, prefix_lens=None, workspace=None, mode=None, stream=None):
+    """q, out [total_q][Hq][D]: sequence b's queries are rows cu_q_lens[b] ..
+    cu_q_lens[b + 1] - 1, the last of its seq_lens[b] tokens; causal, with an
+    optional score cap, distance bias (slopes fp32 [Hq]), window and bidirectional
+    prefix (int32 [B])."""
+    total, Hq, D = q.shape
+    B = seq_lens.shape[0]
+    opt = None
+    if logit_cap != 0.0 or alibi_slopes is not None or window != 0 or prefix_lens is not None:
+        opt = ctypes.byref(AttentionOptions(
+            logit_cap, window,
+            None if alibi_slopes is None else _take(alibi_slopes, "alibi_slopes", cache, torch.float32, (Hq,)),
+            None if prefix_lens is None else _take(prefix_lens, "prefix_lens", cache, torch.int32, (B,))))
+    _check(_lib.kvq_chunk_attention(
+        cache.handle, _take(q, "q", cache, _io_torch(cache), (None, None, cache.cfg.head_dim)), total,
+        _take(cu_q_lens, "cu_q_lens", cache, torch.int32, (B + 1,)),
+        _take(block_table, "block_table", cache, torch.int32, (B, None)), block_table.shape[1],
+        _take(seq_lens, "seq_lens", cache, torch.int32, (B,)), B, Hq, max_q_len, max_seq_len,
+        cache.mode if mode is None else _mode(mode), D ** -0.5 if softmax_scale is None else softmax_scale, opt,
+        _take(out, "out", cache, out.dtype, (total, Hq, D)), _dtype_code(out.dtype), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
