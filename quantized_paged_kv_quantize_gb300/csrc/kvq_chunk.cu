@@ -402,25 +402,36 @@ cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int row
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Row tiles per kv head, splits of their token ranges, workspace.  The lengths
-// are on the device: every tile is taken to see max_seq_len tokens (a window
-// bounds what it sees).  A plan of s splits is estimated at
+// The tcgen05 kernel takes fp16 in and out at head_dim 128; its variant goes by
+// the longest chunk: up to 128 rows per kv head leave half of a 256-row CTA
+// empty, so those run as 128 rows and two streams of tokens.
+bool chunk_on_umma(const kvq_cache* c, int out_dtype) {
+  return c->cfg.head_dim == 128 && c->cfg.io_dtype == KVQ_F16 && out_dtype == KVQ_F16;
+}
+int umma_streams(int max_q_len, int G) { return (long long)max_q_len * G <= umma_chunk_rows(2) ? 2 : 1; }
+
+// Splits of the token ranges, and the workspace.  The lengths are on the device:
+// every tile of rows is taken to see max_seq_len tokens (a window bounds what
+// it sees).  A plan of s splits is estimated at
 //   ceil(units s / slots) waves x (token tiles / s + cost of a CTA)
 // as for the decode kernels; more splits than one are worth their partials'
 // way through memory only where a wave is not full or its last one is ragged.
 ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_heads, int max_q_len, int max_seq_len,
                      int window, bool has_prefix) {
-  (void)max_q_len;
   ChunkPlan p;
-  p.rows = kRows;
-  const int D = c->cfg.head_dim, kt = D == 128 ? kTile<128> : kTile<32>;
-  const int G = num_q_heads / c->cfg.num_kv_heads;
+  const int D = c->cfg.head_dim, G = num_q_heads / c->cfg.num_kv_heads;
+  const bool umma = chunk_on_umma(c, KVQ_F16);
+  const int streams = umma_streams(max_q_len, G);
+  const int rows = umma ? umma_chunk_rows(streams) : kRows;
+  const int kt = umma ? 128 * streams : kTile<32>;       // tokens a CTA takes at a time
+  const long long slots = (umma ? 1ll : 4ll) * num_sms();  // CTAs side by side
+  constexpr long long kCost = 4;                         // start-up, merge and partials of a CTA, in such tiles
   long long len = max_seq_len;
-  if (window > 0 && !has_prefix) len = std::min<long long>(len, (long long)window + kRows);
+  if (window > 0 && !has_prefix) len = std::min<long long>(len, (long long)window + max_q_len + kt);
   const long long tiles = (len + kt - 1) / kt;
-  const long long units = chunk_tile_bound(total_q, num_seqs, G, p.rows) * c->cfg.num_kv_heads;
-  const long long slots = 2ll * num_sms();  // CTAs side by side
-  constexpr long long kCost = 6;            // start-up, merge and partials of a CTA, in tiles
+  const long long per_seq = ((long long)max_q_len * G + rows - 1) / rows;
+  long long units = ((long long)total_q * G + rows - 1) / rows + num_seqs / 2;
+  units = std::min(units, per_seq * num_seqs) * c->cfg.num_kv_heads;
   long long best = -1;
   for (long long s = 1; s <= 32 && s <= std::max(1ll, tiles); ++s) {
     const long long cost = (units * s + slots - 1) / slots * ((tiles + s - 1) / s + kCost);
@@ -467,6 +478,12 @@ cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkC
   a.out_span = Span{o, o + rows * D * (a.out_f32 ? 4 : 2)};
   uint8_t* w = static_cast<uint8_t*>(k.workspace);
   a.ws_span = Span{w, w ? w + plan.workspace_bytes : nullptr};
+  if (chunk_on_umma(c, k.out_dtype)) {
+    const int streams = umma_streams(a.max_q_len, a.G);
+    cudaError_t e = launch_chunk_umma(c, a, streams, stream);
+    if (e != cudaSuccess || a.num_splits == 1) return e;
+    return launch_chunk_combine(c, a, umma_chunk_rows(streams), stream);
+  }
   const dim3 grid((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, kRows), a.Hkv, a.num_splits);
   const bool qf32 = c->cfg.io_dtype == KVQ_F32;
   const int mode = c->cfg.mode;

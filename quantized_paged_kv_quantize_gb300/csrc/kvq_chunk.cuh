@@ -142,4 +142,9 @@ __device__ __forceinline__ RowSees row_sees(const ChunkArgs& a, const TokenRange
 // Merge of the splits of the row tiles (kvq_chunk.cu); `rows`: of a tile.
 cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream);
 
+// The tcgen05 kernel (kvq_chunk_umma.cu): rows of a CTA, and the launch.
+// streams 1: 256 rows; 2: 128 rows and two streams of token tiles.
+constexpr int umma_chunk_rows(int streams) { return streams == 1 ? 256 : 128; }
+cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, int streams, cudaStream_t s);
+
 }  // namespace kvq

@@ -1,0 +1,737 @@
+// kvq_chunk_umma.cu -- chunk attention on the 5th-generation tensor cores
+// (tcgen05, scores, weights and accumulators in tensor memory) for fp16 queries
+// and outputs at head_dim 128, all 16-token-page modes.
+//
+// Mathematics (kvq_chunk.cu has the operator's definition).  With codes K, V
+// (exact in fp16) and scales apart, one 128 x 128 block of (row, token) pairs is
+//   S = Q K^T,  y = S ks_t (log2 units),  P = 2^(y - R) vs_t,  O += P V,  l += 2^(y - R)
+// in fp32 but for P, which is rounded to fp16 (relative 2^-12 a weight, random in
+// sign: below the output's own rounding).  R is a row's reference: the largest
+// y + floor(log2 vs) met, moved (O and l rescaled) only when a block passes it by
+// more than 2^8, so that P stays inside fp16's normal range whatever the
+// magnitude of scores and values.
+//
+// Roles (13 warps, 128 registers a thread, one CTA per SM):
+//  warps 0-3, 4-7  softmax: thread = row of S_0 / S_1;
+//  warps 8-11      dequantization: a warp takes two pages of a 128-token tile, their
+//                  packed words in registers one tile ahead, and writes the
+//                  codes as fp16 core matrices (8 tokens x 16 bytes), which
+//                  serve as the K-major B operand of Q K^T and, for V, as the
+//                  MN-major B operand of P V;
+//  warp 12         issues the tcgen05.mma.
+// Two blocks are in work at a time, so that the tensor cores run one block's
+// products during the other's softmax:
+//  kStreams = 1    256 rows; both blocks use the same tile of keys and values;
+//  kStreams = 2    128 rows; even and odd tiles are two streams with a reference,
+//                  sum and accumulator each, merged at the end.
+// Tensor memory: S_0 S_1 (128 columns each; P over the first 64 of S) O_0 O_1.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kvq_chunk.cuh"
+#include "kvq_unpack.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kD = 128;
+constexpr int kTok = 128;       // tokens of a tile
+constexpr int kThreads = 416;
+constexpr int kPages = 2;       // pages of a tile that one warp dequantizes
+constexpr int kOpBytes = kTok * kD * 2;  // one fp16 operand tile
+constexpr int kLbo = 128, kSbo = 2048;   // core matrices: along channels, along rows / tokens
+constexpr int kSlots = 4;       // tiles whose scales are kept
+constexpr float kSlack = 8.0f;  // log2
+constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
+
+template <int STREAMS>
+struct Smem {
+  static constexpr int Q = 0;
+  static constexpr int K = Q + (STREAMS == 1 ? 2 : 1) * kOpBytes;  // two stages each
+  static constexpr int V = K + 2 * kOpBytes;
+  static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] score factors
+  static constexpr int VS = KS + kSlots * kTok * 4;
+  static constexpr int ONES = VS + kSlots * kTok * 4;
+  static constexpr int PAGE = ONES + kTok * 4;                     // [slot][8] page states
+  static constexpr int BYTES = PAGE + kSlots * 8 * 4;
+  static constexpr size_t dynamic() { return BYTES + 128; }
+};
+constexpr int kMissing = INT32_MIN;  // page state: not there; else the exponent of its largest value scale
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// 32 columns of this warp's lanes; the registers hold them after the next tm_wait.
+__device__ __forceinline__ void tm_ld(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait(uint32_t* r) {  // the registers pass through, so that no use precedes the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ float2 pair(const uint32_t* r, int i) {
+  return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+__device__ __forceinline__ int exponent(float x) {  // floor(log2 x), x > 0, clamped
+  return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
+}
+
+// ---------------------------------------------------------------- dequantization of one page by one warp
+// A lane's packed words of a page: K and V.
+template <int MODE>
+struct Words {
+  static constexpr bool FOUR = MODE == KVQ_NVFP4 || MODE == KVQ_INT4_PER_TOKEN_HEAD;
+  static constexpr int N = FOUR ? 2 : 4;  // 16-byte loads per side
+  uint4 w[N];
+  uint32_t s[MODE == KVQ_NVFP4 ? 2 : 1];  // NVFP4: the two block scales of each load, as bytes 0 and 1
+};
+
+// 16-byte load r of this lane.  One-byte codes: token (lane & 7) + 8 (r & 1),
+// channels 16 c .. with c = (lane >> 3) + 4 (r >> 1).  Four-bit keys: token
+// (lane & 7) + 8 r, channels 32 (lane >> 3) ..; four-bit values: token pair
+// lane & 7, channels 16 c .. with c = (lane >> 3) + 4 r.
+template <int MODE, int SIDE>
+__device__ __forceinline__ void load_words(const uint8_t* blk, int lane, Words<MODE>& x) {
+  using W = Words<MODE>;
+  const int a = lane & 7, b = lane >> 3;
+#pragma unroll
+  for (int r = 0; r < W::N; ++r) {
+    int off;
+    if constexpr (!W::FOUR) off = SIDE * 16 * kD + (a + 8 * (r & 1)) * kD + 16 * (b + 4 * (r >> 1));
+    else if constexpr (SIDE == 0) off = (a + 8 * r) * (kD / 2) + 16 * b;
+    else off = 16 * kD / 2 + a * kD + 16 * (b + 4 * r);
+    x.w[r] = __ldg(reinterpret_cast<const uint4*>(blk + off));
+    if constexpr (MODE == KVQ_NVFP4) {
+      const uint8_t* s = blk + 16 * kD + SIDE * 16 * kD / 16;
+      if constexpr (SIDE == 0) x.s[r] = __ldg(reinterpret_cast<const uint16_t*>(s + (a + 8 * r) * 8 + 2 * b));
+      else x.s[r] = (uint32_t)__ldg(s + 16 * a + b + 4 * r) | ((uint32_t)__ldg(s + 16 * a + 8 + b + 4 * r) << 8);
+    }
+  }
+}
+template <int MODE>
+__device__ __forceinline__ void zero_words(Words<MODE>& x) {
+#pragma unroll
+  for (int r = 0; r < Words<MODE>::N; ++r) {
+    x.w[r] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (MODE == KVQ_NVFP4) x.s[r] = 0u;
+  }
+}
+// Values of tokens >= valid of the page must not reach a product: E4M3 codes
+// and block scales can be NaN there.
+template <int MODE>
+__device__ __forceinline__ void drop_tokens(Words<MODE>& x, int lane, int valid) {
+  const int a = lane & 7;
+#pragma unroll
+  for (int r = 0; r < Words<MODE>::N; ++r) {
+    if constexpr (!Words<MODE>::FOUR) {
+      if (a + 8 * (r & 1) >= valid) x.w[r] = make_uint4(0u, 0u, 0u, 0u);
+    } else if constexpr (MODE == KVQ_NVFP4) {
+      if (2 * a >= valid) x.s[r] &= 0xFF00u;
+      if (2 * a + 1 >= valid) x.s[r] &= 0x00FFu;
+    }
+  }
+}
+
+// One-byte codes: four words -> two 16-byte chunks of fp16.
+template <int MODE>
+__device__ __forceinline__ void codes16(const uint4& w, uint4* out) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (MODE == KVQ_INT8_PER_TOKEN_HEAD) {
+      const __half2 bias = u32_as_h2(0x64806480u);  // 1024 + (x + 128) - 1152
+      const uint32_t v = in[i] ^ 0x80808080u;
+      h[2 * i] = h2_as_u32(__hsub2(u32_as_h2(prmt(v, 0x64646464u, 0x4140u)), bias));
+      h[2 * i + 1] = h2_as_u32(__hsub2(u32_as_h2(prmt(v, 0x64646464u, 0x4342u)), bias));
+    } else {
+      h[2 * i] = e4m3x2_to_f16x2(in[i] & 0xFFFFu);
+      h[2 * i + 1] = e4m3x2_to_f16x2(in[i] >> 16);
+    }
+  }
+  out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  out[1] = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// Write page `w` (tokens 16 w ..) of a tile into the operand at `op`: channel
+// group c of token t at (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring
+// lanes always fill one core matrix row set, so the stores have no conflicts.
+template <int MODE, int SIDE>
+__device__ __forceinline__ void store_page(const Words<MODE>& x, uint8_t* op, int w, int lane) {
+  const int a = lane & 7, b = lane >> 3;
+  uint8_t* base = op + 2 * w * kSbo;
+#pragma unroll
+  for (int r = 0; r < Words<MODE>::N; ++r) {
+    if constexpr (!Words<MODE>::FOUR) {
+      uint4 c[2];
+      codes16<MODE>(x.w[r], c);
+      uint8_t* p = base + (r & 1) * kSbo + a * 16 + 2 * (b + 4 * (r >> 1)) * kLbo;
+      *reinterpret_cast<uint4*>(p) = c[0];
+      *reinterpret_cast<uint4*>(p + kLbo) = c[1];
+    } else if constexpr (SIDE == 0) {
+      const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
+      uint8_t* p = base + r * kSbo + a * 16 + 4 * b * kLbo;
+      __half2 s2[2];
+      if constexpr (MODE == KVQ_NVFP4) {
+        const __half2 s = u32_as_h2(e4m3x2_to_f16x2(x.s[r]));
+        s2[0] = __low2half2(s);
+        s2[1] = __high2half2(s);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];
+        if constexpr (MODE == KVQ_NVFP4) {
+          e2m1x8_to_f16x2x4(in[i], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = h2_as_u32(__hmul2(u32_as_h2(h[e]), s2[i >> 1]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = s4_pair(in[i] >> (4 * e));
+        }
+        *reinterpret_cast<uint4*>(p + i * kLbo) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    } else {
+      const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
+      uint32_t even[8], odd[8];  // the pair's two tokens, 16 channels
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];  // (even token, odd token) of channels 4 i ..
+        if constexpr (MODE == KVQ_NVFP4) {
+          e2m1x8_to_f16x2x4(in[i], h);
+          const __half2 s = u32_as_h2(e4m3x2_to_f16x2(x.s[r]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = h2_as_u32(__hmul2(u32_as_h2(h[e]), s));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = s4_pair(in[i] >> (4 * e));
+        }
+        even[2 * i] = prmt(h[0], h[1], 0x5410u);
+        even[2 * i + 1] = prmt(h[2], h[3], 0x5410u);
+        odd[2 * i] = prmt(h[0], h[1], 0x7632u);
+        odd[2 * i + 1] = prmt(h[2], h[3], 0x7632u);
+      }
+      // tokens 2a and 2a + 1; lanes 4..7 of each eight store the odd one first,
+      // so that the eight rows stored together differ modulo 8
+      const bool flip = a & 4;
+      uint8_t* p = base + (a >> 2) * kSbo + 2 * (b + 4 * r) * kLbo + ((2 * a) & 7) * 16;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool o = flip != (u == 1);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(p + (o ? 16 : 0) + c * kLbo) =
+              make_uint4(o ? odd[4 * c] : even[4 * c], o ? odd[4 * c + 1] : even[4 * c + 1],
+                         o ? odd[4 * c + 2] : even[4 * c + 2], o ? odd[4 * c + 3] : even[4 * c + 3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+struct Bars {
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full;
+};
+
+template <int MODE, int STREAMS, bool OPT>
+__global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_constant__ ChunkArgs a) {
+  using L = Smem<STREAMS>;
+  constexpr bool PT = kPerTokenScale<MODE>;
+  constexpr int ROWS = STREAMS == 1 ? 256 : 128;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ Bars bar;
+  __shared__ uint32_t tmem_s;
+  __shared__ RowTile tile_s;
+  float* ksm = reinterpret_cast<float*>(sm + L::KS);
+  float* vsm = reinterpret_cast<float*>(sm + L::VS);
+  float* ones = reinterpret_cast<float*>(sm + L::ONES);
+  int* page_s = reinterpret_cast<int*>(sm + L::PAGE);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kvh = blockIdx.x % a.Hkv, tile_index = blockIdx.x / a.Hkv, split = blockIdx.y;
+  uint8_t* pool = const_cast<uint8_t*>(a.pool);
+  if (warp == 0) {
+    const RowTile t = find_tile(a, tile_index, ROWS, tile_index == 0 && kvh == 0 && split == 0);
+    if (lane == 0) tile_s = t;
+  }
+  __syncthreads();
+  const RowTile t = tile_s;
+  if (t.seq < 0) return;
+  const TokenRange tr = token_range(a, t, kTok);
+  const int i0 = (int)((long long)tr.tiles * split / a.num_splits);
+  const int n = (int)((long long)tr.tiles * (split + 1) / a.num_splits) - i0;  // this CTA's tiles
+  const int items = STREAMS == 1 ? 2 * n : n;  // (tile, block) pairs; item k belongs to block k & 1
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], 4);
+      mbar_init(&bar.v_full[i], 4);
+      mbar_init(&bar.k_free[i], 1);
+      mbar_init(&bar.v_free[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+    }
+    mbar_init(&bar.o_full, 1);
+    mbar_fence_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
+  }
+  // Q: row r's channel group c at (r % 8) 16 + c kLbo + (r / 8) kSbo; zero past the tile's rows
+  for (int it = tid; it < ROWS * 16; it += kThreads) {
+    const int r = it >> 4, c = it & 15;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r < t.count) {
+      const int rr = t.r0 + r;
+      const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + row * kD) + c);
+    }
+    *reinterpret_cast<uint4*>(sm + L::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * kSbo) = x;
+  }
+  if (tid < kTok) ones[tid] = 1.0f;
+  fence_proxy_async_smem();  // Q is read by the tensor core
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = tmem_s;
+  bool ok = true;
+
+  float kfac = a.scale * kLog2e, vfac = 1.0f;  // score factor in log2 units, output factor
+  if constexpr (!PT) {
+    kfac *= *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
+    vfac = *reinterpret_cast<const float*>(a.pool + kHdrVScaleOffset);
+  }
+
+  // row state of the softmax threads
+  const int blk = warp >> 2;  // S_0 or S_1 (warps 0-7)
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  const int row = STREAMS == 1 ? tid : (tid & 127);
+  float R = -1e30f;
+  float2 l2 = make_float2(0.0f, 0.0f);
+  bool any = false;  // this block has accumulated something
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ dequantization
+    Words<MODE> kw[kPages], vw[kPages];
+    float sc[kPages];
+    int pid[kPages], ahead[kPages];  // page ids of tile i, and (unchecked) of tile i + 1
+    auto page = [&](int i, int u) { return tr.tile(i0 + i) * 8 + (warp - 8) + 4 * u; };
+    auto page_id = [&](int i, int u) -> int {
+      return i < n && page(i, u) * 16 < t.n
+                 ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page(i, u)) : -1;
+    };
+    auto checked = [&](int id, int i, int u) -> int {
+      if (i < n && page(i, u) * 16 < t.n && (id < 0 || id >= a.num_pages)) {
+        if (lane == 0) set_error(pool, KVQ_DEVERR_PAGE_RANGE);
+        return -1;
+      }
+      return id;
+    };
+    auto block = [&](int id) { return a.pool + kHeaderBytes + ((size_t)id * a.Hkv + kvh) * a.block_bytes; };
+    auto load_k = [&]() {
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        sc[u] = 0.0f;
+        if (pid[u] >= 0) {
+          load_words<MODE, 0>(block(pid[u]), lane, kw[u]);
+          if constexpr (PT)
+            sc[u] = __ldg(reinterpret_cast<const float*>(block(pid[u]) + (Words<MODE>::FOUR ? 16 * kD : 32 * kD)) + lane);
+        } else {
+          zero_words<MODE>(kw[u]);
+        }
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        if (pid[u] >= 0) load_words<MODE, 1>(block(pid[u]), lane, vw[u]);
+        else zero_words<MODE>(vw[u]);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kPages; ++u) {
+      pid[u] = checked(page_id(0, u), 0, u);
+      ahead[u] = page_id(1, u);
+    }
+    load_k();
+    load_v();
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1, slot = i & (kSlots - 1);
+      if (i >= 2) ok = mbar_wait_bounded(&bar.k_free[st], ((i >> 1) - 1) & 1) && ok;
+      if (!ok) break;
+      // Scales of the pages: keys in lanes 0-15, values in 16-31.  The slot's last
+      // readers are done: the wait for v_free of tile i - 3 lies behind.
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        const int w = (warp - 8) + 4 * u;  // page of the tile
+        const int valid = pid[u] >= 0 ? min(16, t.n - page(i, u) * 16) : 0;
+        if constexpr (PT) {
+          const float s = (lane & 15) < valid ? sc[u] : 0.0f;
+          (lane < 16 ? ksm : vsm)[slot * kTok + 16 * w + (lane & 15)] = lane < 16 ? s * kfac : s;
+          const uint32_t top = __reduce_max_sync(kFull, lane >= 16 ? __float_as_uint(fabsf(s)) : 0u);
+          if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : top ? exponent(__uint_as_float(top)) : -100;
+        } else {
+          if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : 0;
+        }
+        store_page<MODE, 0>(kw[u], sm + L::K + st * kOpBytes, w, lane);
+        if (valid < 16) drop_tokens<MODE>(vw[u], lane, valid);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.k_full[st]);
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) {
+        pid[u] = checked(ahead[u], i + 1, u);
+        ahead[u] = page_id(i + 2, u);
+      }
+      load_k();  // of tile i + 1
+      if (i >= 2) ok = mbar_wait_bounded(&bar.v_free[st], ((i >> 1) - 1) & 1) && ok;
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) store_page<MODE, 1>(vw[u], sm + L::V + st * kOpBytes, (warp - 8) + 4 * u, lane);
+      load_v();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.v_full[st]);
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ products
+    const uint64_t dq = umma_sdesc(smem_u32(sm + L::Q), kLbo, kSbo);
+    const uint64_t dk = umma_sdesc(smem_u32(sm + L::K), kLbo, kSbo);
+    const uint64_t dv = umma_sdesc(smem_u32(sm + L::V), kSbo, kLbo);  // MN-major: tokens along K, channels along N
+    constexpr uint64_t kStepK = (2 * kLbo) >> 4, kStepV = (2 * kSbo) >> 4, kOp = kOpBytes >> 4;
+    auto qk = [&](int k) {  // S of item k
+      const int i = STREAMS == 1 ? k >> 1 : k, b = k & 1, st = i & 1;
+      ok = mbar_wait_bounded(&bar.k_full[st], (i >> 1) & 1) && ok;
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t A = dq + (STREAMS == 1 ? b * kOp : 0), B = dk + st * kOp;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) umma_f16_ss(tb + 128 * b, A + j * kStepK, B + j * kStepK, kIdescQK, j > 0 ? 1u : 0u);
+        tc_commit(&bar.s_full[b]);
+        if (STREAMS == 2 || b == 1) tc_commit(&bar.k_free[st]);
+      }
+      __syncwarp();
+    };
+    for (int k = 0; k < min(2, items); ++k) qk(k);
+    for (int k = 0; k < items && ok; ++k) {
+      const int i = STREAMS == 1 ? k >> 1 : k, b = k & 1, st = i & 1;
+      ok = mbar_wait_bounded(&bar.v_full[st], (i >> 1) & 1) && ok;
+      ok = mbar_wait_bounded(&bar.p_full[b], (k >> 1) & 1) && ok;
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t B = dv + st * kOp;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          umma_f16_ts(tb + 256 + 128 * b, tb + 128 * b + 8 * j, B + j * kStepV, kIdescPV, (k >= 2 || j > 0) ? 1u : 0u);
+        if (STREAMS == 2 || b == 1) tc_commit(&bar.v_free[st]);
+        if (k + 1 == items) tc_commit(&bar.o_full);
+      }
+      __syncwarp();
+      if (k + 2 < items) qk(k + 2);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const bool real = row < t.count;
+    const int rr = t.r0 + (real ? row : 0);
+    const int pos = t.n - t.m + rr / a.G;
+    // the block's own positions decide which tiles need a mask
+    TokenRange mine = tr;
+    if (STREAMS == 1) {
+      mine.p_min = t.n - t.m + (t.r0 + 128 * blk) / a.G;
+      mine.p_max = t.n - t.m + (t.r0 + min(t.count - 1, 128 * blk + 127)) / a.G;
+    }
+    const RowSees sees = row_sees(a, tr, pos, real);
+    float slope = 0.0f;
+    if constexpr (OPT) slope = a.slopes ? __ldg(a.slopes + kvh * a.G + rr % a.G) * kLog2e : 0.0f;
+    const float cap2 = OPT ? a.cap * kLog2e : 0.0f;                        // the cap in log2 units
+    const float rcap = OPT && a.cap > 0.0f ? 2.0f * kLog2e / cap2 : 0.0f;  // log2 of e^(2 x / cap) per log2 unit of x
+    const uint32_t tS = tb + 128 * blk + lanes, tO = tb + 256 + 128 * blk + lanes;
+
+    for (int k = blk; k < items; k += 2) {
+      const int i = STREAMS == 1 ? k >> 1 : k, st = i & 1, slot = i & (kSlots - 1);
+      const int t0 = tr.tile(i0 + i) * kTok;
+      ok = mbar_wait_bounded(&bar.k_full[st], (i >> 1) & 1) && ok;  // the scales (already complete: S needed them)
+      ok = mbar_wait_bounded(&bar.s_full[blk], (k >> 1) & 1) && ok;
+      if (!__all_sync(kFull, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float* ks = ksm + slot * kTok;
+      const float* vs = vsm + slot * kTok;
+      const int4 pg0 = *reinterpret_cast<const int4*>(page_s + slot * 8), pg1 = *reinterpret_cast<const int4*>(page_s + slot * 8 + 4);
+      const int pmin = min(min(min(pg0.x, pg0.y), min(pg0.z, pg0.w)), min(min(pg1.x, pg1.y), min(pg1.z, pg1.w)));
+      const int pmax = max(max(max(pg0.x, pg0.y), max(pg0.z, pg0.w)), max(max(pg1.x, pg1.y), max(pg1.z, pg1.w)));
+      const float ve = PT ? (float)max(pmax, -100) : 0.0f;
+      const bool masked = pmin == kMissing || !all_see(a, mine, t0, kTok);
+      const bool slow = OPT || masked;  // scores are finished in the first pass and put back
+
+      // first pass: the row's maximum (log2 units)
+      float mx = -INFINITY;
+      uint32_t x[2][32];
+      tm_ld(tS, x[0]);
+      if (!slow) {
+        float2 m2 = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tm_wait(x[c & 1]);
+          if (c < 3) tm_ld(tS + 32 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float2 y0 = pair(x[c & 1], e), y1 = pair(x[c & 1], e + 1);
+            if constexpr (PT) {
+              const float4 f = *reinterpret_cast<const float4*>(ks + 32 * c + 2 * e);
+              y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
+              y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
+            }
+            m2.x = fmaxf(m2.x, fmaxf(y0.x, y1.x));
+            m2.y = fmaxf(m2.y, fmaxf(y0.y, y1.y));
+          }
+        }
+        mx = fmaxf(m2.x, m2.y);
+        if constexpr (!PT) mx *= kfac;
+      } else {
+        const int there[8] = {pg0.x, pg0.y, pg0.z, pg0.w, pg1.x, pg1.y, pg1.z, pg1.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t* v = x[0];
+          tm_wait(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int tok = t0 + 32 * c + e;
+            float y = __uint_as_float(v[e]) * (PT ? ks[32 * c + e] : kfac);
+            if constexpr (OPT) {
+              // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+              if (a.cap > 0.0f) y = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(y * rcap));
+              y = fmaf(-slope, fabsf((float)(pos - tok)), y);
+            }
+            if (masked && (there[2 * c + (e >> 4)] == kMissing || !sees(tok))) y = -INFINITY;
+            v[e] = __float_as_uint(y);
+            mx = fmaxf(mx, y);
+          }
+          tmem_st<32>(tS + 32 * c, v);
+          if (c < 3) tm_ld(tS + 32 * (c + 1), v);
+        }
+        tmem_wait_st();
+      }
+
+      // the reference: moved when this tile passes it by more than the slack
+      const float cand = mx + ve;
+      if (__any_sync(kFull, cand > R + kSlack)) {
+        const float to = fmaxf(R, cand), al = ex2(R - to);
+        R = to;
+        l2 = __fmul2_rn(l2, make_float2(al, al));
+        if (any) {  // every product issued before this S has completed
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* v = x[0];
+            tm_ld(tO + 32 * c, v);
+            tm_wait(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+            tmem_st<32>(tO + 32 * c, v);
+          }
+          tmem_wait_st();
+        }
+      }
+      any = true;
+
+      // second pass: weights, their sum, and P in fp16 over the first half of S
+      const float* kp = slow ? ones : ks;
+      const float2 nR = make_float2(-R, -R);
+      const float kf = slow ? 1.0f : kfac;
+      tm_ld(tS, x[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tm_wait(x[c & 1]);
+        if (c < 3) tm_ld(tS + 32 * (c + 1), x[(c + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          float2 f0 = make_float2(kf, kf), f1 = f0;
+          if constexpr (PT) {
+            const float4 f = *reinterpret_cast<const float4*>(kp + 32 * c + 2 * e);
+            f0 = make_float2(f.x, f.y);
+            f1 = make_float2(f.z, f.w);
+          }
+          const float2 y0 = __ffma2_rn(pair(x[c & 1], e), f0, nR), y1 = __ffma2_rn(pair(x[c & 1], e + 1), f1, nR);
+          float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+          l2 = __fadd2_rn(l2, __fadd2_rn(p0, p1));
+          if constexpr (PT) {
+            const float4 f = *reinterpret_cast<const float4*>(vs + 32 * c + 2 * e);
+            if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
+              p0.x = y0.x == -INFINITY ? 0.0f : p0.x * f.x;
+              p0.y = y0.y == -INFINITY ? 0.0f : p0.y * f.y;
+              p1.x = y1.x == -INFINITY ? 0.0f : p1.x * f.z;
+              p1.y = y1.y == -INFINITY ? 0.0f : p1.y * f.w;
+            } else {
+              p0 = __fmul2_rn(p0, make_float2(f.x, f.y));
+              p1 = __fmul2_rn(p1, make_float2(f.z, f.w));
+            }
+          }
+          p[e] = h2_as_u32(__floats2half2_rn(p0.x, p0.y));
+          p[e + 1] = h2_as_u32(__floats2half2_rn(p1.x, p1.y));
+        }
+        tmem_st<16>(tS + 16 * c, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[blk]);
+    }
+  }
+
+  // ------------------------------------------------------------ outputs
+  if (items > 0) ok = mbar_wait_bounded(&bar.o_full, 0) && ok;
+  tc_fence_after();
+  const bool failed = __syncthreads_or(!ok);
+  if (failed) {
+    if (tid == 0) set_error(pool, KVQ_DEVERR_TIMEOUT);
+  } else {
+    float l = l2.x + l2.y;
+    float f0 = 1.0f, f1 = 0.0f;                          // two streams: factors of their accumulators
+    float* other = reinterpret_cast<float*>(sm + L::K);  // the second stream's rows: [128][132], then R and l
+    constexpr int kStride = 132;
+    if constexpr (STREAMS == 2) {
+      if (warp >= 4 && warp < 8) {
+        float* o = other + row * kStride;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          if (any) {
+            tm_ld(tb + 384 + lanes + 32 * c, v);
+            tm_wait(v);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(o + 32 * c + e) = any ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3])
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+        }
+        other[128 * kStride + row] = R;
+        other[128 * kStride + 128 + row] = l;
+      }
+      __syncthreads();
+      if (warp < 4) {
+        const float R1 = other[128 * kStride + row], l1 = other[128 * kStride + 128 + row];
+        const float top = fmaxf(R, R1);
+        f0 = exp2f(R - top);
+        f1 = exp2f(R1 - top);
+        l = l * f0 + l1 * f1;
+        R = top;
+      }
+    }
+    const int last = STREAMS == 1 ? 8 : 4;
+    if (warp < last && row < ((t.count + 31) & ~31)) {  // whole warps
+      const bool real = row < t.count;
+      const int rr = t.r0 + (real ? row : 0);
+      const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+      const float g = a.num_splits > 1 ? vfac : l > 0.0f ? vfac / l : 0.0f;
+      const long long pi = qrow * a.num_splits + split;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        if (any) {
+          tm_ld(tb + 256 + 128 * blk + lanes + 32 * c, v);
+          tm_wait(v);
+        }
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(v[e]) * f0 : 0.0f;
+        if constexpr (STREAMS == 2) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(other + row * kStride + 32 * c + e);
+            o[e] += u.x * f1;
+            o[e + 1] += u.y * f1;
+            o[e + 2] += u.z * f1;
+            o[e + 3] += u.w * f1;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = l > 0.0f ? o[e] * g : 0.0f;
+        if (!real) continue;
+        if (a.num_splits == 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const uint4 h = make_uint4(h2_as_u32(__floats2half2_rn(o[e], o[e + 1])), h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3])),
+                                       h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5])), h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7])));
+            st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD + 32 * c + e), h, a.out_span, a.pool);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            st_chk(reinterpret_cast<float4*>(a.ws_o + pi * kD + 32 * c + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]),
+                   a.ws_span, a.pool);
+        }
+      }
+      if (real && a.num_splits > 1)
+        st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l > 0.0f ? R : -INFINITY, l), a.ws_span, a.pool);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tb, 512);
+}
+
+template <int MODE, int STREAMS, bool OPT>
+cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
+  auto kern = chunk_umma_kernel<MODE, STREAMS, OPT>;
+  constexpr size_t smem = Smem<STREAMS>::dynamic();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long tiles = chunk_tile_bound(a.total_q, a.B, a.G, umma_chunk_rows(STREAMS));
+  kern<<<dim3((unsigned)(tiles * a.Hkv), a.num_splits), kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int STREAMS, bool OPT>
+cudaError_t launch_mode(int mode, const ChunkArgs& a, cudaStream_t s) {
+  switch (mode) {
+    case KVQ_FP8_PER_TENSOR: return launch<KVQ_FP8_PER_TENSOR, STREAMS, OPT>(a, s);
+    case KVQ_INT8_PER_TOKEN_HEAD: return launch<KVQ_INT8_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
+    case KVQ_FP8_PER_TOKEN_HEAD: return launch<KVQ_FP8_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
+    case KVQ_NVFP4:
+    case KVQ_NVFP4_4OVER6: return launch<KVQ_NVFP4, STREAMS, OPT>(a, s);
+    case KVQ_INT4_PER_TOKEN_HEAD: return launch<KVQ_INT4_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, int streams, cudaStream_t s) {
+  const bool opt = a.cap > 0.0f || a.slopes != nullptr;
+  const int mode = c->cfg.mode;
+  if (streams == 1) return opt ? launch_mode<1, true>(mode, a, s) : launch_mode<1, false>(mode, a, s);
+  return opt ? launch_mode<2, true>(mode, a, s) : launch_mode<2, false>(mode, a, s);
+}
+
+}  // namespace kvq

@@ -53,7 +53,6 @@ cudaError_t launch_norm_rope_write(const kvq_cache* c, const kvq_norm_rope& r, c
 
 // Chunk attention (kvq_chunk.cu).
 struct ChunkPlan {
-  int rows = 0;        // (query, head) rows of a CTA
   int num_splits = 1;  // parts of a row tile's token range
   size_t workspace_bytes = 0;
 };

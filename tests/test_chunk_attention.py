@@ -360,3 +360,12 @@ def test_one_query_agrees_with_decode():
                            workspace=torch.empty(max(wsb, 16), dtype=torch.uint8, device="cuda"))
     assert (got - ref).abs().max().item() < 1e-4
     assert ctypes.sizeof(K.AttentionOptions) == 24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ROWS)
+@pytest.mark.parametrize("qlens,lens,heads", [([700], [700], (1, 4)), ([300, 64, 90], [1500, 64, 91], (2, 2)),
+                                              ([16, 3, 16], [1200, 900, 16], (1, 8))])
+def test_longer_chunks(mode, qlens, lens, heads):
+    check(mode, "f16", "f16", heads[0], heads[1], 128, qlens, lens)
+    check(mode, "f16", "f16", heads[0], heads[1], 128, qlens, lens, cap=3.0, alibi=True, window=200)
