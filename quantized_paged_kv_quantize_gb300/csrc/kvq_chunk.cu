@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   Packed8 pk[U], pv[U];
   float psc = 0.0f;  // per-token scale of token tid % KT, keys for tid < KT, values above
   auto page_of = [&](int tok) -> int {  // the token's page, -1 past the sequence or out of the pool
-    if (tok >= t.n) return -1;
+    if (tok >= t.n || tr.unseen(tok >> 4)) return -1;
     const int pid = __ldg(a.block_table + (long long)t.seq * a.max_pages + (tok >> 4));
     if (pid < 0 || pid >= a.num_pages) {
       set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
       }
     }
   };
-  // missing pages inside the sequence are not seen
+  // missing pages inside the sequence are not seen either
   auto present = [&](int tok) { return tok < t.n && page_of(tok) >= 0; };
 
   float o[D / 8][4];
@@ -420,6 +420,15 @@ ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_he
                      int window, bool has_prefix) {
   ChunkPlan p;
   const int D = c->cfg.head_dim, G = num_q_heads / c->cfg.num_kv_heads;
+  if (max_q_len <= 1 && num_seqs <= 65535) {  // single tokens: the decode kernels (one grid row per sequence)
+    int len = max_seq_len;
+    if (window > 0 && !has_prefix) len = (int)std::min<long long>(len, (long long)window + 15);
+    p.single = true;
+    p.decode = plan_decode(c, num_seqs, num_q_heads, len);
+    p.num_splits = p.decode.num_splits;
+    p.workspace_bytes = p.decode.workspace_bytes;
+    return p;
+  }
   const bool umma = chunk_on_umma(c, KVQ_F16);
   const int streams = umma_streams(max_q_len, G);
   const int rows = umma ? umma_chunk_rows(streams) : kRows;
@@ -446,6 +455,9 @@ ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_he
 }
 
 cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkCall& k, cudaStream_t stream) {
+  if (plan.single)
+    return launch_decode(c, plan.decode, k.q, k.block_table, k.max_pages, k.seq_lens, k.num_seqs, k.num_q_heads,
+                         k.max_seq_len, k.scale, k.out, k.out_dtype, k.workspace, stream, nullptr, 1, &k);
   ChunkArgs a;
   a.pool = c->base;
   a.q = k.q;

@@ -8,8 +8,6 @@
 
 namespace kvq {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 struct ChunkArgs {
   const uint8_t* pool;
   const void* q;                // [total_q][Hq][D]
@@ -103,9 +101,13 @@ __device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int 
 // of tile numbers: the prefix's, then the causal (and windowed) ones.
 struct TokenRange {
   int p_min, p_max;   // positions of the CTA's first and last query
+  int lowest;         // first token of the window of the CTA's first query (0 without a window)
   int prefix;         // tokens below it are seen by every row (at a position >= 0)
   int first, second;  // tiles of the first run (from 0); first tile of the second run
   int tiles;          // in all
+  // a page of the tiles that lies wholly between the prefix and the windows: not seen by any row, and not read
+  // (it may have been given up)
+  __device__ __forceinline__ bool unseen(int page) const { return page * 16 + 16 <= lowest && page * 16 >= prefix; }
   __device__ __forceinline__ int tile(int i) const { return i < first ? i : second + (i - first); }
 };
 __device__ __forceinline__ TokenRange token_range(const ChunkArgs& a, const RowTile& t, int kt) {
@@ -113,12 +115,13 @@ __device__ __forceinline__ TokenRange token_range(const ChunkArgs& a, const RowT
   r.p_min = t.n - t.m + t.r0 / a.G;
   r.p_max = t.n - t.m + (t.r0 + t.count - 1) / a.G;
   r.prefix = a.prefix_lens ? max(0, min(__ldg(a.prefix_lens + t.seq), t.n)) : 0;
+  r.lowest = a.window > 0 ? max(0, max(r.p_min, 0) - a.window + 1) : 0;
   if (r.p_max < 0) {  // more queries than tokens: these see nothing
     r.first = r.second = r.tiles = 0;
     return r;
   }
   const int hi = (r.p_max + kt) / kt;  // tiles up to the last query's own token
-  const int lo = a.window > 0 ? max(0, max(r.p_min, 0) - a.window + 1) / kt : 0;
+  const int lo = r.lowest / kt;
   r.first = min((r.prefix + kt - 1) / kt, lo);
   r.second = lo;
   r.tiles = r.first + max(hi, (r.prefix + kt - 1) / kt) - lo;

@@ -341,12 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
     float sc[kPages];
     int pid[kPages], ahead[kPages];  // page ids of tile i, and (unchecked) of tile i + 1
     auto page = [&](int i, int u) { return tr.tile(i0 + i) * 8 + (warp - 8) + 4 * u; };
+    auto wanted = [&](int i, int u) { return i < n && page(i, u) * 16 < t.n && !tr.unseen(page(i, u)); };
     auto page_id = [&](int i, int u) -> int {
-      return i < n && page(i, u) * 16 < t.n
+      return wanted(i, u)
                  ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page(i, u)) : -1;
     };
     auto checked = [&](int id, int i, int u) -> int {
-      if (i < n && page(i, u) * 16 < t.n && (id < 0 || id >= a.num_pages)) {
+      if (wanted(i, u) && (id < 0 || id >= a.num_pages)) {
         if (lane == 0) set_error(pool, KVQ_DEVERR_PAGE_RANGE);
         return -1;
       }
@@ -526,17 +527,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           tm_wait(v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const int tok = t0 + 32 * c + e;
-            float y = __uint_as_float(v[e]) * (PT ? ks[32 * c + e] : kfac);
-            if constexpr (OPT) {
-              // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-              if (a.cap > 0.0f) y = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(y * rcap));
-              y = fmaf(-slope, fabsf((float)(pos - tok)), y);
-            }
-            if (masked && (there[2 * c + (e >> 4)] == kMissing || !sees(tok))) y = -INFINITY;
-            v[e] = __float_as_uint(y);
-            mx = fmaxf(mx, y);
+            v[e] = __float_as_uint(__uint_as_float(v[e]) * (PT ? ks[32 * c + e] : kfac));
           }
+          if constexpr (OPT) {
+            if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(v[e]) * rcap)));
+            }
+            if (a.slopes) {
+              const float d = (float)(pos - t0 - 32 * c);  // distances are whole numbers below 2^24: exact
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(-slope, fabsf(d - (float)e), __uint_as_float(v[e])));
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (there[2 * c + (e >> 4)] == kMissing || !sees(t0 + 32 * c + e)) v[e] = 0xff800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
           tmem_st<32>(tS + 32 * c, v);
           if (c < 3) tm_ld(tS + 32 * (c + 1), v);
         }

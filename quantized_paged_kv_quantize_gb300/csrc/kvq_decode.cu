@@ -59,8 +59,6 @@ constexpr int kWarps = 4;
 // A warp's page ids for one split live in shared memory (at most this many
 // pages per warp, so at most kWarps * kIdsPerWarp pages per split).
 constexpr int kIdsPerWarp = 256;
-constexpr float kLog2e = 1.4426950408889634f;
-
 template <int MODE, int D>
 struct Cfg {
   // 4-bit payloads (NVFP4 -- also the storage of NVFP4 4over6 -- and INT4):
@@ -167,11 +165,11 @@ __device__ __forceinline__ void cvt_pair4_biased(uint32_t w, uint32_t& lo, uint3
 // Q as the B operand of S^T = K Q^T: b0 = Q[g][d(j,2tq..2tq+1)], b1 = Q[g][d(j,2tq+8..+9)]
 // with d(j, .) = tq*D/4 + 4j + {0,1} and {2,3}.  Heads >= G are zero.
 template <int D, bool QF32>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int g, int tq, uint32_t (*qh)[2],
+__device__ __forceinline__ void load_q(const DecodeArgs& a, long long b, int kvh, int g, int tq, uint32_t (*qh)[2],
                                        uint32_t (*ql)[2]) {
   constexpr int KSTEPS = D / 16;
   const bool ok = g < a.G;
-  const long long row = ((long long)b * a.Hq + (long long)kvh * a.G + (ok ? g : 0)) * D + tq * (D / 4);
+  const long long row = (b * a.Hq + (long long)kvh * a.G + (ok ? g : 0)) * D + tq * (D / 4);
 #pragma unroll
   for (int j = 0; j < KSTEPS; ++j) {
     float x[4];
@@ -455,7 +453,7 @@ constexpr size_t decode_smem() {
 // a row without tokens).  The second barrier keeps every CTA's shared memory
 // alive until its peers have read it.
 template <int D>
-__device__ void merge_in_cluster(const DecodeArgs& a, int b, int kvh, const float* part) {
+__device__ void merge_in_cluster(const DecodeArgs& a, long long b, int kvh, const float* part) {
   cluster_barrier();
   const int r = cluster_rank(), ns = cluster_size();
   const float* pm = part;
@@ -481,12 +479,15 @@ __device__ void merge_in_cluster(const DecodeArgs& a, int b, int kvh, const floa
         }
       }
     }
-    store_out(a, ((long long)b * a.Hq + (long long)kvh * a.G + h) * D + d, L > 0.0f ? O / L : 0.0f);
+    store_out(a, (b * a.Hq + (long long)kvh * a.G + h) * D + d, L > 0.0f ? O / L : 0.0f);
   }
   cluster_barrier();
 }
 
-template <int MODE, int D, bool QF32>
+// OPT: single tokens of a chunk attention batch -- the query row comes from
+// cu_q, scores may be capped and biased by distance, and tokens below a window
+// (and past a prefix) are not seen.
+template <int MODE, int D, bool QF32, bool OPT = false>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel(const __grid_constant__ DecodeArgs a,
                                                                const __grid_constant__ CUtensorMap tmap) {
   using C = Cfg<MODE, D>;
@@ -506,25 +507,35 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   const int seq = b / a.nq;
   pdl_launch_dependents();
 
-  int n = a.seq_lens[seq];
-  const int lim = min(a.max_seq_len, a.max_pages * kPage);
-  if (n > lim || n < 0) {
-    if (threadIdx.x == 0 && split == 0 && kvh == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
-    n = n < 0 ? 0 : lim;
+  int n;
+  long long row = b;  // of q and out
+  SingleQuery sq{0, 0, 0, 0, 0};
+  if constexpr (OPT) {
+    sq = single_query(a, seq, threadIdx.x == 0 && split == 0 && kvh == 0);
+    if (sq.row < 0) return;  // no query: all CTAs of the row's cluster leave alike
+    row = sq.row;
+    n = sq.n;
+  } else {
+    n = a.seq_lens[seq];
+    const int lim = min(a.max_seq_len, a.max_pages * kPage);
+    if (n > lim || n < 0) {
+      if (threadIdx.x == 0 && split == 0 && kvh == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
+      n = n < 0 ? 0 : lim;
+    }
+    n = max(n - (a.nq - 1 - b % a.nq), 0);  // causal: the tokens up to the query's own position
   }
-  n = max(n - (a.nq - 1 - b % a.nq), 0);  // causal: the tokens up to the query's own position
-  const int t_begin = split * a.tokens_per_split;
+  const int t_begin = (OPT ? sq.base : 0) + split * a.tokens_per_split;
   const int t_end = min(n, t_begin + a.tokens_per_split);
   float* cpart = reinterpret_cast<float*>(smem + warp_merge_bytes<D>());  // merge across the cluster
   if (t_begin >= t_end) {
     if (a.num_splits == 1) {  // empty sequence: zero output rows
       for (int i = threadIdx.x; i < a.G * D; i += blockDim.x) {
-        const long long o = ((long long)b * a.Hq + (long long)kvh * a.G + i / D) * D + i % D;
+        const long long o = (row * a.Hq + (long long)kvh * a.G + i / D) * D + i % D;
         store_out(a, o, 0.0f);
       }
     } else if (a.cluster) {  // an empty split still takes part in its cluster's merge
       for (int i = threadIdx.x; i < 8 * (D + 2); i += blockDim.x) cpart[i] = i < 8 ? -INFINITY : 0.0f;
-      merge_in_cluster<D>(a, b, kvh, cpart);
+      merge_in_cluster<D>(a, row, kvh, cpart);
     }
     return;
   }
@@ -543,6 +554,13 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   // the warp's page ids (an out-of-range id is flagged and its page skipped)
   int* ids = page_ids + warp * kIdsPerWarp;
   for (int k = lane; k < my_count; k += 32) {
+    if constexpr (OPT) {  // a page between the prefix and the window: nothing of it is seen or read
+      const int t0 = (p0 + warp + kWarps * k) * kPage;
+      if (t0 + kPage <= sq.lo && t0 >= sq.prefix) {
+        ids[k] = -1;
+        continue;
+      }
+    }
     int pid = __ldg(a.block_table + (long long)seq * a.max_pages + p0 + warp + kWarps * k);
     if (pid < 0 || pid >= a.num_pages) {
       set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   // query fragments: in registers, or one copy in shared memory (C::QSMEM)
   __shared__ uint2 qsm[C::QSMEM ? (QF32 ? 2 : 1) * KSTEPS * 32 : 1];
   uint32_t qh[KSTEPS][2], ql[QF32 ? KSTEPS : 1][2];
-  if (!C::QSMEM || warp == 0) load_q<D, QF32>(a, b, kvh, g, tq, qh, ql);
+  if (!C::QSMEM || warp == 0) load_q<D, QF32>(a, row, kvh, g, tq, qh, ql);
   if constexpr (C::QSMEM) {
     if (warp == 0) {
 #pragma unroll
@@ -600,6 +618,18 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   }
   constexpr bool kPerToken =
       MODE == KVQ_INT8_PER_TOKEN_HEAD || MODE == KVQ_FP8_PER_TOKEN_HEAD || MODE == KVQ_INT4_PER_TOKEN_HEAD;
+
+  float slope0 = 0.0f, slope1 = 0.0f;  // heads 2tq, 2tq + 1 (log2 units)
+  if constexpr (OPT) {
+    if (a.slopes) {
+      if (2 * tq < a.G) slope0 = __ldg(a.slopes + kvh * a.G + 2 * tq) * kLog2e;
+      if (2 * tq + 1 < a.G) slope1 = __ldg(a.slopes + kvh * a.G + 2 * tq + 1) * kLog2e;
+    }
+  }
+  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))), in log2 units
+  auto capped = [&](float s) {
+    return a.cap_log2 - __fdividef(2.0f * a.cap_log2, 1.0f + ex2(s * (2.0f * kLog2e / a.cap_log2)));
+  };
 
   float o[MTILES][4];
 #pragma unroll
@@ -671,6 +701,37 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
                     __fmul2_rn(make_float2(cA[2], cA[3]), make_float2(fA8, fA8))};  // tokens g, g + 8
     float2 sB[2] = {__fmul2_rn(make_float2(cB[0], cB[1]), make_float2(fB0, fB0)),
                     __fmul2_rn(make_float2(cB[2], cB[3]), make_float2(fB8, fB8))};
+    if constexpr (OPT) {
+      if (a.cap_log2 > 0.0f) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sA[r] = make_float2(capped(sA[r].x), capped(sA[r].y));
+          sB[r] = make_float2(capped(sB[r].x), capped(sB[r].y));
+        }
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // distances to the last token
+          const float dA = (float)(n - 1 - (tokA + g + 8 * r)), dB = (float)(n - 1 - (tokB + g + 8 * r));
+          sA[r] = make_float2(fmaf(-slope0, dA, sA[r].x), fmaf(-slope1, dA, sA[r].y));
+          sB[r] = make_float2(fmaf(-slope0, dB, sB[r].x), fmaf(-slope1, dB, sB[r].y));
+        }
+      }
+      if (tokA < sq.lo) {  // (the pair's second page lies behind the first)
+        auto hidden = [&](int tok) { return tok < sq.lo && tok >= sq.prefix; };
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (hidden(tokA + g + 8 * r)) {
+            sA[r] = make_float2(-INFINITY, -INFINITY);
+            (r ? vA8 : vA0) = 0.0f;
+          }
+          if (hidden(tokB + g + 8 * r)) {
+            sB[r] = make_float2(-INFINITY, -INFINITY);
+            (r ? vB8 : vB0) = 0.0f;
+          }
+        }
+      }
+    }
     if (nvA < kPage || nvB < kPage) {  // rare: a partial or missing page
       if (g >= nvA) { sA[0] = make_float2(-INFINITY, -INFINITY); vA0 = 0.f; }
       if (g + 8 >= nvA) { sA[1] = make_float2(-INFINITY, -INFINITY); vA8 = 0.f; }
@@ -788,7 +849,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
     const int hq = kvh * a.G + h;
     if (a.num_splits == 1) {
       const float r = L > 0.0f ? O * vfac / L : 0.0f;
-      const long long oi = ((long long)b * a.Hq + hq) * D + d;
+      const long long oi = (row * a.Hq + hq) * D + d;
       store_out(a, oi, r);
     } else if (a.cluster) {
       cpart[16 + h * D + d] = O * vfac;
@@ -805,22 +866,31 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
       }
     }
   }
-  if (a.cluster) merge_in_cluster<D>(a, b, kvh, cpart);
+  if (a.cluster) merge_in_cluster<D>(a, row, kvh, cpart);
 }
 
 // Merge the splits of each (sequence, query head).
-template <int D>
+template <int D, bool OPT = false>
 __global__ void __launch_bounds__(D) combine_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float wts[D], red[D / 32];
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, d = threadIdx.x;  // b: query row
   pdl_wait_primary();  // the decode grid's partials are complete and visible
-  int n = a.seq_lens[b / a.nq];
-  const int lim = min(a.max_seq_len, a.max_pages * kPage);
-  n = n < 0 ? 0 : (n > lim ? lim : n);
-  n = max(n - (a.nq - 1 - b % a.nq), 0);
+  int n;
+  long long row = b;
+  if constexpr (OPT) {
+    const SingleQuery sq = single_query(a, b, false);
+    if (sq.row < 0) return;
+    row = sq.row;
+    n = sq.n - sq.base;
+  } else {
+    n = a.seq_lens[b / a.nq];
+    const int lim = min(a.max_seq_len, a.max_pages * kPage);
+    n = n < 0 ? 0 : (n > lim ? lim : n);
+    n = max(n - (a.nq - 1 - b % a.nq), 0);
+  }
   const int ns = (n + a.tokens_per_split - 1) / a.tokens_per_split;
   const float r = merge_split_row<D>(a, ((long long)b * a.Hq + hq) * a.num_splits, ns, wts, red);
-  const long long oi = ((long long)b * a.Hq + hq) * D + d;
+  const long long oi = (row * a.Hq + hq) * D + d;
   store_out(a, oi, r);
 }
 
@@ -861,10 +931,10 @@ int resident_ctas_of(const kvq_cache* c) {
   return f32 ? resident_ctas_d<32, true>(c->cfg.mode) : resident_ctas_d<32, false>(c->cfg.mode);
 }
 
-template <int MODE, int D, bool QF32>
+template <int MODE, int D, bool QF32, bool OPT>
 cudaError_t launch_mode(const kvq_cache* c, const DecodeArgs& a, cudaStream_t s) {
   constexpr size_t smem = decode_smem<MODE, D>();
-  auto kern = decode_kernel<MODE, D, QF32>;
+  auto kern = decode_kernel<MODE, D, QF32, OPT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid(a.num_splits, a.Hkv, a.B);
@@ -887,19 +957,19 @@ cudaError_t launch_mode(const kvq_cache* c, const DecodeArgs& a, cudaStream_t s)
   kern<<<grid, kWarps * 32, smem, s>>>(a, c->tmap);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.num_splits == 1) return e;
-  e = launch_dependent(combine_kernel<D>, dim3(a.B * a.Hq), dim3(D), s, a);
+  e = launch_dependent(combine_kernel<D, OPT>, dim3(a.B * a.Hq), dim3(D), s, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D, bool QF32>
+template <int D, bool QF32, bool OPT = false>
 cudaError_t launch_d(const kvq_cache* c, const DecodeArgs& a, cudaStream_t s) {
   switch (c->cfg.mode) {
-    case KVQ_FP8_PER_TENSOR: return launch_mode<KVQ_FP8_PER_TENSOR, D, QF32>(c, a, s);
-    case KVQ_INT8_PER_TOKEN_HEAD: return launch_mode<KVQ_INT8_PER_TOKEN_HEAD, D, QF32>(c, a, s);
-    case KVQ_FP8_PER_TOKEN_HEAD: return launch_mode<KVQ_FP8_PER_TOKEN_HEAD, D, QF32>(c, a, s);
+    case KVQ_FP8_PER_TENSOR: return launch_mode<KVQ_FP8_PER_TENSOR, D, QF32, OPT>(c, a, s);
+    case KVQ_INT8_PER_TOKEN_HEAD: return launch_mode<KVQ_INT8_PER_TOKEN_HEAD, D, QF32, OPT>(c, a, s);
+    case KVQ_FP8_PER_TOKEN_HEAD: return launch_mode<KVQ_FP8_PER_TOKEN_HEAD, D, QF32, OPT>(c, a, s);
     case KVQ_NVFP4:  // NVFP4 4over6 shares NVFP4's storage: only the write differs
-    case KVQ_NVFP4_4OVER6: return launch_mode<KVQ_NVFP4, D, QF32>(c, a, s);
-    case KVQ_INT4_PER_TOKEN_HEAD: return launch_mode<KVQ_INT4_PER_TOKEN_HEAD, D, QF32>(c, a, s);
+    case KVQ_NVFP4_4OVER6: return launch_mode<KVQ_NVFP4, D, QF32, OPT>(c, a, s);
+    case KVQ_INT4_PER_TOKEN_HEAD: return launch_mode<KVQ_INT4_PER_TOKEN_HEAD, D, QF32, OPT>(c, a, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1005,7 +1075,7 @@ DecodePlan plan_decode(const kvq_cache* c, int num_seqs, int num_q_heads, int ma
 cudaError_t launch_decode(const kvq_cache* c, const DecodePlan& plan, const void* q, const int32_t* block_table,
                           int max_pages, const int32_t* seq_lens, int num_seqs, int num_q_heads, int max_seq_len,
                           float softmax_scale, void* out, int out_dtype, void* workspace, cudaStream_t stream,
-                          const void* kvarn_tail, int num_queries) {
+                          const void* kvarn_tail, int num_queries, const ChunkCall* chunk) {
   DecodeArgs a;
   a.pool = c->base;
   a.q = q;
@@ -1033,11 +1103,17 @@ cudaError_t launch_decode(const kvq_cache* c, const DecodePlan& plan, const void
   a.q_f32 = c->cfg.io_dtype == KVQ_F32;
   a.sm_log2 = softmax_scale * kLog2e;
   a.block_bytes = c->block_bytes;
+  a.cu_q = nullptr;
+  a.prefix_lens = nullptr;
+  a.slopes = nullptr;
+  a.total_q = a.window = 0;
+  a.cap_log2 = 0.0f;
   a.tail = static_cast<const uint8_t*>(kvarn_tail);
   a.rows_per_block = c->rows_per_block;
   {
     uint8_t* o = static_cast<uint8_t*>(out);
-    const size_t oel = (size_t)num_seqs * num_q_heads * c->cfg.head_dim;  // num_seqs counts query rows here
+    // num_seqs counts query rows here
+    const size_t oel = (size_t)(chunk ? chunk->total_q : num_seqs) * num_q_heads * c->cfg.head_dim;
     a.out_span = Span{o, o + oel * (out_dtype == KVQ_F32 ? 4 : 2)};
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const size_t wbytes = partials
@@ -1046,6 +1122,20 @@ cudaError_t launch_decode(const kvq_cache* c, const DecodePlan& plan, const void
     a.ws_span = Span{w, w ? w + wbytes : nullptr};
   }
   if (num_seqs == 0) return cudaSuccess;
+  if (chunk) {  // single tokens of a chunk attention batch
+    a.cu_q = chunk->cu_q;
+    a.prefix_lens = chunk->prefix_lens;
+    a.slopes = chunk->slopes;
+    a.total_q = chunk->total_q;
+    a.window = chunk->window;
+    a.cap_log2 = chunk->cap * kLog2e;
+    const bool f32 = c->cfg.io_dtype == KVQ_F32;
+    if (c->cfg.head_dim == 128)
+      return f32 ? launch_d<128, true, true>(c, a, stream) : launch_d<128, false, true>(c, a, stream);
+    if (c->cfg.head_dim == 32)
+      return f32 ? launch_d<32, true, true>(c, a, stream) : launch_d<32, false, true>(c, a, stream);
+    return cudaErrorInvalidValue;
+  }
   if (c->cfg.mode == KVQ_KVARN_K4V2_G128) return launch_kvarn_decode(a, stream);
   if (umma_decode_eligible(c, num_q_heads, num_queries)) {
     cudaError_t e = launch_umma_decode(c, a, stream);

@@ -15,6 +15,7 @@ struct kvq_cache;
 
 namespace kvq {
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHeaderBytes = 256;
 constexpr int kHdrErrOffset = 12;    // uint32 device error word
 constexpr int kHdrKScaleOffset = 16; // float
@@ -430,7 +431,42 @@ struct DecodeArgs {
   int cluster;
   // the output [B][Hq][D] and the split workspace, as spans (debug-build checks)
   Span out_span, ws_span;
+  // Single tokens of a chunk attention batch (kernels built with OPT): sequence
+  // b's query is row cu_q[b] of the total_q rows of q and out, if it has one; see
+  // kvq_attention_options for the rest.  cap, slopes and prefixes may be absent.
+  const int32_t* cu_q;
+  const int32_t* prefix_lens;
+  const float* slopes;
+  int total_q, window;
+  float cap_log2;  // logit_cap * log2(e)
 };
+
+// The query row of a sequence in such a batch and the tokens it sees: t in
+// [lo, n) or t < prefix; the splits divide the tokens from `base` on.
+struct SingleQuery {
+  int row;  // -1: none
+  int n, lo, prefix, base;
+};
+__device__ __forceinline__ SingleQuery single_query(const DecodeArgs& a, int seq, bool flag) {
+  SingleQuery s{-1, 0, 0, 0, 0};
+  const int q0 = __ldg(a.cu_q + seq), q1 = __ldg(a.cu_q + seq + 1);
+  if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > 1) {
+    if (flag) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_QUERY_RANGE);
+    return s;
+  }
+  if (q1 == q0) return s;
+  s.row = q0;
+  const long long lim = min((long long)a.max_seq_len, (long long)a.max_pages * 16);
+  s.n = __ldg(a.seq_lens + seq);
+  if (s.n > lim || s.n < 0) {
+    if (flag) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
+    s.n = s.n < 0 ? 0 : (int)lim;
+  }
+  s.lo = a.window > 0 ? max(0, s.n - a.window) : 0;
+  s.prefix = a.prefix_lens ? max(0, min(__ldg(a.prefix_lens + seq), s.n)) : 0;
+  s.base = a.prefix_lens ? 0 : s.lo & ~15;
+  return s;
+}
 // Checked stores of one output element and of one split partial.
 __device__ __forceinline__ void store_out(const DecodeArgs& a, long long i, float v) {
   if (a.out_f32) st_chk(static_cast<float*>(a.out) + i, v, a.out_span, a.pool);

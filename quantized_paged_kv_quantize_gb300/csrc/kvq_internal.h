@@ -53,6 +53,8 @@ cudaError_t launch_norm_rope_write(const kvq_cache* c, const kvq_norm_rope& r, c
 
 // Chunk attention (kvq_chunk.cu).
 struct ChunkPlan {
+  bool single = false;  // at most one query per sequence: the decode kernels, planned by `decode`
+  DecodePlan decode{1, 16, 0};
   int num_splits = 1;  // parts of a row tile's token range
   size_t workspace_bytes = 0;
 };
@@ -77,6 +79,7 @@ DecodePlan plan_decode(const kvq_cache* c, int num_seqs, int num_q_heads, int ma
 cudaError_t launch_decode(const kvq_cache* c, const DecodePlan& plan, const void* q, const int32_t* block_table,
                           int max_pages, const int32_t* seq_lens, int num_seqs, int num_q_heads,
                           int max_seq_len, float softmax_scale, void* out, int out_dtype, void* workspace,
-                          cudaStream_t stream, const void* kvarn_tail = nullptr, int num_queries = 1);
+                          cudaStream_t stream, const void* kvarn_tail = nullptr, int num_queries = 1,
+                          const ChunkCall* chunk = nullptr);
 
 }  // namespace kvq

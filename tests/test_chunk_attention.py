@@ -369,3 +369,23 @@ def test_one_query_agrees_with_decode():
 def test_longer_chunks(mode, qlens, lens, heads):
     check(mode, "f16", "f16", heads[0], heads[1], 128, qlens, lens)
     check(mode, "f16", "f16", heads[0], heads[1], 128, qlens, lens, cap=3.0, alibi=True, window=200)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f16", "f32"])
+@pytest.mark.parametrize("qlens,lens", [([40, 3], [700, 500]), ([200, 9], [900, 40]), ([1, 1], [700, 33])])
+def test_pages_below_the_window_are_not_read(io, qlens, lens):
+    """A server may give up the pages that no window reaches: their table entries can be anything."""
+    K = kvq()
+    window = 100
+    cache, table, vals = build("fp8_per_token_head", io, 2, 128, lens)
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    q = torch.randn(cu[-1], 8, 128, device="cuda").to(torch.float16 if io == "f16" else torch.float32)
+    want = formula(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5, window=window)
+    for b, (m, n) in enumerate(zip(qlens, lens)):
+        table[b, :max(0, n - m - window + 1) // 16] = -7
+    got = run(cache, table, q, cu, lens, torch.float32, window=window)
+    half = run(cache, table, q, cu, lens, torch.float16, window=window) if io == "f16" else got
+    assert K.kvq_cache_read_errors(cache) == 0
+    assert np.abs(got.double().cpu().numpy() - want).max() < 1e-4
+    assert np.abs(half.double().cpu().numpy() - want).max() < 1e-2
