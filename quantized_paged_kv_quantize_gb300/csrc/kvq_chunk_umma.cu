@@ -11,8 +11,9 @@
 // more than 2^8, so that P stays inside fp16's normal range whatever the
 // magnitude of scores and values.
 //
-// Roles (13 warps, 128 registers a thread, one CTA per SM):
-//  warps 0-3, 4-7  softmax: thread = row of S_0 / S_1;
+// Roles (one CTA per SM; registers are shared out between the warpgroups):
+//  warps 0-3, 4-7  softmax: thread = row of S_0 / S_1, the row's 128 scores in
+//                  registers from the load to the weights;
 //  warps 8-11      dequantization: a warp takes two pages of a 128-token tile, their
 //                  packed words in registers one tile ahead, and writes the
 //                  codes as fp16 core matrices (8 tokens x 16 bytes), which
@@ -38,7 +39,9 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kD = 128;
 constexpr int kTok = 128;       // tokens of a tile
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;    // warps 13-15 only fill the last warpgroup
+// Registers a thread (the launch gives 128 each): 256 x 176 + 128 x 104 + 128 x 48 <= 512 x 128.
+constexpr int kRegsSoftmax = 176, kRegsDequant = 104, kRegsIssue = 48;
 constexpr int kPages = 2;       // pages of a tile that one warp dequantizes
 constexpr int kOpBytes = kTok * kD * 2;  // one fp16 operand tile
 constexpr int kLbo = 128, kSbo = 2048;   // core matrices: along channels, along rows / tokens
@@ -93,9 +96,14 @@ __device__ __forceinline__ void tm_wait(uint32_t* r) {  // the registers pass th
                : "memory");
   asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ float2 pair(const uint32_t* r, int i) {
-  return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+__device__ __forceinline__ float2 get(const uint32_t* r, int i) {  // columns i, i + 1
+  return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
 }
+__device__ __forceinline__ void put(uint32_t* r, int i, float2 x) {
+  r[i] = __float_as_uint(x.x);
+  r[i + 1] = __float_as_uint(x.y);
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
 __device__ __forceinline__ int exponent(float x) {  // floor(log2 x), x > 0, clamped
   return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
 }
@@ -216,7 +224,10 @@ __device__ __forceinline__ void store_page(const Words<MODE>& x, uint8_t* op, in
       }
     } else {
       const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
-      uint32_t even[8], odd[8];  // the pair's two tokens, 16 channels
+      // tokens 2a and 2a + 1; lanes 4..7 of each eight take the odd one first, so
+      // that the eight rows stored together differ modulo 8
+      const uint32_t first = (a & 4) ? 0x7632u : 0x5410u, second = first ^ 0x2222u;
+      uint32_t t0[8], t1[8];  // 16 channels of the first and of the second token
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t h[4];  // (even token, odd token) of channels 4 i ..
@@ -229,24 +240,20 @@ __device__ __forceinline__ void store_page(const Words<MODE>& x, uint8_t* op, in
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = s4_pair(in[i] >> (4 * e));
         }
-        even[2 * i] = prmt(h[0], h[1], 0x5410u);
-        even[2 * i + 1] = prmt(h[2], h[3], 0x5410u);
-        odd[2 * i] = prmt(h[0], h[1], 0x7632u);
-        odd[2 * i + 1] = prmt(h[2], h[3], 0x7632u);
+        t0[2 * i] = prmt(h[0], h[1], first);
+        t0[2 * i + 1] = prmt(h[2], h[3], first);
+        t1[2 * i] = prmt(h[0], h[1], second);
+        t1[2 * i + 1] = prmt(h[2], h[3], second);
       }
-      // tokens 2a and 2a + 1; lanes 4..7 of each eight store the odd one first,
-      // so that the eight rows stored together differ modulo 8
-      const bool flip = a & 4;
       uint8_t* p = base + (a >> 2) * kSbo + 2 * (b + 4 * r) * kLbo + ((2 * a) & 7) * 16;
+      uint8_t* p0 = p + ((a & 4) ? 16 : 0);
+      uint8_t* p1 = p + ((a & 4) ? 0 : 16);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool o = flip != (u == 1);
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint4*>(p0 + c * kLbo) = make_uint4(t0[4 * c], t0[4 * c + 1], t0[4 * c + 2], t0[4 * c + 3]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint4*>(p + (o ? 16 : 0) + c * kLbo) =
-              make_uint4(o ? odd[4 * c] : even[4 * c], o ? odd[4 * c + 1] : even[4 * c + 1],
-                         o ? odd[4 * c + 2] : even[4 * c + 2], o ? odd[4 * c + 3] : even[4 * c + 3]);
-      }
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint4*>(p1 + c * kLbo) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
     }
   }
 }
@@ -266,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ RowTile tile_s;
+  __shared__ int failed_s;
   float* ksm = reinterpret_cast<float*>(sm + L::KS);
   float* vsm = reinterpret_cast<float*>(sm + L::VS);
   float* ones = reinterpret_cast<float*>(sm + L::ONES);
@@ -296,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       mbar_init(&bar.p_full[i], 4);
     }
     mbar_init(&bar.o_full, 1);
+    failed_s = 0;
     mbar_fence_init();
   }
   if (warp == 12) {
@@ -327,16 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
     vfac = *reinterpret_cast<const float*>(a.pool + kHdrVScaleOffset);
   }
 
-  // row state of the softmax threads
-  const int blk = warp >> 2;  // S_0 or S_1 (warps 0-7)
-  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  const int row = STREAMS == 1 ? tid : (tid & 127);
-  float R = -1e30f;
-  float2 l2 = make_float2(0.0f, 0.0f);
-  bool any = false;  // this block has accumulated something
-
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ dequantization
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
     Words<MODE> kw[kPages], vw[kPages];
     float sc[kPages];
     int pid[kPages], ahead[kPages];  // page ids of tile i, and (unchecked) of tile i + 1
@@ -420,8 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.v_full[st]);
     }
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     const uint64_t dq = umma_sdesc(smem_u32(sm + L::Q), kLbo, kSbo);
     const uint64_t dk = umma_sdesc(smem_u32(sm + L::K), kLbo, kSbo);
     const uint64_t dv = umma_sdesc(smem_u32(sm + L::V), kSbo, kLbo);  // MN-major: tokens along K, channels along N
@@ -440,8 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       }
       __syncwarp();
     };
-    for (int k = 0; k < min(2, items); ++k) qk(k);
-    for (int k = 0; k < items && ok; ++k) {
+    const int mine = warp == 12 ? items : 0;
+    for (int k = 0; k < min(2, mine); ++k) qk(k);
+    for (int k = 0; k < mine && ok; ++k) {
       const int i = STREAMS == 1 ? k >> 1 : k, b = k & 1, st = i & 1;
       ok = mbar_wait_bounded(&bar.v_full[st], (i >> 1) & 1) && ok;
       ok = mbar_wait_bounded(&bar.p_full[b], (k >> 1) & 1) && ok;
@@ -458,8 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       __syncwarp();
       if (k + 2 < items) qk(k + 2);
     }
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int blk = warp >> 2;  // S_0 or S_1
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int row = STREAMS == 1 ? tid : (tid & 127);
+    float R = -1e30f;
+    float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    bool any = false;  // this block has accumulated something
     const bool real = row < t.count;
     const int rr = t.r0 + (real ? row : 0);
     const int pos = t.n - t.m + rr / a.G;
@@ -486,6 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         break;
       }
       tc_fence_after();
+      uint32_t x[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tm_ld(tS + 32 * c, x + 32 * c);
       const float* ks = ksm + slot * kTok;
       const float* vs = vsm + slot * kTok;
       const int4 pg0 = *reinterpret_cast<const int4*>(page_s + slot * 8), pg1 = *reinterpret_cast<const int4*>(page_s + slot * 8 + 4);
@@ -493,111 +507,84 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       const int pmax = max(max(max(pg0.x, pg0.y), max(pg0.z, pg0.w)), max(max(pg1.x, pg1.y), max(pg1.z, pg1.w)));
       const float ve = PT ? (float)max(pmax, -100) : 0.0f;
       const bool masked = pmin == kMissing || !all_see(a, mine, t0, kTok);
-      const bool slow = OPT || masked;  // scores are finished in the first pass and put back
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tm_wait(x + 32 * c);
 
-      // first pass: the row's maximum (log2 units)
-      float mx = -INFINITY;
-      uint32_t x[2][32];
-      tm_ld(tS, x[0]);
-      if (!slow) {
-        float2 m2 = make_float2(-INFINITY, -INFINITY);
+      // scores in log2 units (without per-token scales the factor waits for the
+      // exponents, unless the score is needed now)
+      float kf = kfac;
+      if constexpr (PT) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tm_wait(x[c & 1]);
-          if (c < 3) tm_ld(tS + 32 * (c + 1), x[(c + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 y0 = pair(x[c & 1], e), y1 = pair(x[c & 1], e + 1);
-            if constexpr (PT) {
-              const float4 f = *reinterpret_cast<const float4*>(ks + 32 * c + 2 * e);
-              y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
-              y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
-            }
-            m2.x = fmaxf(m2.x, fmaxf(y0.x, y1.x));
-            m2.y = fmaxf(m2.y, fmaxf(y0.y, y1.y));
-          }
+        for (int e = 0; e < 128; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(ks + e);
+          put(x, e, __fmul2_rn(get(x, e), make_float2(f.x, f.y)));
+          put(x, e + 2, __fmul2_rn(get(x, e + 2), make_float2(f.z, f.w)));
         }
-        mx = fmaxf(m2.x, m2.y);
-        if constexpr (!PT) mx *= kfac;
-      } else {
-        const int there[8] = {pg0.x, pg0.y, pg0.z, pg0.w, pg1.x, pg1.y, pg1.z, pg1.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t* v = x[0];
-          tm_wait(v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[e] = __float_as_uint(__uint_as_float(v[e]) * (PT ? ks[32 * c + e] : kfac));
-          }
-          if constexpr (OPT) {
-            if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                v[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(v[e]) * rcap)));
-            }
-            if (a.slopes) {
-              const float d = (float)(pos - t0 - 32 * c);  // distances are whole numbers below 2^24: exact
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(-slope, fabsf(d - (float)e), __uint_as_float(v[e])));
-            }
-          }
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (there[2 * c + (e >> 4)] == kMissing || !sees(t0 + 32 * c + e)) v[e] = 0xff800000u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-          tmem_st<32>(tS + 32 * c, v);
-          if (c < 3) tm_ld(tS + 32 * (c + 1), v);
-        }
-        tmem_wait_st();
+        kf = 1.0f;
       }
+      if constexpr (OPT) {
+        if constexpr (!PT) {
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) put(x, e, __fmul2_rn(get(x, e), make_float2(kfac, kfac)));
+          kf = 1.0f;
+        }
+        if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            x[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(x[e]) * rcap)));
+        }
+        if (a.slopes) {
+          const float d = (float)(pos - t0);  // distances are whole numbers below 2^24: exact
+#pragma unroll
+          for (int e = 0; e < 128; ++e) x[e] = __float_as_uint(fmaf(-slope, fabsf(d - (float)e), __uint_as_float(x[e])));
+        }
+      }
+      if (masked) {
+        const int there[8] = {pg0.x, pg0.y, pg0.z, pg0.w, pg1.x, pg1.y, pg1.z, pg1.w};
+        // tokens of the tile that the row sees: [lo, hi) or below pre
+        const int lo = sees.lo - t0, hi = sees.hi - t0, pre = sees.prefix - t0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const bool gone = there[p] == kMissing;
+#pragma unroll
+          for (int e = 16 * p; e < 16 * p + 16; ++e)
+            if (gone || !((e >= lo && e < hi) || e < pre)) x[e] = 0xff800000u;  // -inf
+        }
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; e += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          m4[u] = fmaxf(m4[u], fmaxf(__uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1])));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kf;  // kf > 0
 
       // the reference: moved when this tile passes it by more than the slack
       const float cand = mx + ve;
-      if (__any_sync(kFull, cand > R + kSlack)) {
-        const float to = fmaxf(R, cand), al = ex2(R - to);
+      float al = 1.0f;
+      const bool move = __any_sync(kFull, cand > R + kSlack);
+      if (move) {
+        const float to = fmaxf(R, cand);
+        al = ex2(R - to);
         R = to;
-        l2 = __fmul2_rn(l2, make_float2(al, al));
-        if (any) {  // every product issued before this S has completed
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t* v = x[0];
-            tm_ld(tO + 32 * c, v);
-            tm_wait(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-            tmem_st<32>(tO + 32 * c, v);
-          }
-          tmem_wait_st();
-        }
+        l2[0] = __fmul2_rn(l2[0], make_float2(al, al));
+        l2[1] = __fmul2_rn(l2[1], make_float2(al, al));
       }
-      any = true;
 
-      // second pass: weights, their sum, and P in fp16 over the first half of S
-      const float* kp = slow ? ones : ks;
-      const float2 nR = make_float2(-R, -R);
-      const float kf = slow ? 1.0f : kfac;
-      tm_ld(tS, x[0]);
+      // weights, their sum, and P in fp16 over the first half of S
+      const float2 nR = make_float2(-R, -R), kf2 = make_float2(kf, kf);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        tm_wait(x[c & 1]);
-        if (c < 3) tm_ld(tS + 32 * (c + 1), x[(c + 1) & 1]);
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          float2 f0 = make_float2(kf, kf), f1 = f0;
-          if constexpr (PT) {
-            const float4 f = *reinterpret_cast<const float4*>(kp + 32 * c + 2 * e);
-            f0 = make_float2(f.x, f.y);
-            f1 = make_float2(f.z, f.w);
-          }
-          const float2 y0 = __ffma2_rn(pair(x[c & 1], e), f0, nR), y1 = __ffma2_rn(pair(x[c & 1], e + 1), f1, nR);
+          const int at = 32 * c + 2 * e;
+          const float2 y0 = __ffma2_rn(get(x, at), kf2, nR), y1 = __ffma2_rn(get(x, at + 2), kf2, nR);
           float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-          l2 = __fadd2_rn(l2, __fadd2_rn(p0, p1));
+          l2[0] = __fadd2_rn(l2[0], p0);
+          l2[1] = __fadd2_rn(l2[1], p1);
           if constexpr (PT) {
-            const float4 f = *reinterpret_cast<const float4*>(vs + 32 * c + 2 * e);
+            const float4 f = *reinterpret_cast<const float4*>(vs + at);
             if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
               p0.x = y0.x == -INFINITY ? 0.0f : p0.x * f.x;
               p0.y = y0.y == -INFINITY ? 0.0f : p0.y * f.y;
@@ -613,98 +600,108 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         }
         tmem_st<16>(tS + 16 * c, p);
       }
+      if (move && any) {  // every product issued before this S has completed
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tm_ld(tO + 32 * c, v);
+          tm_wait(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+          tmem_st<32>(tO + 32 * c, v);
+        }
+      }
+      any = true;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[blk]);
     }
-  }
 
-  // ------------------------------------------------------------ outputs
-  if (items > 0) ok = mbar_wait_bounded(&bar.o_full, 0) && ok;
-  tc_fence_after();
-  const bool failed = __syncthreads_or(!ok);
-  if (failed) {
-    if (tid == 0) set_error(pool, KVQ_DEVERR_TIMEOUT);
-  } else {
-    float l = l2.x + l2.y;
+    // ------------------------------------------------------------ outputs
+    if (items > 0) ok = mbar_wait_bounded(&bar.o_full, 0) && ok;
+    tc_fence_after();
+    if (!ok) failed_s = 1;
+    softmax_sync();
+    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     float f0 = 1.0f, f1 = 0.0f;                          // two streams: factors of their accumulators
     float* other = reinterpret_cast<float*>(sm + L::K);  // the second stream's rows: [128][132], then R and l
     constexpr int kStride = 132;
-    if constexpr (STREAMS == 2) {
-      if (warp >= 4 && warp < 8) {
-        float* o = other + row * kStride;
+    if (failed_s) {
+      if (tid == 0) set_error(pool, KVQ_DEVERR_TIMEOUT);
+    } else {
+      if constexpr (STREAMS == 2) {
+        if (blk == 1) {
+          float* o = other + row * kStride;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            if (any) {
+              tm_ld(tO + 32 * c, v);
+              tm_wait(v);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(o + 32 * c + e) = any ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3])
+                                                              : make_uint4(0u, 0u, 0u, 0u);
+          }
+          other[128 * kStride + row] = R;
+          other[128 * kStride + 128 + row] = l;
+        }
+        softmax_sync();
+        if (blk == 0) {
+          const float R1 = other[128 * kStride + row], l1 = other[128 * kStride + 128 + row];
+          const float top = fmaxf(R, R1);
+          f0 = exp2f(R - top);
+          f1 = exp2f(R1 - top);
+          l = l * f0 + l1 * f1;
+          R = top;
+        }
+      }
+      if ((STREAMS == 1 || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
+        const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+        const float g = a.num_splits > 1 ? vfac : l > 0.0f ? vfac / l : 0.0f;
+        const long long pi = qrow * a.num_splits + split;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           if (any) {
-            tm_ld(tb + 384 + lanes + 32 * c, v);
+            tm_ld(tO + 32 * c, v);
             tm_wait(v);
           }
+          float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(o + 32 * c + e) = any ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3])
-                                                            : make_uint4(0u, 0u, 0u, 0u);
-        }
-        other[128 * kStride + row] = R;
-        other[128 * kStride + 128 + row] = l;
-      }
-      __syncthreads();
-      if (warp < 4) {
-        const float R1 = other[128 * kStride + row], l1 = other[128 * kStride + 128 + row];
-        const float top = fmaxf(R, R1);
-        f0 = exp2f(R - top);
-        f1 = exp2f(R1 - top);
-        l = l * f0 + l1 * f1;
-        R = top;
-      }
-    }
-    const int last = STREAMS == 1 ? 8 : 4;
-    if (warp < last && row < ((t.count + 31) & ~31)) {  // whole warps
-      const bool real = row < t.count;
-      const int rr = t.r0 + (real ? row : 0);
-      const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
-      const float g = a.num_splits > 1 ? vfac : l > 0.0f ? vfac / l : 0.0f;
-      const long long pi = qrow * a.num_splits + split;
+          for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(v[e]) * f0 : 0.0f;
+          if constexpr (STREAMS == 2) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        if (any) {
-          tm_ld(tb + 256 + 128 * blk + lanes + 32 * c, v);
-          tm_wait(v);
-        }
-        float o[32];
+            for (int e = 0; e < 32; e += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(other + row * kStride + 32 * c + e);
+              o[e] += u.x * f1;
+              o[e + 1] += u.y * f1;
+              o[e + 2] += u.z * f1;
+              o[e + 3] += u.w * f1;
+            }
+          }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(v[e]) * f0 : 0.0f;
-        if constexpr (STREAMS == 2) {
+          for (int e = 0; e < 32; ++e) o[e] = l > 0.0f ? o[e] * g : 0.0f;
+          if (!real) continue;
+          if (a.num_splits == 1) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(other + row * kStride + 32 * c + e);
-            o[e] += u.x * f1;
-            o[e + 1] += u.y * f1;
-            o[e + 2] += u.z * f1;
-            o[e + 3] += u.w * f1;
+            for (int e = 0; e < 32; e += 8) {
+              const uint4 h = make_uint4(h2_as_u32(__floats2half2_rn(o[e], o[e + 1])), h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3])),
+                                         h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5])), h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7])));
+              st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD + 32 * c + e), h, a.out_span, a.pool);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              st_chk(reinterpret_cast<float4*>(a.ws_o + pi * kD + 32 * c + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]),
+                     a.ws_span, a.pool);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = l > 0.0f ? o[e] * g : 0.0f;
-        if (!real) continue;
-        if (a.num_splits == 1) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            const uint4 h = make_uint4(h2_as_u32(__floats2half2_rn(o[e], o[e + 1])), h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3])),
-                                       h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5])), h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7])));
-            st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD + 32 * c + e), h, a.out_span, a.pool);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            st_chk(reinterpret_cast<float4*>(a.ws_o + pi * kD + 32 * c + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]),
-                   a.ws_span, a.pool);
-        }
+        if (real && a.num_splits > 1)
+          st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l > 0.0f ? R : -INFINITY, l), a.ws_span, a.pool);
       }
-      if (real && a.num_splits > 1)
-        st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l > 0.0f ? R : -INFINITY, l), a.ws_span, a.pool);
     }
   }
   tc_fence_before();
