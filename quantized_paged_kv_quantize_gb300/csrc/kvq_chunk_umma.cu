@@ -4,16 +4,16 @@
 //
 // Mathematics (kvq_chunk.cu has the operator's definition).  With codes K, V
 // (exact in fp16) and scales apart, one 128 x 128 block of (row, token) pairs is
-//   S = Q K^T,  y = S ks_t (log2 units),  P = 2^(y + C - R),  O += P V',
-//   l += 2^(y - R),  V' = V vs_t 2^-C,  out = O / l
-// in fp32 but for two roundings to fp16, each 2^-12 of its value and random in
-// sign, below the output's own rounding: P, and with per-token scales V' (one
-// rounding of the exact product; C is the exponent of the tile's largest value
-// scale, so V' keeps its bits whatever the values' magnitude).  Scores stay exact
-// products of fp32 grade.  R is a row's reference: the largest y + C met, moved (O
-// and l rescaled) only when a block passes it by more than 2^8, so that P stays
-// inside fp16's normal range.  Tiles are taken from the nearest tokens to the
-// farthest: a bias by distance then never moves the reference again.
+//   S = Q K^T,  y = S ks_t (log2 units),  P = 2^(y - R) vs_t,  O += P V,  l += 2^(y - R)
+// in fp32 but for P, which is rounded to fp16 (2^-12 of a weight, random in sign: of
+// the size of the output's own rounding.  Taking vs_t into the fp16 values instead
+// was 20% faster and a second such rounding: 3.3e-4 against 2.7e-4 in the 2-norm,
+// where an exact result rounded to fp16 is 2.1e-4 off; it was not kept).  R is a
+// row's reference: the largest y + floor(log2 vs) of a tile met, moved (O and l
+// rescaled) only when a block passes it by more than 2^8, so that P stays inside
+// fp16's normal range whatever the magnitude of scores and values.  Tiles are taken
+// from the nearest tokens to the farthest: a bias by distance then never moves the
+// reference again.
 //
 // Roles (16 warps, one CTA per SM; registers are shared out between the warpgroups):
 //  warps 0-3, 4-7  softmax of block 0 and block 1: thread = row, whose 128 scores are
@@ -61,10 +61,10 @@ struct Smem {
   static constexpr int K = Q + (STREAMS == 1 ? 2 : 1) * kOpBytes;  // two stages each
   static constexpr int V = K + 2 * kOpBytes;
   static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] key scales in log2 units
-  static constexpr int PAGE = KS + kSlots * kTok * 4;              // [slot][8] page states
+  static constexpr int VS = KS + kSlots * kTok * 4;                // [slot][128] value scales
+  static constexpr int PAGE = VS + kSlots * kTok * 4;              // [slot][8] page states
   static constexpr int START = PAGE + kSlots * 8 * 4;              // [slot] first token of the tile
-  static constexpr int EXP = START + kSlots * 4;                   // [slot] C of the tile
-  static constexpr int BYTES = EXP + kSlots * 4;
+  static constexpr int BYTES = START + kSlots * 4;
   static constexpr size_t dynamic() { return BYTES + 128; }
 };
 constexpr int kMissing = INT32_MIN;  // page state: not there; else the exponent of its largest value scale
@@ -110,7 +110,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
   return a;
 }
-__device__ __forceinline__ void dequant_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }  // warps 8-11
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
 __device__ __forceinline__ int exponent(float x) {  // floor(log2 x), x > 0, clamped
   return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
@@ -193,39 +192,11 @@ __device__ __forceinline__ void codes16(const uint4& w, uint4* out) {
   out[1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// Scales of the value tokens that a lane converts, as hi + lo in fp16: one-byte
-// codes, tokens lane & 7 and + 8, each in both halves; 4-bit codes, entry 0: the
-// tokens of its pair.
-struct ValueScale {
-  uint32_t hi[2], lo[2];
-};
-template <int MODE>
-__device__ __forceinline__ ValueScale value_scale(float s, int lane) {  // s: of token lane - 16, in lanes 16-31
-  ValueScale v;
-  constexpr bool FOUR = Words<MODE>::FOUR;
-  const float a = __shfl_sync(kFull, s, 16 + (FOUR ? 2 * (lane & 7) : (lane & 7)));
-  const float b = __shfl_sync(kFull, s, 16 + (FOUR ? 2 * (lane & 7) + 1 : (lane & 7) + 8));
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-  v.hi[0] = h2_as_u32(FOUR ? h : __low2half2(h));
-  v.hi[1] = h2_as_u32(__high2half2(h));
-  v.lo[0] = h2_as_u32(FOUR ? l : __low2half2(l));
-  v.lo[1] = h2_as_u32(__high2half2(l));
-  return v;
-}
-// code (hi + lo), rounded to fp16: the fused step rounds once, the small product
-// beneath it is within 2^-24 of the result.
-__device__ __forceinline__ uint32_t scaled(uint32_t code, const ValueScale& v, int i) {
-  const __half2 c = u32_as_h2(code);
-  return h2_as_u32(__hfma2(c, u32_as_h2(v.hi[i]), __hmul2(c, u32_as_h2(v.lo[i]))));
-}
-
 // Write page `w` (tokens 16 w ..) of a tile into the operand at `op`: channel
 // group c of token t at (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring
 // lanes always fill one core matrix row set, so the stores have no conflicts.
 template <int MODE, int SIDE>
-__device__ __forceinline__ void store_page(const Words<MODE>& x, const ValueScale& vs, uint8_t* op, int w, int lane) {
+__device__ __forceinline__ void store_page(const Words<MODE>& x, uint8_t* op, int w, int lane) {
   const int a = lane & 7, b = lane >> 3;
   uint8_t* base = op + 2 * w * kSbo;
 #pragma unroll
@@ -233,11 +204,6 @@ __device__ __forceinline__ void store_page(const Words<MODE>& x, const ValueScal
     if constexpr (!Words<MODE>::FOUR) {
       uint4 c[2];
       codes16<MODE>(x.w[r], c);
-      if constexpr (SIDE == 1 && kPerTokenScale<MODE>) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          c[i] = make_uint4(scaled(c[i].x, vs, r & 1), scaled(c[i].y, vs, r & 1), scaled(c[i].z, vs, r & 1), scaled(c[i].w, vs, r & 1));
-      }
       uint8_t* p = base + (r & 1) * kSbo + a * 16 + 2 * (b + 4 * (r >> 1)) * kLbo;
       *reinterpret_cast<uint4*>(p) = c[0];
       *reinterpret_cast<uint4*>(p + kLbo) = c[1];
@@ -279,7 +245,7 @@ __device__ __forceinline__ void store_page(const Words<MODE>& x, const ValueScal
           for (int e = 0; e < 4; ++e) h[e] = h2_as_u32(__hmul2(u32_as_h2(h[e]), s));
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = scaled(s4_pair(in[i] >> (4 * e)), vs, 0);
+          for (int e = 0; e < 4; ++e) h[e] = s4_pair(in[i] >> (4 * e));
         }
         t0[2 * i] = prmt(h[0], h[1], first);
         t0[2 * i + 1] = prmt(h[2], h[3], first);
@@ -316,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   __shared__ RowTile tile_s;
   __shared__ int failed_s;
   float* ksm = reinterpret_cast<float*>(sm + L::KS);
-  float* exp_s = reinterpret_cast<float*>(sm + L::EXP);
+  float* vsm = reinterpret_cast<float*>(sm + L::VS);
   int* start_s = reinterpret_cast<int*>(sm + L::START);
   int* page_s = reinterpret_cast<int*>(sm + L::PAGE);
 
@@ -438,24 +404,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         valid[u] = pid[u] >= 0 ? min(16, t.n - page(i, u) * 16) : 0;
         if constexpr (PT) {
           if ((lane & 15) >= valid[u]) sc[u] = 0.0f;
-          if (lane < 16) ksm[slot * kTok + 16 * w + lane] = sc[u] * kfac;
+          (lane < 16 ? ksm : vsm)[slot * kTok + 16 * w + (lane & 15)] = lane < 16 ? sc[u] * kfac : sc[u];
           const uint32_t top = __reduce_max_sync(kFull, lane >= 16 ? __float_as_uint(fabsf(sc[u])) : 0u);
           if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : top ? exponent(__uint_as_float(top)) : -100;
         } else {
           if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : 0;
         }
-        store_page<MODE, 0>(kw[u], ValueScale{}, sm + L::K + st * kOpBytes, w, lane);
+        store_page<MODE, 0>(kw[u], sm + L::K + st * kOpBytes, w, lane);
         if (valid[u] < 16) drop_tokens<MODE>(vw[u], lane, valid[u]);
-      }
-      // C of the tile, and each token's value scale under it as an fp16 pair hi + lo
-      ValueScale vsc[kPages];
-      if constexpr (PT) {
-        dequant_sync();
-        const int4 a4 = *reinterpret_cast<const int4*>(page_s + slot * 8), b4 = *reinterpret_cast<const int4*>(page_s + slot * 8 + 4);
-        const int C = max(max(max(max(a4.x, a4.y), max(a4.z, a4.w)), max(max(b4.x, b4.y), max(b4.z, b4.w))), -100);
-        if (warp == kDequantWarp && lane == 0) exp_s[slot] = (float)C;
-#pragma unroll
-        for (int u = 0; u < kPages; ++u) vsc[u] = value_scale<MODE>(sc[u] * __int_as_float((127 - C) << 23), lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -469,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       if (i >= 2) ok = wait(&bar.v_free[st], ((i >> 1) - 1) & 1) && ok;
       if (!ok) break;
 #pragma unroll
-      for (int u = 0; u < kPages; ++u) store_page<MODE, 1>(vw[u], vsc[u], sm + L::V + st * kOpBytes, (warp - kDequantWarp) + 4 * u, lane);
+      for (int u = 0; u < kPages; ++u) store_page<MODE, 1>(vw[u], sm + L::V + st * kOpBytes, (warp - kDequantWarp) + 4 * u, lane);
       load_v();
       fence_proxy_async_smem();
       __syncwarp();
@@ -553,109 +509,154 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         break;
       }
       tc_fence_after();
-      uint32_t x[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tm_ld(tS + 32 * c, x + 32 * c);
       const int t0 = start_s[slot];
-      const float* ks = ksm + slot * kTok;
       const int4 pg0 = *reinterpret_cast<const int4*>(page_s + slot * 8), pg1 = *reinterpret_cast<const int4*>(page_s + slot * 8 + 4);
       const int pmin = min(min(min(pg0.x, pg0.y), min(pg0.z, pg0.w)), min(min(pg1.x, pg1.y), min(pg1.z, pg1.w)));
       const bool masked = pmin == kMissing || !all_see(a, mine, t0, kTok);
-      const float C = PT ? exp_s[slot] : 0.0f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tm_wait(x + 32 * c);
+      // exponent of the tile's largest value scale
+      const float ve = PT ? (float)max(max(max(max(pg0.x, pg0.y), max(pg0.z, pg0.w)), max(max(pg1.x, pg1.y), max(pg1.z, pg1.w))), -100) : 0.0f;
 
-      // exponents of the weights: scores in log2 units less the reference
-      const float2 nR = make_float2(C - R, C - R);
+      // Half a tile's scores at a time: P of a half goes over columns of S that have
+      // been read.
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const float* ks = ksm + slot * kTok + 64 * h;
+        const float* vs = vsm + slot * kTok + 64 * h;
+        uint32_t x[64];
+        tm_ld(tS + 64 * h, x);
+        tm_ld(tS + 64 * h + 32, x + 32);
+        tm_wait(x);
+        tm_wait(x + 32);
+
+        // Exponents of the weights: scores in log2 units less the reference.  Where
+        // one factor serves the whole tile (RAW) the scores stay as they are until the
+        // weights are computed: one fused step then does both, in the shadow of the
+        // exponentials.
+        constexpr bool RAW = !PT && !OPT;
+        const float2 nR = make_float2(-R, -R);
 #pragma unroll
-      for (int e = 0; e < 128; e += 4) {
-        float4 f = make_float4(kfac, kfac, kfac, kfac);
-        if constexpr (PT) f = *reinterpret_cast<const float4*>(ks + e);
+        for (int e = 0; e < (RAW ? 0 : 64); e += 4) {
+          float4 f = make_float4(kfac, kfac, kfac, kfac);
+          if constexpr (PT) f = *reinterpret_cast<const float4*>(ks + e);
+          if constexpr (OPT) {
+            put(x, e, __fmul2_rn(get(x, e), make_float2(f.x, f.y)));
+            put(x, e + 2, __fmul2_rn(get(x, e + 2), make_float2(f.z, f.w)));
+          } else {
+            put(x, e, __ffma2_rn(get(x, e), make_float2(f.x, f.y), nR));
+            put(x, e + 2, __ffma2_rn(get(x, e + 2), make_float2(f.z, f.w), nR));
+          }
+        }
         if constexpr (OPT) {
-          put(x, e, __fmul2_rn(get(x, e), make_float2(f.x, f.y)));
-          put(x, e + 2, __fmul2_rn(get(x, e + 2), make_float2(f.z, f.w)));
-        } else {
-          put(x, e, __ffma2_rn(get(x, e), make_float2(f.x, f.y), nR));
-          put(x, e + 2, __ffma2_rn(get(x, e + 2), make_float2(f.z, f.w), nR));
+          if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
+            const float cap2 = a.cap * kLog2e, rcap = 2.0f * kLog2e / cap2;
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              x[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(x[e]) * rcap)));
+          }
+          if (a.slopes) {
+            const float d = (float)(pos - t0 - 64 * h);  // distances are whole numbers below 2^24: exact
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(fmaf(slope, fabsf(d - (float)e), __uint_as_float(x[e])));
+          }
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) put(x, e, __fadd2_rn(get(x, e), nR));
         }
-      }
-      if constexpr (OPT) {
-        if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-          const float cap2 = a.cap * kLog2e, rcap = 2.0f * kLog2e / cap2;
+        if (masked) {
+          const int4 pg = h ? pg1 : pg0;
+          const int there[4] = {pg.x, pg.y, pg.z, pg.w};
+          // tokens of the half that the row sees: [lo, hi) or below pre
+          const int lo = sees.lo - t0 - 64 * h, hi = sees.hi - t0 - 64 * h, pre = sees.prefix - t0 - 64 * h;
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            x[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(x[e]) * rcap)));
+          for (int p = 0; p < 4; ++p) {
+            const bool gone = there[p] == kMissing;
+#pragma unroll
+            for (int e = 16 * p; e < 16 * p + 16; ++e)
+              if (gone || !((e >= lo && e < hi) || e < pre)) x[e] = 0xff800000u;  // -inf
+          }
         }
-        if (a.slopes) {
-          const float d = (float)(pos - t0);  // distances are whole numbers below 2^24: exact
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 128; ++e) x[e] = __float_as_uint(fmaf(slope, fabsf(d - (float)e), __uint_as_float(x[e])));
-        }
+        for (int e = 0; e < 64; e += 8)
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) put(x, e, __fadd2_rn(get(x, e), nR));
-      }
-      if (masked) {
-        const int there[8] = {pg0.x, pg0.y, pg0.z, pg0.w, pg1.x, pg1.y, pg1.z, pg1.w};
-        // tokens of the tile that the row sees: [lo, hi) or below pre
-        const int lo = sees.lo - t0, hi = sees.hi - t0, pre = sees.prefix - t0;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const bool gone = there[p] == kMissing;
-#pragma unroll
-          for (int e = 16 * p; e < 16 * p + 16; ++e)
-            if (gone || !((e >= lo && e < hi) || e < pre)) x[e] = 0xff800000u;  // -inf
-        }
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 128; e += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + ve;
+        if constexpr (RAW) mx = fmaf(mx, kfac, -R);  // kfac > 0; ve = 0
 
-      // The reference moves (and exponents, sum and accumulator with it) only when
-      // a row meets its first score or one passes it by more than the slack.
-      float al = 1.0f;
-      const bool move = __any_sync(kFull, mx > (fresh ? -INFINITY : kSlack));
-      if (move) {
-        const bool first = fresh && mx > -INFINITY;
-        const float up = first ? mx : fmaxf(mx, 0.0f);
-        if (first) fresh = false;
-        else al = ex2(-up);
-        R += up;
-        l *= al;
+        // The reference moves (and exponents, sum, accumulator and the first half's
+        // weights with it) only when a row meets its first score or one passes it by
+        // more than the slack.
+        if (__any_sync(kFull, mx > (fresh ? -INFINITY : kSlack))) {
+          const bool first = fresh && mx > -INFINITY;
+          const float up = first ? mx : fmaxf(mx, 0.0f);
+          const float al = first ? 1.0f : ex2(-up);  // (a first score: nothing accumulated yet)
+          fresh = fresh && !first;
+          R += up;
+          l *= al;
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) put(x, e, __fadd2_rn(get(x, e), make_float2(-up, -up)));
-      }
+          for (int e = 0; e < (RAW ? 0 : 64); e += 2) put(x, e, __fadd2_rn(get(x, e), make_float2(-up, -up)));
+          if (any) {  // every product issued before this S has completed
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t v[16];
+              tmem_ld<16>(tO + 16 * c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+              tmem_st<16>(tO + 16 * c, v);
+            }
+          }
+          if (h) {
+            tmem_wait_st();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[16];
+              tmem_ld<16>(tS + 16 * c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 w = __half22float2(u32_as_h2(v[e]));
+                v[e] = h2_as_u32(__floats2half2_rn(w.x * al, w.y * al));
+              }
+              tmem_st<16>(tS + 16 * c, v);
+            }
+          }
+        }
 
-      // weights, their sum, and P in fp16 over the first half of S
-      float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        // weights, their sum, and P in fp16
+        const float2 nR2 = make_float2(-R, -R), kf2 = make_float2(kfac, kfac);
+        float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float2 y0 = get(x, 32 * c + 2 * e), y1 = get(x, 32 * c + 2 * e + 2);
-          const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-          l2[0] = __fadd2_rn(l2[0], p0);
-          l2[1] = __fadd2_rn(l2[1], p1);
-          p[e] = h2_as_u32(__floats2half2_rn(p0.x, p0.y));
-          p[e + 1] = h2_as_u32(__floats2half2_rn(p1.x, p1.y));
+          for (int e = 0; e < 16; e += 2) {
+            float2 y0 = get(x, 32 * c + 2 * e), y1 = get(x, 32 * c + 2 * e + 2);
+            if constexpr (RAW) {
+              y0 = __ffma2_rn(y0, kf2, nR2);
+              y1 = __ffma2_rn(y1, kf2, nR2);
+            }
+            float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+            l2[0] = __fadd2_rn(l2[0], p0);
+            l2[1] = __fadd2_rn(l2[1], p1);
+            if constexpr (PT) {
+              const float4 f = *reinterpret_cast<const float4*>(vs + 32 * c + 2 * e);
+              if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
+                p0.x = y0.x == -INFINITY ? 0.0f : p0.x * f.x;
+                p0.y = y0.y == -INFINITY ? 0.0f : p0.y * f.y;
+                p1.x = y1.x == -INFINITY ? 0.0f : p1.x * f.z;
+                p1.y = y1.y == -INFINITY ? 0.0f : p1.y * f.w;
+              } else {
+                p0 = __fmul2_rn(p0, make_float2(f.x, f.y));
+                p1 = __fmul2_rn(p1, make_float2(f.z, f.w));
+              }
+            }
+            p[e] = h2_as_u32(__floats2half2_rn(p0.x, p0.y));
+            p[e + 1] = h2_as_u32(__floats2half2_rn(p1.x, p1.y));
+          }
+          tmem_st<16>(tS + 32 * h + 16 * c, p);
         }
-        tmem_st<16>(tS + 16 * c, p);
-      }
-      const float2 ls = __fadd2_rn(l2[0], l2[1]);
-      l = fmaf(ls.x + ls.y, PT ? ex2(-C) : 1.0f, l);
-      if (move && any) {  // every product issued before this S has completed
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tm_ld(tO + 32 * c, v);
-          tm_wait(v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-          tmem_st<32>(tO + 32 * c, v);
-        }
+        const float2 ls = __fadd2_rn(l2[0], l2[1]);
+        l += ls.x + ls.y;
       }
       any = true;
       tmem_wait_st();
