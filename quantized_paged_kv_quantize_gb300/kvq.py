@@ -167,12 +167,18 @@ def _take(t, name: str, cache: "KVCache", dtype, shape, dense: bool = True):
     """The data pointer of tensor `t`, which must have this dtype and shape
     (None: any size), lie on the cache's device, and be contiguous -- or, when
     not `dense`, have contiguous trailing dimensions (a row of a wider tensor)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.device:
+        return t.data_ptr()
+    return _take_slowly(t, name, cache, dtype, shape, dense)
+
+
+def _take_slowly(t, name, cache, dtype, shape, dense):
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     have = t.shape
     if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
         raise ValueError(f"{name}: shape {tuple(have)}, expected {tuple('*' if w is None else w for w in shape)}")
-    if t.device != cache.pool.device:
+    if t.get_device() != cache.device:
         raise ValueError(f"{name}: on {t.device}, the cache is on {cache.pool.device}")
     if not t.is_contiguous():
         if dense:
@@ -185,8 +191,14 @@ def _take(t, name: str, cache: "KVCache", dtype, shape, dense: bool = True):
     return t.data_ptr()
 
 
-def _io_torch(cache: "KVCache"):
-    return torch.float16 if cache.cfg.io_dtype == KVQ_F16 else torch.float32
+_FLOATS = {torch.float16: KVQ_F16, torch.float32: KVQ_F32}
+# the current stream's handle by device index (the public call builds a Stream object around it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream_of(cache: "KVCache", stream) -> Optional[int]:
+    return _raw_stream(cache.device) if stream is None else _stream(stream)
 
 
 def make_config(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, mode,
@@ -241,6 +253,9 @@ class KVCache:
         self.cfg = cfg
         self.pool = pool
         self.handle = handle
+        self.device = pool.get_device()
+        self.io_dtype = torch.float16 if cfg.io_dtype == KVQ_F16 else torch.float32
+        self.heads, self.head_dim = cfg.num_kv_heads, cfg.head_dim
 
     @property
     def mode(self) -> int:
@@ -425,12 +440,14 @@ def kvq_cache_read(cache: "KVCache", slot_mapping, k_out=None, v_out=None, *, st
     out = k_out if k_out is not None else v_out
     if out is None:
         raise ValueError("k_out and v_out are both None")
-    n = slot_mapping.shape[0]
-    shape = (n, cache.cfg.num_kv_heads, cache.cfg.head_dim)
-    k = None if k_out is None else _take(k_out, "k_out", cache, out.dtype, shape)
-    v = None if v_out is None else _take(v_out, "v_out", cache, out.dtype, shape)
-    _check(_lib.kvq_cache_read(cache.handle, _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,)), n, k, v,
-                               _dtype_code(out.dtype), _stream(stream)))
+    n, dt = slot_mapping.shape[0], out.dtype
+    if dt not in _FLOATS:
+        raise ValueError(f"k_out: dtype {dt}, expected float16 or float32")
+    shape = (n, cache.heads, cache.head_dim)
+    _check(_lib.kvq_cache_read(cache.handle, _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,)), n,
+                               None if k_out is None else _take(k_out, "k_out", cache, dt, shape),
+                               None if v_out is None else _take(v_out, "v_out", cache, dt, shape),
+                               _FLOATS[dt], _stream_of(cache, stream)))
 
 
 def kvq_norm_rope_write(cache: "KVCache", q, k, v, positions, cos_sin, q_out, *, slot_mapping=None, k_out=None,
@@ -442,31 +459,26 @@ def kvq_norm_rope_write(cache: "KVCache", q, k, v, positions, cos_sin, q_out, *,
     once into q_out (and k_out); with slot_mapping, k and v [n][Hkv][D] are
     quantized into the cache.  q, k and v may be slices of one projection's
     rows (any token stride that is a multiple of 16 bytes)."""
-    c, dt = cache.cfg, _io_torch(cache)
-    n, Hq, D = q.shape[0], q.shape[1], c.head_dim
-    r = NormRope()
-    r.q = _take(q, "q", cache, dt, (n, Hq, D), dense=False)
-    r.k = _take(k, "k", cache, dt, (n, c.num_kv_heads, D), dense=False)
-    r.q_stride, r.k_stride = (t.stride(0) if n > 1 else t.shape[1] * D for t in (q, k))
-    if v is not None:
-        r.v = _take(v, "v", cache, dt, (n, c.num_kv_heads, D), dense=False)
-        r.v_stride = v.stride(0) if n > 1 else c.num_kv_heads * D
+    dt, H, D = cache.io_dtype, cache.heads, cache.head_dim
+    n, Hq = q.shape[0], q.shape[1]
+    qs, ks, vs = (n, Hq, D), (n, H, D), (n,)
+    rot, positions_max = 0, 0
     if cos_sin is not None:
-        r.positions = _take(positions, "positions", cache, torch.int32, (n,))
-        r.cos_sin = _take(cos_sin, "cos_sin", cache, torch.float32, (None, None))
-        r.max_position, r.rot_dim = cos_sin.shape
-    if q_weight is not None:
-        r.q_weight = _take(q_weight, "q_weight", cache, dt, (D,))
-    if k_weight is not None:
-        r.k_weight = _take(k_weight, "k_weight", cache, dt, (D,))
-    if slot_mapping is not None:
-        r.slot_mapping = _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,))
-    r.q_out = _take(q_out, "q_out", cache, dt, (n, Hq, D))
-    if k_out is not None:
-        r.k_out = _take(k_out, "k_out", cache, dt, (n, c.num_kv_heads, D))
-    r.num_tokens, r.num_q_heads, r.interleaved, r.eps = n, Hq, int(interleaved), eps
-    _check(_lib.kvq_norm_rope_write(cache.handle, ctypes.byref(r), cache.mode if mode is None else _mode(mode),
-                                    _stream(stream)))
+        positions_max, rot = cos_sin.shape
+    r = NormRope(
+        _take(q, "q", cache, dt, qs, False), _take(k, "k", cache, dt, ks, False),
+        None if v is None else _take(v, "v", cache, dt, ks, False),
+        q.stride(0) if n > 1 else Hq * D, k.stride(0) if n > 1 else H * D,
+        v.stride(0) if v is not None and n > 1 else H * D,
+        None if cos_sin is None else _take(positions, "positions", cache, torch.int32, vs),
+        None if cos_sin is None else _take(cos_sin, "cos_sin", cache, torch.float32, (positions_max, rot)),
+        None if q_weight is None else _take(q_weight, "q_weight", cache, dt, (D,)),
+        None if k_weight is None else _take(k_weight, "k_weight", cache, dt, (D,)),
+        None if slot_mapping is None else _take(slot_mapping, "slot_mapping", cache, torch.int32, vs),
+        _take(q_out, "q_out", cache, dt, qs), None if k_out is None else _take(k_out, "k_out", cache, dt, ks),
+        n, Hq, rot, positions_max, interleaved, eps)
+    _check(_lib.kvq_norm_rope_write(cache.handle, ctypes.byref(r), cache.cfg.mode if mode is None else _mode(mode),
+                                    _stream_of(cache, stream)))
 
 
 # ---- chunk attention
@@ -486,20 +498,25 @@ def kvq_chunk_attention(cache: "KVCache", q, cu_q_lens, block_table, seq_lens, o
     """q, out [total_q][Hq][D]: sequence b's queries are rows cu_q_lens[b] ..
     cu_q_lens[b + 1] - 1, the last of its seq_lens[b] tokens; causal, with an
     optional score cap, distance bias (slopes fp32 [Hq]), window and bidirectional
-    prefix (int32 [B])."""
-    total, Hq, D = q.shape
-    B = seq_lens.shape[0]
+    prefix (int32 [B]).  block_table: int32 [B][max_pages]."""
+    shape, i32 = q.shape, torch.int32
+    total, Hq, D = shape
+    B, pages = block_table.shape
+    odt = out.dtype
+    if odt not in _FLOATS:
+        raise ValueError(f"out: dtype {odt}, expected float16 or float32")
     opt = None
-    if logit_cap != 0.0 or alibi_slopes is not None or window != 0 or prefix_lens is not None:
+    if logit_cap != 0.0 or window != 0 or alibi_slopes is not None or prefix_lens is not None:
         opt = ctypes.byref(AttentionOptions(
             logit_cap, window,
             None if alibi_slopes is None else _take(alibi_slopes, "alibi_slopes", cache, torch.float32, (Hq,)),
-            None if prefix_lens is None else _take(prefix_lens, "prefix_lens", cache, torch.int32, (B,))))
+            None if prefix_lens is None else _take(prefix_lens, "prefix_lens", cache, i32, (B,))))
+    if workspace is not None and workspace.get_device() != cache.device:
+        raise ValueError(f"workspace: on {workspace.device}, the cache is on {cache.pool.device}")
     _check(_lib.kvq_chunk_attention(
-        cache.handle, _take(q, "q", cache, _io_torch(cache), (None, None, cache.cfg.head_dim)), total,
-        _take(cu_q_lens, "cu_q_lens", cache, torch.int32, (B + 1,)),
-        _take(block_table, "block_table", cache, torch.int32, (B, None)), block_table.shape[1],
-        _take(seq_lens, "seq_lens", cache, torch.int32, (B,)), B, Hq, max_q_len, max_seq_len,
-        cache.mode if mode is None else _mode(mode), D ** -0.5 if softmax_scale is None else softmax_scale, opt,
-        _take(out, "out", cache, out.dtype, (total, Hq, D)), _dtype_code(out.dtype), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        cache.handle, _take(q, "q", cache, cache.io_dtype, (total, Hq, cache.head_dim)), total,
+        _take(cu_q_lens, "cu_q_lens", cache, i32, (B + 1,)), _take(block_table, "block_table", cache, i32, (B, pages)),
+        pages, _take(seq_lens, "seq_lens", cache, i32, (B,)), B, Hq, max_q_len, max_seq_len,
+        cache.cfg.mode if mode is None else _mode(mode), D ** -0.5 if softmax_scale is None else softmax_scale, opt,
+        _take(out, "out", cache, odt, shape), _FLOATS[odt], None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, _stream_of(cache, stream)))
