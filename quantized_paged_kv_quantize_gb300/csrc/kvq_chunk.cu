@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
 
   // packed words of tile i: thread's units u = tid + 128 r -> token u / J, channels 8 (u % J) ..
   Packed8 pk[U], pv[U];
-  float psc = 0.0f;  // per-token scale of token tid % KT, keys for tid < KT, values above
+  float psc = 0.0f;    // per-token scale of token tid % KT, keys for tid < KT, values above
+  bool there = false;  // that token is in the cache
   auto page_of = [&](int tok) -> int {  // the token's page, -1 past the sequence or out of the pool
     if (tok >= t.n || tr.unseen(tok >> 4)) return -1;
     const int pid = __ldg(a.block_table + (long long)t.seq * a.max_pages + (tok >> 4));
@@ -164,18 +165,17 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
         pv[r] = load_packed8<MODE, D, 1>(block(pid), tok & 15, j);
       }
     }
-    if constexpr (PT) {
-      psc = 0.0f;
-      if (tid < 2 * KT) {
-        const int tok = t0 + tid % KT, pid = page_of(tok);
-        if (pid >= 0)
+    psc = 0.0f;
+    if (tid < 2 * KT) {
+      const int tok = t0 + tid % KT, pid = page_of(tok);
+      there = pid >= 0;
+      if constexpr (PT) {
+        if (there)
           psc = __ldg(reinterpret_cast<const float*>(block(pid) + (MODE == KVQ_INT4_PER_TOKEN_HEAD ? 16 * D : 32 * D) +
                                                      (tid < KT ? 0 : 64)) + (tok & 15));
       }
     }
   };
-  // missing pages inside the sequence are not seen either
-  auto present = [&](int tok) { return tok < t.n && page_of(tok) >= 0; };
 
   float o[D / 8][4];
 #pragma unroll
@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   for (int i = i0; i < i1; ++i) {
     const int t0 = tr.tile(i) * KT;
     __syncthreads();  // the previous tile has been read
-    // absent tokens of the tile (past the sequence, missing pages): a flag in the scales' place
 #pragma unroll
     for (int r = 0; r < U; ++r) {
       const int u = tid + kThreads * r, tok = u / J, j = u % J;
@@ -200,8 +199,8 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     if (tid < 2 * KT) {
       float* sc = tid < KT ? kscale : vscale;
       const int k = tid % KT;
-      // an absent token is marked by a negative key scale
-      sc[k] = tid < KT ? (present(t0 + k) ? (PT ? psc : 1.0f) : -1.0f) : (PT ? psc : 1.0f);
+      // an absent token (past the sequence, a missing page) is marked by a negative key scale
+      sc[k] = tid < KT && !there ? -1.0f : PT ? psc : 1.0f;
       if constexpr (PT) {
         if (tid >= KT) {  // whole warps
           const int e = __reduce_max_sync(kFull, psc > 0.0f ? exponent(psc) : -100);
@@ -323,11 +322,12 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   }
 }
 
-// Merge of the splits: a warp per row (query x head) of a row tile, D / 32
-// channels a lane.  A split without tokens has m = -inf, and its partial is not
-// read into the sum.
+// Merge of the splits: a warp per row (query x head) of a row tile (8 rows a CTA),
+// D / 32 channels a lane, eight partials in flight.  A split without tokens has
+// m = -inf, and its partial is not read.
+constexpr int kCombineRows = 8;
 template <int D>
-__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int rows) {
+__global__ void __launch_bounds__(32 * kCombineRows) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int rows) {
   constexpr int C = D / 32;
   __shared__ RowTile tile_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y;
@@ -338,35 +338,41 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
   }
   __syncthreads();
   const RowTile t = tile_s;
-  if (t.seq < 0) return;
-  for (int r = warp; r < t.count; r += 8) {
-    const int rr = t.r0 + r;
-    const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
-    const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
-    const float2 v = lane < a.num_splits ? ml[lane] : make_float2(-INFINITY, 0.0f);  // at most 32 splits
-    const float M = warp_max_xor(v.x, 1, 16);
-    const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
-    float L = v.y * w;
+  const int r = blockIdx.z * kCombineRows + warp;
+  if (t.seq < 0 || r >= t.count) return;
+  const int rr = t.r0 + r;
+  const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+  const float2 v = lane < a.num_splits ? reinterpret_cast<const float2*>(a.ws_ml)[row * a.num_splits + lane]
+                                       : make_float2(-INFINITY, 0.0f);  // at most 32 splits
+  const float M = warp_max_xor(v.x, 1, 16);
+  const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
+  float L = v.y * w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
-    float acc[C];
+  for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+  float acc[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-    for (int s = 0; s < a.num_splits; ++s) {
-      const float ws = __shfl_sync(kFull, w, s);
-      if (ws == 0.0f) continue;
-      const float* src = a.ws_o + (row * a.num_splits + s) * D + C * lane;
+  for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+  for (int s0 = 0; s0 < a.num_splits; s0 += 8) {
+    float x[8][C], ws[8];
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += ws * src[c];
+    for (int u = 0; u < 8; ++u) {
+      ws[u] = __shfl_sync(kFull, w, (s0 + u) & 31);  // (zero past the splits)
+      const float* src = a.ws_o + (row * a.num_splits + s0 + u) * D + C * lane;
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[u][c] = s0 + u < a.num_splits && ws[u] != 0.0f ? src[c] : 0.0f;
     }
-    const float f = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float x = L > 0.0f ? acc[c] * f : 0.0f;
-      const long long at = row * D + C * lane + c;
-      if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
-      else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);
-    }
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += ws[u] * x[u][c];
+  }
+  const float f = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const float x = L > 0.0f ? acc[c] * f : 0.0f;
+    const long long at = row * D + C * lane + c;
+    if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
+    else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);
   }
 }
 
@@ -387,10 +393,10 @@ cudaError_t launch_mma(int mode, const ChunkArgs& a, dim3 grid, cudaStream_t s) 
 }  // namespace
 
 cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream) {
-  const dim3 grid((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, rows), a.Hkv);
+  const int most = (int)std::min<long long>(rows, (long long)a.max_q_len * a.G);  // rows of a tile
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, rows), a.Hkv, (most + kCombineRows - 1) / kCombineRows);
+  cfg.blockDim = dim3(32 * kCombineRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -402,13 +408,10 @@ cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int row
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The tcgen05 kernel takes fp16 in and out at head_dim 128; its variant goes by
-// the longest chunk: up to 128 rows per kv head leave half of a 256-row CTA
-// empty, so those run as 128 rows and two streams of tokens.
+// The tcgen05 kernel takes fp16 in and out at head_dim 128.
 bool chunk_on_umma(const kvq_cache* c, int out_dtype) {
   return c->cfg.head_dim == 128 && c->cfg.io_dtype == KVQ_F16 && out_dtype == KVQ_F16;
 }
-int umma_streams(int max_q_len, int G) { return (long long)max_q_len * G <= umma_chunk_rows(2) ? 2 : 1; }
 
 // Splits of the token ranges, and the workspace.  The lengths are on the device:
 // every tile of rows is taken to see max_seq_len tokens (a window bounds what
@@ -430,9 +433,9 @@ ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_he
     return p;
   }
   const bool umma = chunk_on_umma(c, KVQ_F16);
-  const int streams = umma_streams(max_q_len, G);
-  const int rows = umma ? umma_chunk_rows(streams) : kRows;
-  const int kt = umma ? 128 * streams : kTile<32>;       // tokens a CTA takes at a time
+  const int rows = umma ? kUmmaRows : kRows;
+  // tokens a CTA takes at a time: the tcgen05 kernel runs two tiles at once for up to 128 rows
+  const int kt = !umma ? kTile<32> : (long long)max_q_len * G <= 128 ? 256 : 128;
   const long long slots = (umma ? 1ll : 4ll) * num_sms();  // CTAs side by side
   constexpr long long kCost = 4;                         // start-up, merge and partials of a CTA, in such tiles
   long long len = max_seq_len;
@@ -491,10 +494,9 @@ cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkC
   uint8_t* w = static_cast<uint8_t*>(k.workspace);
   a.ws_span = Span{w, w ? w + plan.workspace_bytes : nullptr};
   if (chunk_on_umma(c, k.out_dtype)) {
-    const int streams = umma_streams(a.max_q_len, a.G);
-    cudaError_t e = launch_chunk_umma(c, a, streams, stream);
+    cudaError_t e = launch_chunk_umma(c, a, stream);
     if (e != cudaSuccess || a.num_splits == 1) return e;
-    return launch_chunk_combine(c, a, umma_chunk_rows(streams), stream);
+    return launch_chunk_combine(c, a, kUmmaRows, stream);
   }
   const dim3 grid((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, kRows), a.Hkv, a.num_splits);
   const bool qf32 = c->cfg.io_dtype == KVQ_F32;

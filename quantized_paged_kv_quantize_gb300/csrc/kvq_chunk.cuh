@@ -34,6 +34,7 @@ struct ChunkArgs {
 struct RowTile {
   int seq;       // -1: no such tile
   int q0, m, n;  // first query row of the chunk, its queries, the sequence's tokens
+  int prefix;    // tokens that every query of the sequence sees
   int r0, count;
 };
 
@@ -50,19 +51,26 @@ inline long long chunk_tile_bound(int total_q, int B, int G, int rows) {
 // no tiles; a seq_len outside its bounds is flagged and clamped.
 __device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int rows, bool flag) {
   const int lane = threadIdx.x & 31;
-  RowTile t{-1, 0, 0, 0, 0, 0};
+  RowTile t{-1, 0, 0, 0, 0, 0, 0};
+  const int lim = (int)min((long long)a.max_seq_len, (long long)a.max_pages * 16);
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    int q0 = 0, m = 0, tiles = 0;
-    if (b < a.B) {
+    int q0 = 0, m = 0, tiles = 0, n = 0, prefix = 0;
+    if (b < a.B) {  // (all loads at once)
       q0 = __ldg(a.cu_q + b);
       const int q1 = __ldg(a.cu_q + b + 1);
+      n = __ldg(a.seq_lens + b);
+      if (a.prefix_lens) prefix = __ldg(a.prefix_lens + b);
       if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > a.max_q_len) {
         if (flag) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_QUERY_RANGE);
       } else {
         m = q1 - q0;
         tiles = (int)(((long long)m * a.G + rows - 1) / rows);
+      }
+      if (n > lim || n < 0) {
+        if (flag && m > 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
+        n = n < 0 ? 0 : lim;
       }
     }
     int upto = tiles;  // inclusive prefix sum over the warp
@@ -73,26 +81,19 @@ __device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int 
     }
     const bool mine = index >= before + upto - tiles && index < before + upto;
     const uint32_t who = __ballot_sync(0xffffffffu, mine);
-    if (who) {
+    if (who && t.seq < 0) {
       const int src = __ffs(who) - 1;
       t.seq = b0 + src;
       t.q0 = __shfl_sync(0xffffffffu, q0, src);
       t.m = __shfl_sync(0xffffffffu, m, src);
+      t.n = __shfl_sync(0xffffffffu, n, src);
+      t.prefix = max(0, min(__shfl_sync(0xffffffffu, prefix, src), t.n));
       const int k = before + __shfl_sync(0xffffffffu, upto, src) - 1 - index;  // from the chunk's first rows
       t.r0 = k * rows;
       t.count = (int)min((long long)rows, (long long)t.m * a.G - t.r0);
-      break;
+      if (!flag) break;  // (a flagging warp looks at every sequence)
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  if (t.seq >= 0) {
-    int n = __ldg(a.seq_lens + t.seq);
-    const int lim = (int)min((long long)a.max_seq_len, (long long)a.max_pages * 16);
-    if (n > lim || n < 0) {
-      if (flag && lane == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
-      n = n < 0 ? 0 : lim;
-    }
-    t.n = n;
   }
   return t;
 }
@@ -114,7 +115,7 @@ __device__ __forceinline__ TokenRange token_range(const ChunkArgs& a, const RowT
   TokenRange r;
   r.p_min = t.n - t.m + t.r0 / a.G;
   r.p_max = t.n - t.m + (t.r0 + t.count - 1) / a.G;
-  r.prefix = a.prefix_lens ? max(0, min(__ldg(a.prefix_lens + t.seq), t.n)) : 0;
+  r.prefix = t.prefix;
   r.lowest = a.window > 0 ? max(0, max(r.p_min, 0) - a.window + 1) : 0;
   if (r.p_max < 0) {  // more queries than tokens: these see nothing
     r.first = r.second = r.tiles = 0;
@@ -146,8 +147,7 @@ __device__ __forceinline__ RowSees row_sees(const ChunkArgs& a, const TokenRange
 cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream);
 
 // The tcgen05 kernel (kvq_chunk_umma.cu): rows of a CTA, and the launch.
-// streams 1: 256 rows; 2: 128 rows and two streams of token tiles.
-constexpr int umma_chunk_rows(int streams) { return streams == 1 ? 256 : 128; }
-cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, int streams, cudaStream_t s);
+constexpr int kUmmaRows = 256;
+cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, cudaStream_t s);
 
 }  // namespace kvq

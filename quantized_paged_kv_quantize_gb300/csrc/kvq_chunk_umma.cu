@@ -26,10 +26,10 @@
 //                  MN-major B operand of P V;
 //  warp 12         issues the tcgen05.mma (13-15 only fill its warpgroup).
 // Two blocks are in work at a time, so that the tensor cores run one block's
-// products during the other's softmax:
-//  STREAMS = 1     256 rows; both blocks use the same tile of keys and values;
-//  STREAMS = 2     128 rows; even and odd tiles are two streams with a reference,
-//                  sum and accumulator each, merged at the end.
+// products during the other's softmax.  A CTA with more than 128 rows has two
+// blocks of rows that use the same tile of keys and values; one with fewer takes
+// even and odd tiles as two streams, with a reference, sum and accumulator each,
+// merged at the end.
 // Tensor memory: S_0 S_1 (128 columns each; P over the first 64 of S) O_0 O_1.
 #include <cuda_fp16.h>
 
@@ -55,10 +55,9 @@ constexpr int kSlots = 4;       // tiles whose scales are kept
 constexpr float kSlack = 8.0f;  // log2
 constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
 
-template <int STREAMS>
 struct Smem {
   static constexpr int Q = 0;
-  static constexpr int K = Q + (STREAMS == 1 ? 2 : 1) * kOpBytes;  // two stages each
+  static constexpr int K = Q + 2 * kOpBytes;  // two stages each
   static constexpr int V = K + 2 * kOpBytes;
   static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] key scales in log2 units
   static constexpr int VS = KS + kSlots * kTok * 4;                // [slot][128] value scales
@@ -267,14 +266,13 @@ __device__ __forceinline__ void store_page(const Words<MODE>& x, uint8_t* op, in
 
 // ---------------------------------------------------------------- kernel
 struct Bars {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full;
+  uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full;
 };
 
-template <int MODE, int STREAMS, bool OPT>
+template <int MODE, bool OPT>
 __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_constant__ ChunkArgs a) {
-  using L = Smem<STREAMS>;
+  using L = Smem;
   constexpr bool PT = kPerTokenScale<MODE>;
-  constexpr int ROWS = STREAMS == 1 ? 256 : 128;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   __shared__ Bars bar;
@@ -290,50 +288,42 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   const int kvh = blockIdx.x % a.Hkv, tile_index = blockIdx.x / a.Hkv, split = blockIdx.y;
   uint8_t* pool = const_cast<uint8_t*>(a.pool);
   if (warp == 0) {
-    const RowTile t = find_tile(a, tile_index, ROWS, tile_index == 0 && kvh == 0 && split == 0);
+    const RowTile t = find_tile(a, tile_index, kUmmaRows, tile_index == 0 && kvh == 0 && split == 0);
     if (lane == 0) tile_s = t;
+  } else if (warp == 1) {
+    if (elect_one()) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.k_full[i], 4);
+        mbar_init(&bar.v_full[i], 4);
+        mbar_init(&bar.k_free[i], 1);
+        mbar_init(&bar.v_free[i], 1);
+        mbar_init(&bar.s_full[i], 2);
+        mbar_init(&bar.p_full[i], 4);
+      }
+      mbar_init(&bar.q_full, 8);
+      mbar_init(&bar.o_full, 1);
+      failed_s = 0;
+      mbar_fence_init();
+    }
+    __syncwarp();
+  } else if (warp == kIssueWarp) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   const RowTile t = tile_s;
-  if (t.seq < 0) return;
+  if (t.seq < 0) {  // no such tile
+    if (warp == kIssueWarp) tmem_dealloc(tmem_s, 512);
+    return;
+  }
   const TokenRange tr = token_range(a, t, kTok);
   const int i0 = (int)((long long)tr.tiles * split / a.num_splits);
   const int n = (int)((long long)tr.tiles * (split + 1) / a.num_splits) - i0;  // this CTA's tiles,
   const int last = i0 + n - 1;  // taken from the last (the nearest tokens) to the first
-  const int items = STREAMS == 1 ? 2 * n : n;  // (tile, block) pairs; item k belongs to block k & 1
-
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], 4);
-      mbar_init(&bar.v_full[i], 4);
-      mbar_init(&bar.k_free[i], 1);
-      mbar_init(&bar.v_free[i], 1);
-      mbar_init(&bar.s_full[i], 2);
-      mbar_init(&bar.p_full[i], 4);
-    }
-    mbar_init(&bar.o_full, 1);
-    failed_s = 0;
-    mbar_fence_init();
-  }
-  if (warp == kIssueWarp) {
-    tmem_alloc(&tmem_s, 512);
-    tmem_relinquish();
-  }
-  // Q: row r's channel group c at (r % 8) 16 + c kLbo + (r / 8) kSbo; zero past the tile's rows
-  for (int it = tid; it < ROWS * 16; it += kThreads) {
-    const int r = it >> 4, c = it & 15;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < t.count) {
-      const int rr = t.r0 + r;
-      const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + row * kD) + c);
-    }
-    *reinterpret_cast<uint4*>(sm + L::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * kSbo) = x;
-  }
-  fence_proxy_async_smem();  // Q is read by the tensor core
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  const bool two = t.count <= 128;      // one block of rows, two streams of tiles
+  const int items = two ? n : 2 * n;  // (tile, block) pairs; item k belongs to block k & 1
   const uint32_t tb = tmem_s;
   bool ok = true;
 
@@ -443,10 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       // (after the products that read P from the same columns).  A second issuing
       // warp, one for each block, mixes the blocks' products and was slower
       // (2048 queries over 32768 nvfp4 tokens: 2.10 against 1.74 ms).
-      for (int k = -2; k < items; ++k) {
+      ok = wait(&bar.q_full, 0);
+      for (int k = -2; k < items && ok; ++k) {
         const int b = k & 1;
         if (k >= 0) {
-          const int i = STREAMS == 1 ? k >> 1 : k, st = i & 1;
+          const int i = two ? k : k >> 1, st = i & 1;
           ok = wait(&bar.v_full[st], (i >> 1) & 1) && ok;
           ok = wait(&bar.p_full[b], (k >> 1) & 1) && ok;
           if (!ok) break;
@@ -456,23 +447,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               umma_f16_ts(tb + 256 + 128 * b, tb + 128 * b + 8 * e, B + e * kStepV, kIdescPV, (k > 1 || e > 0) ? 1u : 0u);
-            if (STREAMS == 2 || b == 1) tc_commit(&bar.v_free[st]);
+            if (two || b == 1) tc_commit(&bar.v_free[st]);
             if (k + 1 == items) tc_commit(&bar.o_full);
           }
           __syncwarp();
         }
         if (k + 2 < items) {
-          const int i = STREAMS == 1 ? (k + 2) >> 1 : k + 2, st = i & 1;
+          const int i = two ? k + 2 : (k + 2) >> 1, st = i & 1;
           ok = wait(&bar.k_full[st], (i >> 1) & 1) && ok;
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t A = dq + (STREAMS == 1 ? b * kOp : 0), B = dk + st * kOp;
+            const uint64_t A = dq + (two ? 0 : b * kOp), B = dk + st * kOp;
 #pragma unroll
             for (int e = 0; e < 8; ++e) umma_f16_ss(tb + 128 * b, A + e * kStepK, B + e * kStepK, kIdescQK, e > 0 ? 1u : 0u);
             tc_commit(&bar.s_full[b]);
             mbar_arrive(&bar.s_full[b]);  // passes on the scales that came with the keys
-            if (STREAMS == 2 || b == 1) tc_commit(&bar.k_free[st]);
+            if (two || b == 1) tc_commit(&bar.k_free[st]);
           }
           __syncwarp();
         }
@@ -483,13 +474,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int blk = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const int row = STREAMS == 1 ? tid : (tid & 127);
+    // Q: row r's channel group c at (r % 8) 16 + c kLbo + (r / 8) kSbo; zero past the tile's rows
+    for (int it = tid; it < (two ? 128 : 256) * 16; it += 256) {
+      const int r = it >> 4, c = it & 15;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (r < t.count) {
+        const int rr = t.r0 + r;
+        const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + row * kD) + c);
+      }
+      *reinterpret_cast<uint4*>(sm + L::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * kSbo) = x;
+    }
+    fence_proxy_async_smem();  // Q is read by the tensor core
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.q_full);
+    const int row = two ? (tid & 127) : tid;
     const bool real = row < t.count;
     const int rr = t.r0 + (real ? row : 0);
     const int pos = t.n - t.m + rr / a.G;
     // the block's own positions decide which tiles need a mask
     TokenRange mine = tr;
-    if (STREAMS == 1) {
+    if (!two) {
       mine.p_min = t.n - t.m + (t.r0 + 128 * blk) / a.G;
       mine.p_max = t.n - t.m + (t.r0 + min(t.count - 1, 128 * blk + 127)) / a.G;
     }
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
     bool any = false;   // the block has accumulated something
 
     for (int k = blk; k < items; k += 2) {
-      const int i = STREAMS == 1 ? k >> 1 : k, slot = i & (kSlots - 1);
+      const int i = two ? k : k >> 1, slot = i & (kSlots - 1);
       ok = wait(&bar.s_full[blk], (k >> 1) & 1) && ok;
       if (!__all_sync(kFull, ok)) {
         ok = false;
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       if (tid == 0) set_error(pool, KVQ_DEVERR_TIMEOUT);
     } else {
       if (fresh) R = -1e30f;
-      if constexpr (STREAMS == 2) {
+      if (two) {
         if (blk == 1) {
           float* o = other + row * kStride;
 #pragma unroll
@@ -705,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           R = top;
         }
       }
-      if ((STREAMS == 1 || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
+      if ((!two || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
         const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
         const float g = a.num_splits > 1 ? vfac : l > 0.0f ? vfac / l : 0.0f;
         const long long pi = qrow * a.num_splits + split;
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(v[e]) * f0 : 0.0f;
-          if constexpr (STREAMS == 2) {
+          if (two) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 u = *reinterpret_cast<const float4*>(other + row * kStride + 32 * c + e);
@@ -756,37 +761,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   if (warp == kIssueWarp) tmem_dealloc(tb, 512);
 }
 
-template <int MODE, int STREAMS, bool OPT>
+template <int MODE, bool OPT>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
-  auto kern = chunk_umma_kernel<MODE, STREAMS, OPT>;
-  constexpr size_t smem = Smem<STREAMS>::dynamic();
+  auto kern = chunk_umma_kernel<MODE, OPT>;
+  constexpr size_t smem = Smem::dynamic();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const long long tiles = chunk_tile_bound(a.total_q, a.B, a.G, umma_chunk_rows(STREAMS));
+  const long long tiles = chunk_tile_bound(a.total_q, a.B, a.G, kUmmaRows);
   kern<<<dim3((unsigned)(tiles * a.Hkv), a.num_splits), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int STREAMS, bool OPT>
+template <bool OPT>
 cudaError_t launch_mode(int mode, const ChunkArgs& a, cudaStream_t s) {
   switch (mode) {
-    case KVQ_FP8_PER_TENSOR: return launch<KVQ_FP8_PER_TENSOR, STREAMS, OPT>(a, s);
-    case KVQ_INT8_PER_TOKEN_HEAD: return launch<KVQ_INT8_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
-    case KVQ_FP8_PER_TOKEN_HEAD: return launch<KVQ_FP8_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
+    case KVQ_FP8_PER_TENSOR: return launch<KVQ_FP8_PER_TENSOR, OPT>(a, s);
+    case KVQ_INT8_PER_TOKEN_HEAD: return launch<KVQ_INT8_PER_TOKEN_HEAD, OPT>(a, s);
+    case KVQ_FP8_PER_TOKEN_HEAD: return launch<KVQ_FP8_PER_TOKEN_HEAD, OPT>(a, s);
     case KVQ_NVFP4:
-    case KVQ_NVFP4_4OVER6: return launch<KVQ_NVFP4, STREAMS, OPT>(a, s);
-    case KVQ_INT4_PER_TOKEN_HEAD: return launch<KVQ_INT4_PER_TOKEN_HEAD, STREAMS, OPT>(a, s);
+    case KVQ_NVFP4_4OVER6: return launch<KVQ_NVFP4, OPT>(a, s);
+    case KVQ_INT4_PER_TOKEN_HEAD: return launch<KVQ_INT4_PER_TOKEN_HEAD, OPT>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, int streams, cudaStream_t s) {
-  const bool opt = a.cap > 0.0f || a.slopes != nullptr;
-  const int mode = c->cfg.mode;
-  if (streams == 1) return opt ? launch_mode<1, true>(mode, a, s) : launch_mode<1, false>(mode, a, s);
-  return opt ? launch_mode<2, true>(mode, a, s) : launch_mode<2, false>(mode, a, s);
+cudaError_t launch_chunk_umma(const kvq_cache* c, const ChunkArgs& a, cudaStream_t s) {
+  return a.cap > 0.0f || a.slopes ? launch_mode<true>(c->cfg.mode, a, s) : launch_mode<false>(c->cfg.mode, a, s);
 }
 
 }  // namespace kvq

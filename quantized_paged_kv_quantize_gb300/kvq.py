@@ -167,7 +167,8 @@ def _take(t, name: str, cache: "KVCache", dtype, shape, dense: bool = True):
     """The data pointer of tensor `t`, which must have this dtype and shape
     (None: any size), lie on the cache's device, and be contiguous -- or, when
     not `dense`, have contiguous trailing dimensions (a row of a wider tensor)."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.device:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cache.device and (
+            t.is_contiguous() or (not dense and t.stride()[1:] == (shape[2], 1))):
         return t.data_ptr()
     return _take_slowly(t, name, cache, dtype, shape, dense)
 
