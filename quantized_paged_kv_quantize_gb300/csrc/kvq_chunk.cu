@@ -322,12 +322,13 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   }
 }
 
-// Merge of the splits: a warp per row (query x head) of a row tile (8 rows a CTA),
-// D / 32 channels a lane, eight partials in flight.  A split without tokens has
-// m = -inf, and its partial is not read.
-constexpr int kCombineRows = 8;
+// Merge of the splits: a warp per row (query x head) of a row tile, D / 32 channels
+// a lane, eight partials in flight.  A split without tokens has m = -inf, and its
+// partial is not read.  A CTA takes `span` rows: eight, or more where there are
+// many rows, to find its tile once for them.
+constexpr int kCombineWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(32 * kCombineRows) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int rows) {
+__global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const __grid_constant__ ChunkArgs a, int rows, int span) {
   constexpr int C = D / 32;
   __shared__ RowTile tile_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kvh = blockIdx.y;
@@ -338,41 +339,43 @@ __global__ void __launch_bounds__(32 * kCombineRows) chunk_combine_kernel(const 
   }
   __syncthreads();
   const RowTile t = tile_s;
-  const int r = blockIdx.z * kCombineRows + warp;
-  if (t.seq < 0 || r >= t.count) return;
-  const int rr = t.r0 + r;
-  const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
-  const float2 v = lane < a.num_splits ? reinterpret_cast<const float2*>(a.ws_ml)[row * a.num_splits + lane]
-                                       : make_float2(-INFINITY, 0.0f);  // at most 32 splits
-  const float M = warp_max_xor(v.x, 1, 16);
-  const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
-  float L = v.y * w;
+  if (t.seq < 0) return;
+  const int end = min(t.count, ((int)blockIdx.z + 1) * span);
+  for (int r = blockIdx.z * span + warp; r < end; r += kCombineWarps) {
+    const int rr = t.r0 + r;
+    const long long row = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+    const float2 v = lane < a.num_splits ? reinterpret_cast<const float2*>(a.ws_ml)[row * a.num_splits + lane]
+                                         : make_float2(-INFINITY, 0.0f);  // at most 32 splits
+    const float M = warp_max_xor(v.x, 1, 16);
+    const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);
+    float L = v.y * w;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
-  float acc[C];
+    for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+    float acc[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-  for (int s0 = 0; s0 < a.num_splits; s0 += 8) {
-    float x[8][C], ws[8];
+    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+    for (int s0 = 0; s0 < a.num_splits; s0 += 8) {
+      float x[8][C], ws[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      ws[u] = __shfl_sync(kFull, w, (s0 + u) & 31);  // (zero past the splits)
-      const float* src = a.ws_o + (row * a.num_splits + s0 + u) * D + C * lane;
+      for (int u = 0; u < 8; ++u) {
+        ws[u] = __shfl_sync(kFull, w, (s0 + u) & 31);  // (zero past the splits)
+        const float* src = a.ws_o + (row * a.num_splits + s0 + u) * D + C * lane;
 #pragma unroll
-      for (int c = 0; c < C; ++c) x[u][c] = s0 + u < a.num_splits && ws[u] != 0.0f ? src[c] : 0.0f;
+        for (int c = 0; c < C; ++c) x[u][c] = s0 + u < a.num_splits && ws[u] != 0.0f ? src[c] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] += ws[u] * x[u][c];
     }
+    const float f = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += ws[u] * x[u][c];
-  }
-  const float f = L > 0.0f ? 1.0f / L : 0.0f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const float x = L > 0.0f ? acc[c] * f : 0.0f;
-    const long long at = row * D + C * lane + c;
-    if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
-    else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);
+    for (int c = 0; c < C; ++c) {
+      const float x = L > 0.0f ? acc[c] * f : 0.0f;
+      const long long at = row * D + C * lane + c;
+      if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
+      else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);
+    }
   }
 }
 
@@ -395,16 +398,17 @@ cudaError_t launch_mma(int mode, const ChunkArgs& a, dim3 grid, cudaStream_t s) 
 cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream) {
   const int most = (int)std::min<long long>(rows, (long long)a.max_q_len * a.G);  // rows of a tile
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, rows), a.Hkv, (most + kCombineRows - 1) / kCombineRows);
-  cfg.blockDim = dim3(32 * kCombineRows);
+  const int span = (long long)a.total_q * a.Hq >= 64ll * kCombineWarps * num_sms() ? 64 : kCombineWarps;
+  cfg.gridDim = dim3((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, rows), a.Hkv, (most + span - 1) / span);
+  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = c->cfg.head_dim == 128 ? cudaLaunchKernelEx(&cfg, chunk_combine_kernel<128>, a, rows)
-                                         : cudaLaunchKernelEx(&cfg, chunk_combine_kernel<32>, a, rows);
+  cudaError_t e = c->cfg.head_dim == 128 ? cudaLaunchKernelEx(&cfg, chunk_combine_kernel<128>, a, rows, span)
+                                         : cudaLaunchKernelEx(&cfg, chunk_combine_kernel<32>, a, rows, span);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -131,33 +131,61 @@ __device__ __forceinline__ void fwht128x8(float* v, int j) {
   for (int i = 0; i < 8; ++i) v[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
 }
 
-// KVarN: a group reads kKvTokens entries of the list for one head, keeping the
-// page's per-channel key factors (c scale, c zero) and value factors c in
-// registers while the page stays the same.
-constexpr int kKvTokens = 8;
+// KVarN: a group of 16 lanes reads kKvTokens entries of the list for one head,
+// keeping the page's per-channel key factors (c scale, c zero) and value factors c
+// in registers while the page stays the same.  The entries and every token's codes
+// and factors are loaded before the first token is transformed.
+constexpr int kKvTokens = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kvarn_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int D = 128, P = 128, TPR = D / kVec, GRP = kThreads / TPR;
   constexpr int META = P * D * 3 / 4;
-  const int g = threadIdx.x / TPR, j = threadIdx.x % TPR, h = blockIdx.y;
+  const int g = threadIdx.x / TPR, j = threadIdx.x % TPR, h = blockIdx.y, lane = threadIdx.x & 31;
   const long long t0 = ((long long)blockIdx.x * GRP + g) * kKvTokens;
+  int slot = -1;
+  if (j < kKvTokens && t0 + j < a.num_tokens) slot = __ldg(a.slots + t0 + j);
+  if (slot >= 0 && (slot >> 7) >= a.num_pages) {
+    if (h == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SLOT_RANGE);
+    slot = -1;
+  }
+  int sl[kKvTokens];
+  uint32_t kw[kKvTokens], vw[kKvTokens];
+  float kr[kKvTokens], vs[kKvTokens], vz[kKvTokens], vr[kKvTokens];
+  auto block = [&](int s) { return a.pool + kHeaderBytes + ((size_t)(s >> 7) * a.Hkv + h) * a.block_bytes; };
+#pragma unroll
+  for (int i = 0; i < kKvTokens; ++i) {
+    sl[i] = __shfl_sync(kFull, slot, (lane & 16) + i);
+    kw[i] = vw[i] = 0u;
+    kr[i] = vs[i] = vz[i] = vr[i] = 0.0f;
+    if (sl[i] >= 0) {
+      const uint8_t* blk = block(sl[i]);
+      const int off = sl[i] & 127;
+      const float* km = reinterpret_cast<const float*>(blk + META);
+      const float* vm = km + 3 * D + P;
+      if (a.k) {
+        kw[i] = __ldg(reinterpret_cast<const uint32_t*>(blk + off * (D / 2) + kVec / 2 * j));
+        kr[i] = __ldg(km + 3 * D + off);
+      }
+      if (a.v) {
+        vw[i] = __ldg(reinterpret_cast<const uint16_t*>(blk + P * D / 2 + off * (D / 4) + kVec / 4 * j));
+        vs[i] = __ldg(vm + off);
+        vz[i] = __ldg(vm + P + off);
+        vr[i] = __ldg(vm + 2 * P + off);
+      }
+    }
+  }
   int held = -1;
   float ks[8], kz[8], vc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ks[e] = kz[e] = vc[e] = 0.0f;
   // no early exit: every lane takes part in the transform's shuffles
+#pragma unroll
   for (int i = 0; i < kKvTokens; ++i) {
-    const long long token = t0 + i;
-    const int slot = token < a.num_tokens ? __ldg(a.slots + token) : -1;
-    const int page = slot >> 7, off = slot & 127;
-    bool on = slot >= 0;
-    if (on && page >= a.num_pages) {
-      if (j == 0 && h == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SLOT_RANGE);
-      on = false;
-    }
-    const uint8_t* blk = a.pool + kHeaderBytes + ((size_t)(on ? page : 0) * a.Hkv + h) * a.block_bytes;
-    const float* km = reinterpret_cast<const float*>(blk + META);
-    const float* vm = km + 3 * D + P;
-    if (on && page != held) {
-      held = page;
+    const bool on = sl[i] >= 0;
+    if (on && (sl[i] >> 7) != held) {
+      held = sl[i] >> 7;
+      const float* km = reinterpret_cast<const float*>(block(sl[i]) + META);
+      const float* vm = km + 3 * D + P;
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
         const int d = kVec * j + e;
@@ -169,22 +197,17 @@ __global__ void __launch_bounds__(kThreads) read_kvarn_kernel(const __grid_const
         vc[e] = u.x; vc[e + 1] = u.y; vc[e + 2] = u.z; vc[e + 3] = u.w;
       }
     }
-    const long long o = (token * a.Hkv + h) * D + kVec * j;
+    const long long o = ((t0 + i) * a.Hkv + h) * D + kVec * j;
     float f[8];
     if (a.k) {  // uniform
-      const uint32_t w = on ? __ldg(reinterpret_cast<const uint32_t*>(blk + off * (D / 2) + kVec / 2 * j)) : 0u;
-      const float r = on ? __ldg(km + 3 * D + off) : 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = on ? r * fmaf(ks[e], (float)((w >> (4 * e)) & 15u), kz[e]) : 0.0f;
+      for (int e = 0; e < 8; ++e) f[e] = kr[i] * fmaf(ks[e], (float)((kw[i] >> (4 * e)) & 15u), kz[e]);
       fwht128x8(f, j);
       if (on) store8<T>(static_cast<T*>(a.k) + o, f, a.k_span, a.pool);
     }
     if (a.v) {
-      const uint32_t w = on ? __ldg(reinterpret_cast<const uint16_t*>(blk + P * D / 2 + off * (D / 4) + kVec / 4 * j)) : 0u;
-      const float s = on ? __ldg(vm + off) : 0.0f, z = on ? __ldg(vm + P + off) : 0.0f;
-      const float r = on ? __ldg(vm + 2 * P + off) : 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = on ? r * vc[e] * fmaf(s, (float)((w >> (2 * e)) & 3u), z) : 0.0f;
+      for (int e = 0; e < 8; ++e) f[e] = vr[i] * vc[e] * fmaf(vs[i], (float)((vw[i] >> (2 * e)) & 3u), vz[i]);
       fwht128x8(f, j);
       if (on) store8<T>(static_cast<T*>(a.v) + o, f, a.v_span, a.pool);
     }
