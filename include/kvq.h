@@ -353,9 +353,14 @@ kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int
  * block_table, max_pages, seq_lens, max_seq_len, mode, softmax_scale and the
  * workspace are as for kvq_decode_attention, as is the rule for the head group.
  * A sequence's pages hold its queries' own tokens too (write them first).
+ * Pages that lie wholly below every window (and past the prefix) are not read,
+ * and their block_table entries not looked at.  Calls that may overlap on the
+ * GPU need a workspace each.
+ * At head_dim 128 with fp16 in and out the weights are rounded to fp16 before
+ * they meet the values; other combinations carry them to 2^-22.
  * KVarN is not supported (KVQ_ERR_UNSUPPORTED): its open tile lies outside the
- * pages.  A NaN stored as a value (an E4M3 NaN code) may reach the outputs of
- * every query of its sequence's chunk. */
+ * pages.  A token whose stored value codes or scale are not finite may make every
+ * output of its sequence's chunk NaN, those of queries before it too. */
 kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_q, const int32_t* cu_q_lens,
                                const int32_t* block_table, int max_pages, const int32_t* seq_lens, int num_seqs,
                                int num_q_heads, int max_q_len, int max_seq_len, int mode, float softmax_scale,

@@ -528,6 +528,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_
   s = check_decode_args(cache, q, block_table, max_pages, seq_lens, total_q == 0 ? 0 : num_seqs, num_q_heads,
                         max_seq_len, softmax_scale, out, out_dtype, false, nullptr, &empty);
   if (s || empty) return s;
+  if (max_q_len == 0) return fail(KVQ_ERR_INVALID_ARG, "max_q_len is 0 but there are query rows");
   if (!cu_q_lens || !aligned(cu_q_lens, 4))
     return fail(KVQ_ERR_INVALID_ARG, "cu_q_lens must be non-NULL and 4-byte aligned");
   if (options && (!aligned(options->alibi_slopes, 4) || !aligned(options->prefix_lens, 4)))

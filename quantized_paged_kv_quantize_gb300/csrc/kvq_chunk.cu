@@ -302,11 +302,11 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     if (!real[u]) continue;
     const float f = PT ? pow2(vexp) : vfac;
     if (a.num_splits == 1) {
-      const float r = l[u] > 0.0f ? f / l[u] : 0.0f;
+      const float r = f / l[u];  // (a NaN score makes its row NaN; no token seen: 0)
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
         const long long at = qrow[u] * D + 8 * n + 2 * tq;
-        const float x = l[u] > 0.0f ? o[n][2 * u] * r : 0.0f, y = l[u] > 0.0f ? o[n][2 * u + 1] * r : 0.0f;
+        const float x = l[u] == 0.0f ? 0.0f : o[n][2 * u] * r, y = l[u] == 0.0f ? 0.0f : o[n][2 * u + 1] * r;
         if (a.out_f32) st_chk(reinterpret_cast<float2*>(static_cast<float*>(a.out) + at), make_float2(x, y), a.out_span, a.pool);
         else st_chk(reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at), __floats2half2_rn(x, y), a.out_span, a.pool);
       }
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
       for (int n = 0; n < D / 8; ++n)
         st_chk(reinterpret_cast<float2*>(a.ws_o + pi * D + 8 * n + 2 * tq), make_float2(o[n][2 * u] * f, o[n][2 * u + 1] * f),
                a.ws_span, a.pool);
-      if (tq == 0) st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l[u] > 0.0f ? m[u] : -INFINITY, l[u]),
+      if (tq == 0) st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l[u] == 0.0f ? -INFINITY : m[u], l[u]),
                           a.ws_span, a.pool);
     }
   }
@@ -368,10 +368,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] += ws[u] * x[u][c];
     }
-    const float f = L > 0.0f ? 1.0f / L : 0.0f;
+    const float f = 1.0f / L;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float x = L > 0.0f ? acc[c] * f : 0.0f;
+      const float x = L == 0.0f ? 0.0f : acc[c] * f;
       const long long at = row * D + C * lane + c;
       if (a.out_f32) st_chk(static_cast<float*>(a.out) + at, x, a.out_span, a.pool);
       else st_chk(static_cast<__half*>(a.out) + at, __float2half_rn(x), a.out_span, a.pool);

@@ -76,7 +76,7 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd
       "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, 1u << 18); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, 1u << 20); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       }
       if ((!two || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
         const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
-        const float g = a.num_splits > 1 ? vfac : l > 0.0f ? vfac / l : 0.0f;
+        const float g = a.num_splits > 1 ? vfac : vfac / l;
         const long long pi = qrow * a.num_splits + split;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
             }
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = l > 0.0f ? o[e] * g : 0.0f;
+          for (int e = 0; e < 32; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * g;  // (a NaN score makes its row NaN)
           if (!real) continue;
           if (a.num_splits == 1) {
 #pragma unroll
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
         }
         if (real && a.num_splits > 1)
-          st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l > 0.0f ? R : -INFINITY, l), a.ws_span, a.pool);
+          st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l == 0.0f ? -INFINITY : R, l), a.ws_span, a.pool);
       }
     }
   }

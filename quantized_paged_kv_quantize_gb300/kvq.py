@@ -194,11 +194,14 @@ def _take_slowly(t, name, cache, dtype, shape, dense):
 
 _FLOATS = {torch.float16: KVQ_F16, torch.float32: KVQ_F32}
 # the current stream's handle by device index (the public call builds a Stream object around it)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream_of(cache: "KVCache", stream) -> Optional[int]:
+    if _current_device() != cache.device:
+        raise ValueError(f"the cache is on {cache.pool.device}, which is not the current device")
     return _raw_stream(cache.device) if stream is None else _stream(stream)
 
 

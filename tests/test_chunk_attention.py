@@ -261,6 +261,7 @@ def test_refusals():
                         (dict(window=-1), K.KVQError), (dict(logit_cap=-1.0), K.KVQError),
                         (dict(logit_cap=float("nan")), K.KVQError), (dict(softmax_scale=0.0), K.KVQError),
                         (dict(max_seq_len=10 ** 6), K.KVQError), (dict(max_q_len=-1), K.KVQError),
+                        (dict(max_q_len=0), K.KVQError),
                         (dict(mode="nvfp4"), K.KVQError),
                         (dict(q=torch.zeros(20, 3, 128, device="cuda").half(), out=torch.zeros(20, 3, 128, device="cuda")), K.KVQError),
                         (dict(q=torch.zeros(20, 18, 128, device="cuda").half(), out=torch.zeros(20, 18, 128, device="cuda")), K.KVQError)]:
@@ -389,3 +390,26 @@ def test_pages_below_the_window_are_not_read(io, qlens, lens):
     assert K.kvq_cache_read_errors(cache) == 0
     assert np.abs(got.double().cpu().numpy() - want).max() < 1e-4
     assert np.abs(half.double().cpu().numpy() - want).max() < 1e-2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f16", "f32"])
+@pytest.mark.parametrize("qlens,lens", [([40, 3], [300, 50]), ([300], [900])])
+def test_nan_query_and_nan_in_unseen_keys(qlens, lens, out):
+    """A NaN query makes its own row NaN and no other; NaN keys after a query's position do not reach it."""
+    K = kvq()
+    cache, table, vals = build("int8_per_token_head", "f16", 1, 128, lens)
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    q = torch.randn(cu[-1], 4, 128, device="cuda").half()
+    want = formula(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5)
+    q[1, 2, 5] = float("nan")
+    # the key scale of the first sequence's last token
+    tok = lens[0] - 1
+    blk = cache.pool[256:].view(cache.cfg.num_pages, -1)[int(table[0, tok // 16])]
+    blk[4096:4096 + 64].view(torch.float32)[tok % 16] = float("nan")
+    got = run(cache, table, q, cu, lens, torch.float16 if out == "f16" else torch.float32).double().cpu().numpy()
+    last = qlens[0] - 1
+    assert np.isnan(got[1, 2]).all() and np.isnan(got[last]).all()
+    keep = np.ones(got.shape[:2], bool)
+    keep[1, 2] = keep[last] = False
+    assert np.isfinite(got[keep]).all() and np.abs(got[keep] - want[keep]).max() < 5e-3
