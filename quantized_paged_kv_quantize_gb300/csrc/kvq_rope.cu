@@ -27,11 +27,16 @@
 //    good to about 2^-44, and rounded once (to odd in fp32, then to fp16).
 //  fp32 rows always take the double-word form.
 //
+// Bound by instruction issue (71% of the slots; DRAM 30%): about 300 instructions
+// for two fp16 head rows, a third of them the double-word path that 35% of the
+// warps take.  8191 tokens of 64 + 2 x 8 int8 heads: 105 us (3.3 TB/s of the rows in
+// and out and the packed bytes).
+//
 // Layout.  A group of D / VEC lanes holds a head row (16 bytes a lane) and
 // walks over a CTA's heads for one token, so the token's cosines and sines
 // (fp32, from the caller's table) are read once per token and head chunk
 // instead of once per head; the half-split pairs live in two lanes of the
-// group and meet by shuffle.  Rows of four heads are in flight per thread.
+// group and meet by shuffle.
 #include <cuda_fp16.h>
 
 #include "kvq_device.cuh"
@@ -42,7 +47,7 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;  // head rows in flight behind the one a thread converts
+constexpr int kAhead = 1;  // head rows in flight behind the one a thread converts (two: 2% slower)
 
 struct RopeArgs {
   WriteArgs w;  // pool, slots (null: no cache write), geometry
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_con
 
   // The row being converted and the kAhead rows whose loads are in flight.  One
   // copy of the loop's body: unrolled over four heads it outgrew the
-  // instruction cache (8191 tokens of 64 + 2 x 8 heads, int8: 407 us).
+  // instruction cache (8191 tokens of 64 + 2 x 8 int8 heads: 407 us).
   auto load = [&](int h) {
     return in && h < h1 ? *reinterpret_cast<const uint4*>(src + (long long)h * D) : make_uint4(0u, 0u, 0u, 0u);
   };
@@ -355,11 +360,12 @@ template <int MODE, typename T, int D>
 cudaError_t launch(RopeArgs& a, cudaStream_t s) {
   constexpr int TOK = kThreads / (D / (16 / (int)sizeof(T)));
   const long long blocks = (a.w.num_tokens + TOK - 1) / TOK;
-  // Heads per CTA: more heads share a token's table rows and weights, fewer
-  // give more CTAs; eight where that still leaves two CTAs per SM.
+  // Heads per CTA: more heads share a token's table rows and weights, fewer give
+  // more CTAs; doubled while six CTAs per SM are left (8191 tokens of 64 + 2 x 8
+  // int8 heads: 113 us with 8 heads, 105 with up to 32).
   auto chunks = [](int heads, int c) { return (heads + c - 1) / c; };
-  a.chunk = 8;
-  if (blocks * (chunks(a.Hq, a.chunk) + 2 * chunks(a.w.Hkv, a.chunk)) < 2 * num_sms()) a.chunk = 4;
+  a.chunk = 4;
+  while (a.chunk < 32 && blocks * (chunks(a.Hq, 2 * a.chunk) + 2 * chunks(a.w.Hkv, 2 * a.chunk)) >= 6 * num_sms()) a.chunk *= 2;
   a.q_chunks = chunks(a.Hq, a.chunk);
   a.k_chunks = (MODE != 0 || a.k_out) ? chunks(a.w.Hkv, a.chunk) : 0;
   const int v_chunks = MODE != 0 ? chunks(a.w.Hkv, a.chunk) : 0;
