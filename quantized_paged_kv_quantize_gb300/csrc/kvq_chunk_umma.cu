@@ -16,9 +16,9 @@
 // reference again.
 //
 // Roles (16 warps, one CTA per SM; registers are shared out between the warpgroups):
-//  warps 0-3, 4-7  softmax of block 0 and block 1: thread = row, whose 128 scores are
-//                  in registers from the load to the weights (tensor memory is read
-//                  once, and P can go over S);
+//  warps 0-3, 4-7  softmax of block 0 and block 1: thread = row, 64 of its 128
+//                  scores at a time in registers from the load to the weights
+//                  (tensor memory is read once, and P can go over S);
 //  warps 8-11      dequantization: a warp takes two pages of a 128-token tile, their
 //                  packed words in registers one tile ahead, and writes the
 //                  codes as fp16 core matrices (8 tokens x 16 bytes), which
@@ -51,6 +51,8 @@ constexpr int kRegsSoftmax = 176, kRegsDequant = 104, kRegsIssue = 48;
 constexpr int kPages = 2;       // pages of a tile that one warp dequantizes
 constexpr int kOpBytes = kTok * kD * 2;  // one fp16 operand tile
 constexpr int kLbo = 128, kSbo = 2048;   // core matrices: along channels, along rows / tokens
+constexpr int kStageRow = 256 + 16;           // an output row in shared memory; the pad spreads the banks
+constexpr int kStageBytes = 32 * kStageRow;   // of one warp
 constexpr int kSlots = 4;       // tiles whose scales are kept
 constexpr float kSlack = 8.0f;  // log2
 constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
@@ -711,9 +713,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         }
       }
       if ((!two || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
-        const long long qrow = (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
+        // Rows leave through shared memory (Q's place, free now), so that each store
+        // of a warp writes two whole rows of 256 bytes: 128 halves, or 64 of a partial
+        // result's floats.  Thread by row, 16 bytes each, a store touches 32 half sectors.
+        const int rel = (rr / a.G - t.r0 / a.G) * a.Hq + kvh * a.G + rr % a.G;
+        const long long q_base = (long long)(t.q0 + t.r0 / a.G) * a.Hq;
         const float g = a.num_splits > 1 ? vfac : vfac / l;
-        const long long pi = qrow * a.num_splits + split;
+        const int rows = min(32, t.count - (row - lane));
+        uint8_t* stage = sm + L::Q + warp * kStageBytes;
+        auto flush = [&](auto store) {
+          __syncwarp();
+#pragma unroll 4
+          for (int r = lane >> 4; r < 32; r += 2) {
+            const long long qrow = q_base + __shfl_sync(kFull, rel, r);
+            if (r < rows) store(qrow, lane & 15, *reinterpret_cast<const uint4*>(stage + r * kStageRow + 16 * (lane & 15)));
+          }
+          __syncwarp();
+        };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
@@ -736,21 +752,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * g;  // (a NaN score makes its row NaN)
-          if (!real) continue;
           if (a.num_splits == 1) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const uint4 h = make_uint4(h2_as_u32(__floats2half2_rn(o[e], o[e + 1])), h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3])),
-                                         h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5])), h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7])));
-              st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD + 32 * c + e), h, a.out_span, a.pool);
-            }
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(stage + lane * kStageRow + 64 * c + 2 * e) =
+                  make_uint4(h2_as_u32(__floats2half2_rn(o[e], o[e + 1])), h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3])),
+                             h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5])), h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7])));
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              st_chk(reinterpret_cast<float4*>(a.ws_o + pi * kD + 32 * c + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]),
-                     a.ws_span, a.pool);
+              *reinterpret_cast<float4*>(stage + lane * kStageRow + 128 * (c & 1) + 4 * e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if (c & 1)
+              flush([&](long long qrow, int j, uint4 x) {
+                st_chk(reinterpret_cast<uint4*>(a.ws_o + (qrow * a.num_splits + split) * kD + 64 * (c >> 1)) + j, x, a.ws_span, a.pool);
+              });
           }
         }
+        if (a.num_splits == 1)
+          flush([&](long long qrow, int j, uint4 x) {
+            st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD) + j, x, a.out_span, a.pool);
+          });
+        const long long pi = (q_base + rel) * a.num_splits + split;
         if (real && a.num_splits > 1)
           st_chk(reinterpret_cast<float2*>(a.ws_ml + 2 * pi), make_float2(l == 0.0f ? -INFINITY : R, l), a.ws_span, a.pool);
       }
