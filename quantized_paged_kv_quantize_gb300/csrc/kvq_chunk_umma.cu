@@ -107,6 +107,17 @@ __device__ __forceinline__ void put(uint32_t* r, int i, float2 x) {
   r[i] = __float_as_uint(x.x);
   r[i + 1] = __float_as_uint(x.y);
 }
+// The larger magnitude of three, NaN if one is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {  // 1 / x to about 1 ulp; 0 of infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
   return a;
@@ -556,9 +567,32 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         if constexpr (OPT) {
           if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
             const float cap2 = a.cap * kLog2e, rcap = 2.0f * kLog2e / cap2;
+float t4[4] = {};
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              x[e] = __float_as_uint(cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(__uint_as_float(x[e]) * rcap)));
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                t4[u] = max3_abs_nan(t4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+            const float far = max3_abs_nan(max3_abs_nan(t4[0], t4[1], t4[2]), t4[3], 0.0f) * rcap;
+            if (__any_sync(kFull, !(far <= 30.0f))) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                x[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp_ftz(1.0f + ex2(__uint_as_float(x[e]) * rcap)), cap2));
+            } else {
+              const float2 rc2 = make_float2(rcap, rcap), one2 = make_float2(1.0f, 1.0f), c2 = make_float2(cap2, cap2),
+                           m2 = make_float2(-2.0f * cap2, -2.0f * cap2);
+#pragma unroll
+              for (int e = 0; e < 64; e += 4) {
+                float2 u = __fmul2_rn(get(x, e), rc2), v = __fmul2_rn(get(x, e + 2), rc2);
+                u = __fadd2_rn(make_float2(ex2(u.x), ex2(u.y)), one2);
+                v = __fadd2_rn(make_float2(ex2(v.x), ex2(v.y)), one2);
+                const float2 w = __fmul2_rn(u, v);
+                const float r = rcp_ftz(w.x * w.y);
+                const float2 rw = __fmul2_rn(make_float2(w.y, w.x), make_float2(r, r));
+                put(x, e, __ffma2_rn(__fmul2_rn(rw, v), m2, c2));
+                put(x, e + 2, __ffma2_rn(__fmul2_rn(rw, u), m2, c2));
+              }
+            }
           }
           if (a.slopes) {
             const float d = (float)(pos - t0 - 64 * h);  // distances are whole numbers below 2^24: exact

@@ -413,3 +413,35 @@ def test_nan_query_and_nan_in_unseen_keys(qlens, lens, out):
     keep = np.ones(got.shape[:2], bool)
     keep[1, 2] = keep[last] = False
     assert np.isfinite(got[keep]).all() and np.abs(got[keep] - want[keep]).max() < 5e-3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["int8_per_token_head", "nvfp4", "fp8_per_tensor"])
+@pytest.mark.parametrize("cap", [0.25, 4.0, 400.0])
+def test_scores_far_past_the_cap(mode, cap):
+    """Scores of about 11 in size, so that tanh is taken from its linear part to far past where it is 1."""
+    check(mode, "f16", "f16", 1, 8, 128, [70, 1, 20], [70, 260, 301], cap=cap, scale=1.0)
+    check(mode, "f16", "f32", 2, 2, 128, [150, 3], [150, 700], cap=cap, scale=1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_nan_with_a_cap(out):
+    """With capped scores too a NaN stays in its row, and unseen NaN keys reach none."""
+    K = kvq()
+    qlens, lens = [300, 5], [300, 400]
+    cache, table, vals = build("int8_per_token_head", "f16", 1, 128, lens)
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    q = torch.randn(cu[-1], 4, 128, device="cuda").half()
+    want = formula(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5, cap=3.0)
+    q[1, 2, 5] = float("nan")
+    tok = lens[0] - 1
+    blk = cache.pool[256:].view(cache.cfg.num_pages, -1)[int(table[0, tok // 16])]
+    blk[4096:4096 + 64].view(torch.float32)[tok % 16] = float("nan")
+    got = run(cache, table, q, cu, lens, torch.float16 if out == "f16" else torch.float32,
+              logit_cap=3.0).double().cpu().numpy()
+    last = qlens[0] - 1
+    assert np.isnan(got[1, 2]).all() and np.isnan(got[last]).all()
+    keep = np.ones(got.shape[:2], bool)
+    keep[1, 2] = keep[last] = False
+    assert np.isfinite(got[keep]).all() and np.abs(got[keep] - want[keep]).max() < 5e-3
