@@ -61,7 +61,7 @@ struct Smem {
   static constexpr int Q = 0;
   static constexpr int K = Q + 2 * kOpBytes;  // two stages each
   static constexpr int V = K + 2 * kOpBytes;
-  static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] key scales in log2 units
+  static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] key scales times kfac
   static constexpr int VS = KS + kSlots * kTok * 4;                // [slot][128] value scales
   static constexpr int PAGE = VS + kSlots * kTok * 4;              // [slot][8] page states
   static constexpr int START = PAGE + kSlots * 8 * 4;              // [slot] first token of the tile
@@ -112,11 +112,6 @@ __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {  // 1 / x to about 1 ulp; 0 of infinity
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
@@ -340,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   const uint32_t tb = tmem_s;
   bool ok = true;
 
-  float kfac = a.scale * kLog2e, vfac = 1.0f;  // score factor in log2 units, output factor
+  // score factor in log2 units (of the cap where there is one), output factor
+  float kfac = OPT && a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e, vfac = 1.0f;
   if constexpr (!PT) {
     kfac *= *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
     vfac = *reinterpret_cast<const float*>(a.pool + kHdrVScaleOffset);
@@ -551,47 +547,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         // weights are computed: one fused step then does both, in the shadow of the
         // exponentials.
         constexpr bool RAW = !PT && !OPT;
-        const float2 nR = make_float2(-R, -R);
+        const float2 nR = make_float2(-R, -R), add = OPT && a.cap > 0.0f ? make_float2(0.0f, 0.0f) : nR;
 #pragma unroll
         for (int e = 0; e < (RAW ? 0 : 64); e += 4) {
           float4 f = make_float4(kfac, kfac, kfac, kfac);
           if constexpr (PT) f = *reinterpret_cast<const float4*>(ks + e);
-          if constexpr (OPT) {
-            put(x, e, __fmul2_rn(get(x, e), make_float2(f.x, f.y)));
-            put(x, e + 2, __fmul2_rn(get(x, e + 2), make_float2(f.z, f.w)));
-          } else {
-            put(x, e, __ffma2_rn(get(x, e), make_float2(f.x, f.y), nR));
-            put(x, e + 2, __ffma2_rn(get(x, e + 2), make_float2(f.z, f.w), nR));
-          }
+          put(x, e, __ffma2_rn(get(x, e), make_float2(f.x, f.y), add));
+          put(x, e + 2, __ffma2_rn(get(x, e + 2), make_float2(f.z, f.w), add));
         }
         if constexpr (OPT) {
-          if (a.cap > 0.0f) {  // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-            const float cap2 = a.cap * kLog2e, rcap = 2.0f * kLog2e / cap2;
-float t4[4] = {};
+          if (a.cap > 0.0f) {
+            // (the factors hold 1 / cap)  16 short chunks take 131 us with the polynomial,
+            // 142 us with the other form alone and 90 us without a cap.
+            const SoftCap cap{a.cap * kLog2e};
+            float t4[4] = {};
 #pragma unroll
             for (int e = 0; e < 64; e += 8)
 #pragma unroll
               for (int u = 0; u < 4; ++u)
                 t4[u] = max3_abs_nan(t4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
-            const float far = max3_abs_nan(max3_abs_nan(t4[0], t4[1], t4[2]), t4[3], 0.0f) * rcap;
-            if (__any_sync(kFull, !(far <= 30.0f))) {
+            if (__all_sync(kFull, cap.near(max3_abs_nan(max3_abs_nan(t4[0], t4[1], t4[2]), t4[3], 0.0f)))) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                x[e] = __float_as_uint(fmaf(-2.0f * cap2, rcp_ftz(1.0f + ex2(__uint_as_float(x[e]) * rcap)), cap2));
+              for (int e = 0; e < 64; e += 2) put(x, e, __ffma2_rn(cap.slope(get(x, e)), get(x, e), nR));
             } else {
-              const float2 rc2 = make_float2(rcap, rcap), one2 = make_float2(1.0f, 1.0f), c2 = make_float2(cap2, cap2),
-                           m2 = make_float2(-2.0f * cap2, -2.0f * cap2);
 #pragma unroll
-              for (int e = 0; e < 64; e += 4) {
-                float2 u = __fmul2_rn(get(x, e), rc2), v = __fmul2_rn(get(x, e + 2), rc2);
-                u = __fadd2_rn(make_float2(ex2(u.x), ex2(u.y)), one2);
-                v = __fadd2_rn(make_float2(ex2(v.x), ex2(v.y)), one2);
-                const float2 w = __fmul2_rn(u, v);
-                const float r = rcp_ftz(w.x * w.y);
-                const float2 rw = __fmul2_rn(make_float2(w.y, w.x), make_float2(r, r));
-                put(x, e, __ffma2_rn(__fmul2_rn(rw, v), m2, c2));
-                put(x, e + 2, __ffma2_rn(__fmul2_rn(rw, u), m2, c2));
-              }
+              for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(cap.any(__uint_as_float(x[e])) - R);
             }
           }
           if (a.slopes) {
@@ -599,8 +579,6 @@ float t4[4] = {};
 #pragma unroll
             for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(fmaf(slope, fabsf(d - (float)e), __uint_as_float(x[e])));
           }
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) put(x, e, __fadd2_rn(get(x, e), nR));
         }
         if (masked) {
           const int4 pg = h ? pg1 : pg0;

@@ -373,6 +373,29 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the SFU (rel. error ~
   return y;
 }
 
+// Capped scores: x = cap tanh(u) of u = score / cap.  Up to |u| = 1/2 by an odd polynomial
+// (least squares on Chebyshev points of [0, 1/4] in u^2: 5.6e-8 of the value), which
+// keeps small scores to fp32's relative precision under any cap and takes no
+// special-function step; elsewhere by 1 - 2 / (1 + e^2u), whose error is about 2^-23
+// of the cap.
+struct SoftCap {
+  float cap;  // in log2 units, as x
+  __device__ __forceinline__ static bool near(float u) { return fabsf(u) <= 0.5f; }  // (not of a NaN)
+  __device__ __forceinline__ float2 slope(float2 u) const {                          // x / u where near
+    auto k = [&](float c) { return make_float2(c * cap, c * cap); };
+    const float2 z = __fmul2_rn(u, u);
+    float2 y = __ffma2_rn(z, k(0.01799922f), k(-0.05339105f));
+    y = __ffma2_rn(z, y, k(0.13330514f));
+    y = __ffma2_rn(z, y, k(-0.33333312f));
+    return __ffma2_rn(z, y, k(1.0f));
+  }
+  __device__ __forceinline__ float any(float u) const {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(u * (2.0f * kLog2e))));
+    return fmaf(-2.0f * cap, r, cap);
+  }
+};
+
 // Shared-memory loads of N 32-bit words.
 template <int N>
 __device__ __forceinline__ void lds(const uint8_t* p, uint32_t* w);
@@ -417,7 +440,7 @@ struct DecodeArgs {
   int tokens_per_split, num_splits;
   int out_f32;
   int q_f32;
-  float sm_log2;  // softmax_scale * log2(e)
+  float sm_log2;  // softmax_scale * log2(e); with a cap, softmax_scale / cap
   size_t block_bytes;
   int rows_per_block;
   // KVarN open tiles (kvq_kvarn_decode_attention): the tail buffer, K rows
