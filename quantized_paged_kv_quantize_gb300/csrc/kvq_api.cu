@@ -495,8 +495,8 @@ kvq_status check_chunk(const kvq_cache* cache, int total_q, int num_seqs, int nu
     return fail(KVQ_ERR_UNSUPPORTED, "GQA group %d > 8", num_q_heads / c.num_kv_heads);
   if (c.num_kv_heads > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", c.num_kv_heads);
   if (opt) {
-    if (opt->logit_cap != 0.0f && !(opt->logit_cap >= 1.0e-10f && opt->logit_cap <= 1.0e10f))
-      return fail(KVQ_ERR_INVALID_ARG, "logit_cap must be 0 or from 1e-10 to 1e10");
+    if (opt->logit_cap != 0.0f && !(opt->logit_cap >= 1.0e-10f && opt->logit_cap <= 1024.0f))
+      return fail(KVQ_ERR_INVALID_ARG, "logit_cap must be 0 or from 1e-10 to 1024");
     if (opt->window < 0) return fail(KVQ_ERR_INVALID_ARG, "window < 0");
   }
   return KVQ_OK;

@@ -450,9 +450,9 @@ constexpr size_t decode_smem() {
 // heads of its split in `part` ([8] m, [8] l, [8][D] o); CTA r then takes
 // every cluster-size-th element (h, d) from r * blockDim on:
 // M = max_s m_s, w_s = 2^(m_s - M), out = sum_s o_s w_s / sum_s l_s w_s (0 for
-// a row without tokens).  The second barrier keeps every CTA's shared memory
-// alive until its peers have read it.
-template <int D>
+// a row without tokens, and without NAN_ROWS for one with a NaN score).  The
+// second barrier keeps every CTA's shared memory alive until its peers have read it.
+template <int D, bool NAN_ROWS>
 __device__ void merge_in_cluster(const DecodeArgs& a, long long b, int kvh, const float* part) {
   cluster_barrier();
   const int r = cluster_rank(), ns = cluster_size();
@@ -479,7 +479,7 @@ __device__ void merge_in_cluster(const DecodeArgs& a, long long b, int kvh, cons
         }
       }
     }
-    store_out(a, (b * a.Hq + (long long)kvh * a.G + h) * D + d, L > 0.0f ? O / L : 0.0f);
+    store_out(a, (b * a.Hq + (long long)kvh * a.G + h) * D + d, L > 0.0f || (NAN_ROWS && L != 0.0f) ? O / L : 0.0f);
   }
   cluster_barrier();
 }
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
       }
     } else if (a.cluster) {  // an empty split still takes part in its cluster's merge
       for (int i = threadIdx.x; i < 8 * (D + 2); i += blockDim.x) cpart[i] = i < 8 ? -INFINITY : 0.0f;
-      merge_in_cluster<D>(a, row, kvh, cpart);
+      merge_in_cluster<D, OPT>(a, row, kvh, cpart);
     }
     return;
   }
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
     }
     const int hq = kvh * a.G + h;
     if (a.num_splits == 1) {
-      const float r = L > 0.0f ? O * vfac / L : 0.0f;
+      const float r = L > 0.0f || (OPT && L != 0.0f) ? O * vfac / L : 0.0f;
       const long long oi = (row * a.Hq + hq) * D + d;
       store_out(a, oi, r);
     } else if (a.cluster) {
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
       }
     }
   }
-  if (a.cluster) merge_in_cluster<D>(a, row, kvh, cpart);
+  if (a.cluster) merge_in_cluster<D, OPT>(a, row, kvh, cpart);
 }
 
 // Merge the splits of each (sequence, query head).
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(D) combine_kernel(const __grid_constant__ Deco
     n = max(n - (a.nq - 1 - b % a.nq), 0);
   }
   const int ns = (n + a.tokens_per_split - 1) / a.tokens_per_split;
-  const float r = merge_split_row<D>(a, ((long long)b * a.Hq + hq) * a.num_splits, ns, wts, red);
+  const float r = merge_split_row<D, OPT>(a, ((long long)b * a.Hq + hq) * a.num_splits, ns, wts, red);
   const long long oi = (row * a.Hq + hq) * D + d;
   store_out(a, oi, r);
 }

@@ -375,9 +375,8 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the SFU (rel. error ~
 
 // Capped scores: x = cap tanh(u) of u = score / cap.  Up to |u| = 1/2 by an odd polynomial
 // (least squares on Chebyshev points of [0, 1/4] in u^2: 5.6e-8 of the value), which
-// keeps small scores to fp32's relative precision under any cap and takes no
-// special-function step; elsewhere by 1 - 2 / (1 + e^2u), whose error is about 2^-23
-// of the cap.
+// takes no special-function step; elsewhere by 1 - 2 / (1 + e^2u), whose error is about
+// 2^-23 of the cap: 2e-4 at the largest, 1024.
 struct SoftCap {
   float cap;  // in log2 units, as x
   __device__ __forceinline__ static bool near(float u) { return fabsf(u) <= 0.5f; }  // (not of a NaN)
@@ -503,7 +502,8 @@ __device__ __forceinline__ void store_ws(const DecodeArgs& a, float* p, float v)
 // for a row with no tokens).  The weights go through shared memory (wts[D],
 // red[D / 32]) in chunks of D splits and each thread keeps eight partial loads
 // in flight, so a row costs a few memory round trips whatever the split count.
-template <int D>
+// NAN_ROWS: a NaN score makes its row NaN; without, such a row is 0.
+template <int D, bool NAN_ROWS = false>
 __device__ float merge_split_row(const DecodeArgs& a, long long base, int ns, float* wts, float* red,
                                  float* m_out = nullptr, float* l_out = nullptr) {
   constexpr int NW = D / 32;
@@ -555,7 +555,7 @@ __device__ float merge_split_row(const DecodeArgs& a, long long base, int ns, fl
     *l_out = lsum;
     return acc;
   }
-  return lsum > 0.0f ? acc / lsum : 0.0f;
+  return lsum > 0.0f || (NAN_ROWS && lsum != 0.0f) ? acc / lsum : 0.0f;
 }
 
 // The span of the pool's (page, kv head) blocks: every store a write kernel makes.

@@ -449,26 +449,38 @@ def test_nan_with_a_cap(out):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["f16", "f32"])
-@pytest.mark.parametrize("cap", [1.0e4, 1.0e6, 1.0e10])
-def test_a_cap_no_score_comes_near(io, cap):
-    """A large cap changes nothing: each score keeps its own precision, not the cap's."""
-    for D, H, G, qlens, lens in [(128, 1, 8, [70, 1, 20], [70, 260, 301]), (128, 2, 4, [1, 1], [300, 17]),
-                                 (32, 2, 1, [70, 3], [70, 90])]:
-        cache, table, vals = build("int8_per_token_head", io, H, D, lens)
-        cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
-        dt = torch.float16 if io == "f16" else torch.float32
-        q = torch.randn(cu[-1], H * G, D, device="cuda").to(dt)
-        got = run(cache, table, q, cu, lens, dt, logit_cap=cap).double().cpu().numpy()
-        want = formula(vals, table, q.cpu().numpy(), cu, lens, D ** -0.5)
-        tol = tolerance(want, np.abs(vals[1][np.isfinite(vals[1])]).max(), 1.4427 * 8, max(lens), dt, io == "f32")
-        assert (np.abs(got - want) <= tol).all()
+@pytest.mark.parametrize("cap", [1.0e-10, 1024.0])
+def test_the_smallest_and_the_largest_cap(io, cap):
+    check("int8_per_token_head", io, io, 1, 8, 128, [70, 1, 20], [70, 260, 301], cap=cap)
+    check("int8_per_token_head", io, io, 2, 4, 128, [1, 1], [300, 17], cap=cap)
+    check("nvfp4", io, io, 2, 1, 32, [70, 3], [70, 90], cap=cap)
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("cap", [1.0e-11, 2.0e10, 3.0e38, float("inf"), -0.5])
+@pytest.mark.parametrize("cap", [1.0e-11, 1025.0, 3.0e38, float("inf"), -0.5])
 def test_caps_out_of_range_are_refused(cap):
     K = kvq()
     cache, table, _ = build("nvfp4", "f16", 1, 128, [20])
     q = torch.zeros(4, 8, 128, device="cuda", dtype=torch.float16)
     with pytest.raises(K.KVQError):
         run(cache, table, q, np.array([0, 4], np.int32), [20], torch.float16, logit_cap=cap)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qlens,lens", [([300, 5], [300, 400]), ([1, 1], [700, 20])])
+def test_a_nan_stays_in_its_row_under_a_large_cap(qlens, lens):
+    """A NaN query beside heads with small scores and with scores past the cap, in a chunk and in a single token."""
+    K = kvq()
+    cache, table, vals = build("int8_per_token_head", "f16", 1, 128, lens)
+    cu = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    q = torch.randn(cu[-1], 4, 128, device="cuda").half()
+    q[0, 1] *= 3000.0
+    cap = 1000.0
+    want = formula(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5, cap=cap)
+    q[0, 2, 5] = float("nan")
+    got = run(cache, table, q, cu, lens, torch.float16, logit_cap=cap).double().cpu().numpy()
+    assert np.isnan(got[0, 2]).all()
+    keep = np.ones(got.shape[:2], bool)
+    keep[0, 1:3] = False
+    tol = tolerance(want, np.abs(vals[1][np.isfinite(vals[1])]).max(), 1.4427 * cap, max(lens), torch.float16, False)
+    assert np.isfinite(got[0, 1]).all() and (np.abs(got - want) <= tol)[keep].all()
