@@ -533,6 +533,8 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_
     return fail(KVQ_ERR_INVALID_ARG, "cu_q_lens must be non-NULL and 4-byte aligned");
   if (options && (!aligned(options->alibi_slopes, 4) || !aligned(options->prefix_lens, 4)))
     return fail(KVQ_ERR_INVALID_ARG, "alibi_slopes and prefix_lens must be 4-byte aligned");
+  if (options && options->logit_cap > 0.0f && !(softmax_scale / options->logit_cap <= 1.0e30f))
+    return fail(KVQ_ERR_INVALID_ARG, "softmax_scale is more than 1e30 times logit_cap");
   kvq::ChunkCall k;
   k.window = options ? options->window : 0;
   k.prefix_lens = options ? options->prefix_lens : nullptr;

@@ -467,7 +467,18 @@ def test_caps_out_of_range_are_refused(cap):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("qlens,lens", [([300, 5], [300, 400]), ([1, 1], [700, 20])])
+def test_a_scale_too_large_for_the_cap_is_refused():
+    """The kernels work with softmax_scale / logit_cap."""
+    K = kvq()
+    cache, table, _ = build("nvfp4", "f16", 1, 128, [20])
+    q = torch.zeros(4, 8, 128, device="cuda", dtype=torch.float16)
+    with pytest.raises(K.KVQError):
+        run(cache, table, q, np.array([0, 4], np.int32), [20], torch.float16, logit_cap=1.0e-10, softmax_scale=1.0e30)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qlens,lens", [([300, 5], [300, 400]), ([1, 1], [700, 20]), ([1, 1], [20000, 33]),
+                                        ([1] * 40, [90] * 40)])
 def test_a_nan_stays_in_its_row_under_a_large_cap(qlens, lens):
     """A NaN query beside heads with small scores and with scores past the cap, in a chunk and in a single token."""
     K = kvq()
