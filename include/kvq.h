@@ -327,7 +327,7 @@ kvq_status kvq_decode_attention_multi(const kvq_cache* cache, const void* q, con
  * and (with prefix_lens) all tokens t < prefix_len, before or after it, inside
  * the sequence.  A query at a negative position attends to nothing: output 0. */
 typedef struct {
-  float logit_cap;             /* 0: none; else 1e-10 to 1024 */
+  float logit_cap;             /* 0: none; else 1e-10 to 1024, and at least softmax_scale / 1e30 */
   int32_t window;              /* 0: none */
   const float* alibi_slopes;   /* device [num_q_heads], or NULL */
   const int32_t* prefix_lens;  /* device [num_seqs], or NULL */
