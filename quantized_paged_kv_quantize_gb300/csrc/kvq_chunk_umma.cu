@@ -618,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           l *= al;
 #pragma unroll
           for (int e = 0; e < (RAW ? 0 : 64); e += 2) put(x, e, __fadd2_rn(get(x, e), make_float2(-up, -up)));
-          if (any) {  // every product issued before this S has completed
+          tmem_wait_st();  // (the first half may have just rescaled O, and has stored its P: both are read below)
+          if (any) {       // every product issued before this S has completed
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t v[16];
@@ -630,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
             }
           }
           if (h) {
-            tmem_wait_st();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t v[16];

@@ -1,0 +1,95 @@
+"""kvq_chunk_attention where its softmax reference and its weights have to be right:
+scores that jump inside a tile, and value scales far apart.  Every row is held to
+the values that it sees itself."""
+import numpy as np
+import pytest
+import torch
+
+from _helpers import kvq
+from test_chunk_attention import build, run
+from test_norm_rope_read import pool_values
+
+
+def store(cache, table, b, k, v):
+    """Write k, v [n][H][D] (numpy) as sequence b of `table`; the pool's values afterwards."""
+    n = len(k)
+    t = np.arange(n)
+    slots = torch.from_numpy((table[b, t // 16] * 16 + t % 16).astype(np.int32)).cuda()
+    kvq().kvq_quantize_write(cache, *(torch.from_numpy(x).to(cache.io_dtype).cuda() for x in (k, v)), slots)
+
+
+def values(cache, mode, ks=1.0, vs=1.0):
+    torch.cuda.synchronize()
+    return pool_values(mode, cache.pool.cpu().numpy(), cache.cfg.num_pages, cache.heads, cache.head_dim, ks, vs)
+
+
+def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 ** -20):
+    """The formula in 64 bits and, for every output, a bound on its error.
+
+    A score is an fp32 sum of D products (the products are exact: codes of at most 9 bits times fp16, or times the
+    halves of an fp32 value), in steps of 16: 16 roundings (2^-23 where sums are cut off) of sum |q k|, four more of the
+    score itself.  A weight is within that, the exponential (2^-22) and its own bits (`weight`: both), or within 2^-30 of
+    the largest weight x value of the row; the sums over n tokens take n / 16 + 16 steps."""
+    H, (Hq, D) = vals.shape[3], q.shape[1:]
+    want, tol = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        k, v = vals[:, table[b, t // 16], t % 16]
+        m = cu[b + 1] - cu[b]
+        for i in range(m):
+            p = n - m + i
+            see = (t <= p) & ((t > p - window) if window else True)
+            for h in range(Hq):
+                x = q[cu[b] + i, h].astype(np.float64)
+                kk, vv = k[see, h // (Hq // H)], v[see, h // (Hq // H)]
+                s = scale * (kk @ x)
+                ds = 16 * 2.0 ** -23 * scale * (np.abs(kk) @ np.abs(x)) + 8 * 2.0 ** -23 * np.abs(s) + 2.0 ** -21
+                if cap:
+                    s = cap * np.tanh(s / cap)
+                    ds = ds + 2.0 ** -22 * cap
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                want[cu[b] + i, h] = w @ vv
+                ds = ds + weight + (see.sum() / 16 + 16) * 2.0 ** -23
+                mag = w @ np.abs(vv)  # of every channel
+                tol[cu[b] + i, h] = (w * ds) @ np.abs(vv) + (w @ ds) * mag + \
+                    see.sum() * 2.0 ** -30 * (w * np.abs(vv).max(1)).max()
+    return want, tol
+
+
+def hold(got, want, tol):
+    dt = got.dtype
+    got = got.double().cpu().numpy()
+    # its own rounding: eps / 2 of the value, half a step of the smallest numbers
+    tol = tol + torch.finfo(dt).eps / 2 * np.abs(want) + (2.0 ** -25 if dt == torch.float16 else 0.0)
+    err = np.abs(got - want)
+    assert np.isfinite(got).all()
+    assert (err <= tol).all(), f"worst {np.max(err / tol):.3g} of the tolerance"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["int8_per_token_head", "fp8_per_tensor", "nvfp4"])
+@pytest.mark.parametrize("m,G", [(150, 2), (9, 8)])
+def test_scores_that_jump_twice_in_a_tile(mode, m, G):
+    """Tiles behind the first whose scores rise by 2^20 and more in their first 64 tokens and again in the other 64,
+    rows of one warp in different halves: O is rescaled twice within one tile."""
+    D, n = 128, 128 * 5 + 40
+    cache, table, _ = build(mode, "f16", 1, D, [n])
+    rng = np.random.default_rng(3)
+    k = rng.standard_normal((n, 1, D)) * 0.05
+    v = rng.standard_normal((n, 1, D))
+    tile, half = np.arange(n) // 128, np.arange(n) // 64 % 2
+    rise = 4 - tile  # the tiles are met from the last to the first
+    k[:, 0, 0] += 1.0 * rise + 0.5 * half      # both halves
+    k[:, 0, 1] += 1.0 * rise * (half == 0)     # the first half alone
+    k[:, 0, 2] += 1.0 * rise * (half == 1)     # the second half alone
+    kvq().kvq_cache_set_tensor_scales(cache, 6.0 / (448 if mode == "fp8_per_tensor" else 2688), 5.0 / 2688)
+    store(cache, table, 0, k, v)
+    vals = values(cache, mode, *(float(np.float32(x)) for x in (6.0 / (448 if mode == "fp8_per_tensor" else 2688), 5.0 / 2688)))
+    q = rng.standard_normal((m, G, D)) * 0.3
+    for r in range(m * G):
+        q[r // G, r % G, r % 3] += 300.0  # times 1 / sqrt(128) and log2 e: 38 a step
+    q = torch.from_numpy(q).half().cuda()
+    got = run(cache, table, q, [0, m], [n], torch.float16)
+    assert kvq().kvq_cache_read_errors(cache) == 0
+    hold(got, *exact_rows(vals, table, q.cpu().numpy(), [0, m], [n], D ** -0.5, weight=2.0 ** -10))  # weights in fp16, rounded twice at most
