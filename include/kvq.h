@@ -356,8 +356,7 @@ kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int
  * Pages that lie wholly below every window (and past the prefix) are not read,
  * and their block_table entries not looked at.  Calls that may overlap on the
  * GPU need a workspace each.
- * At head_dim 128 with fp16 in and out the weights are rounded to fp16 before
- * they meet the values; other combinations carry them to 2^-22.
+ * Weights meet the values as pairs of fp16 numbers (2^-22 of a weight).
  * KVarN is not supported (KVQ_ERR_UNSUPPORTED): its open tile lies outside the
  * pages.  A token whose stored value codes or scale are not finite may make every
  * output of its sequence's chunk NaN, those of queries before it too. */

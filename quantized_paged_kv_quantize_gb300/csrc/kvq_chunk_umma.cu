@@ -5,15 +5,14 @@
 // Mathematics (kvq_chunk.cu has the operator's definition).  With codes K, V
 // (exact in fp16) and scales apart, one 128 x 128 block of (row, token) pairs is
 //   S = Q K^T,  y = S ks_t (log2 units),  P = 2^(y - R) vs_t,  O += P V,  l += 2^(y - R)
-// in fp32 but for P, which is rounded to fp16 (2^-12 of a weight, random in sign: of
-// the size of the output's own rounding.  Taking vs_t into the fp16 values instead
-// was 20% faster and a second such rounding: 3.3e-4 against 2.7e-4 in the 2-norm,
-// where an exact result rounded to fp16 is 2.1e-4 off; it was not kept).  R is a
-// row's reference: the largest y + floor(log2 vs) of a tile met, moved (O and l
-// rescaled) only when a block passes it by more than 2^8, so that P stays inside
-// fp16's normal range whatever the magnitude of scores and values.  Tiles are taken
-// from the nearest tokens to the farthest: a bias by distance then never moves the
-// reference again.
+// in fp32 but for P, which enters its product as an fp16 pair, P rounded and the
+// remainder rounded: 2^-22 of a weight.  (One fp16 weight instead is an error of the
+// size of the output's own rounding: 2.9e-4 in the 2-norm where an exact result
+// rounded to fp16 is 2.1e-4 off.)  R is a row's reference, a whole number: the largest
+// y + floor(log2 vs) of a tile met, less kTop, moved (O and l rescaled, exactly) only
+// when a block passes it by more than 2^(kTop + kSlack).  Tiles are taken from the
+// nearest tokens to the farthest: a bias by distance then never moves the reference
+// again.
 //
 // Roles (16 warps, one CTA per SM; registers are shared out between the warpgroups):
 //  warps 0-3, 4-7  softmax of block 0 and block 1: thread = row, 64 of its 128
@@ -30,12 +29,14 @@
 // blocks of rows that use the same tile of keys and values; one with fewer takes
 // even and odd tiles as two streams, with a reference, sum and accumulator each,
 // merged at the end.
-// Tensor memory: S_0 S_1 (128 columns each; P over the first 64 of S) O_0 O_1.
+// Tensor memory: S_0 S_1 O_0 O_1, 128 columns each; over the 64 columns of each half of
+// S, the 32 of its P rounded and the 32 of the remainders.
 //
 // Bound by the softmax warps' latency and the dequantization beside the tensor cores:
-// 2048 queries of 64 heads over 32768 nvfp4 tokens take 1.72 ms (1.24 PFLOP/s, the
-// tensor cores busy for 52% of it), three int8 prompts of 700 to 2048 tokens, where a CTA's
-// start and end are half of its time, 123 us.
+// 2048 queries of 64 heads over 32768 nvfp4 tokens take 2.14 ms (1.0 PFLOP/s of the formula;
+// the second product runs twice, and the tensor cores are busy for some 70%), three int8
+// prompts of 700 to 2048 tokens, where a CTA's start and end are half of its time, 133 us.
+// With one fp16 weight they took 1.72 ms and 123 us.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -59,7 +60,9 @@ constexpr int kLbo = 128, kSbo = 2048;   // core matrices: along channels, along
 constexpr int kStageRow = 256 + 16;           // an output row in shared memory; the pad spreads the banks
 constexpr int kStageBytes = 32 * kStageRow;   // of one warp
 constexpr int kSlots = 4;       // tiles whose scales are kept
-constexpr float kSlack = 8.0f;  // log2
+// Log2 of the largest weight times value scale when a reference is set, and how far later
+// ones may pass it: both below fp16's 2^16.
+constexpr float kTop = 6.0f, kSlack = 8.0f;
 constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
 
 struct Smem {
@@ -121,6 +124,13 @@ __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
   return a;
+}
+// x = hi + lo, both in fp16
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  const float2 f = __half22float2(h), r = __fadd2_rn(x, make_float2(-f.x, -f.y));
+  hi = h2_as_u32(h);
+  lo = h2_as_u32(__floats2half2_rn(r.x, r.y));
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
 __device__ __forceinline__ int exponent(float x) {  // floor(log2 x), x > 0, clamped
@@ -459,8 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           if (elect_one()) {
             const uint64_t B = dv + st * kOp;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              umma_f16_ts(tb + 256 + 128 * b, tb + 128 * b + 8 * e, B + e * kStepV, kIdescPV, (k > 1 || e > 0) ? 1u : 0u);
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t P = tb + 128 * b + 64 * (e >> 2) + 8 * (e & 3);
+              umma_f16_ts(tb + 256 + 128 * b, P, B + e * kStepV, kIdescPV, (k > 1 || e > 0) ? 1u : 0u);
+              umma_f16_ts(tb + 256 + 128 * b, P + 32, B + e * kStepV, kIdescPV, 1u);
+            }
             if (two || b == 1) tc_commit(&bar.v_free[st]);
             if (k + 1 == items) tc_commit(&bar.o_full);
           }
@@ -607,12 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         if constexpr (RAW) mx = fmaf(mx, kfac, -R);  // kfac > 0; ve = 0
 
         // The reference moves (and exponents, sum, accumulator and the first half's
-        // weights with it) only when a row meets its first score or one passes it by
-        // more than the slack.
-        if (__any_sync(kFull, mx > (fresh ? -INFINITY : kSlack))) {
+        // weights with it, all by a power of two) only when a row meets its first score
+        // or one passes it by more than the slack.
+        if (__any_sync(kFull, mx > (fresh ? -INFINITY : kTop + kSlack))) {
           const bool first = fresh && mx > -INFINITY;
-          const float up = first ? mx : fmaxf(mx, 0.0f);
-          const float al = first ? 1.0f : ex2(-up);  // (a first score: nothing accumulated yet)
+          const float to = ceilf(mx) - kTop, up = first ? to : fmaxf(to, 0.0f);
+          // (a first score: nothing accumulated yet)
+          const float al = first ? 1.0f : up < 127.0f ? __int_as_float((127 - (int)up) << 23) : 0.0f;
           fresh = fresh && !first;
           R += up;
           l *= al;
@@ -632,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
           if (h) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t v[16];
               tmem_ld<16>(tS + 16 * c, v);
               tmem_wait_ld();
@@ -646,12 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
         }
 
-        // weights, their sum, and P in fp16
+        // weights, their sum, and P as fp16 pairs
         const float2 nR2 = make_float2(-R, -R), kf2 = make_float2(kfac, kfac);
         float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
+          uint32_t p[16], rest[16];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             float2 y0 = get(x, 32 * c + 2 * e), y1 = get(x, 32 * c + 2 * e + 2);
@@ -674,10 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
                 p1 = __fmul2_rn(p1, make_float2(f.z, f.w));
               }
             }
-            p[e] = h2_as_u32(__floats2half2_rn(p0.x, p0.y));
-            p[e + 1] = h2_as_u32(__floats2half2_rn(p1.x, p1.y));
+            split2(p0, p[e], rest[e]);
+            split2(p1, p[e + 1], rest[e + 1]);
           }
-          tmem_st<16>(tS + 32 * h + 16 * c, p);
+          tmem_st<16>(tS + 64 * h + 16 * c, p);
+          tmem_st<16>(tS + 64 * h + 32 + 16 * c, rest);
         }
         const float2 ls = __fadd2_rn(l2[0], l2[1]);
         l += ls.x + ls.y;

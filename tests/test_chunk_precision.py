@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from _helpers import kvq
+from _helpers import header_scales, kvq
 from test_chunk_attention import build, run
 from test_norm_rope_read import pool_values
 
@@ -18,9 +18,10 @@ def store(cache, table, b, k, v):
     kvq().kvq_quantize_write(cache, *(torch.from_numpy(x).to(cache.io_dtype).cuda() for x in (k, v)), slots)
 
 
-def values(cache, mode, ks=1.0, vs=1.0):
+def values(cache, mode):
     torch.cuda.synchronize()
-    return pool_values(mode, cache.pool.cpu().numpy(), cache.cfg.num_pages, cache.heads, cache.head_dim, ks, vs)
+    return pool_values(mode, cache.pool.cpu().numpy(), cache.cfg.num_pages, cache.heads, cache.head_dim,
+                       *header_scales(cache))
 
 
 def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 ** -20):
@@ -85,11 +86,45 @@ def test_scores_that_jump_twice_in_a_tile(mode, m, G):
     k[:, 0, 2] += 1.0 * rise * (half == 1)     # the second half alone
     kvq().kvq_cache_set_tensor_scales(cache, 6.0 / (448 if mode == "fp8_per_tensor" else 2688), 5.0 / 2688)
     store(cache, table, 0, k, v)
-    vals = values(cache, mode, *(float(np.float32(x)) for x in (6.0 / (448 if mode == "fp8_per_tensor" else 2688), 5.0 / 2688)))
+    vals = values(cache, mode)
     q = rng.standard_normal((m, G, D)) * 0.3
     for r in range(m * G):
         q[r // G, r % G, r % 3] += 300.0  # times 1 / sqrt(128) and log2 e: 38 a step
     q = torch.from_numpy(q).half().cuda()
     got = run(cache, table, q, [0, m], [n], torch.float16)
     assert kvq().kvq_cache_read_errors(cache) == 0
-    hold(got, *exact_rows(vals, table, q.cpu().numpy(), [0, m], [n], D ** -0.5, weight=2.0 ** -10))  # weights in fp16, rounded twice at most
+    hold(got, *exact_rows(vals, table, q.cpu().numpy(), [0, m], [n], D ** -0.5))
+
+
+def batch(mode, io, out, H, G, D, qlens, lens, shape_v, q_gain=1.0, k_gain=1.0, sink=False, window=0, seed=7):
+    """Sequences whose values are standard normal times shape_v(n) (a factor per token) against the formula; with
+    `sink` the first token takes most of every row's weight."""
+    cache, table, _ = build(mode, io, H, D, lens)
+    rng = np.random.default_rng(seed)
+    for b, n in enumerate(lens):
+        k = rng.standard_normal((n, H, D))
+        if sink:
+            k[0] = 0.9 * np.sqrt(D)  # against queries with a mean of 0.15 sqrt(128 / D): a score of about 17
+        store(cache, table, b, k * k_gain, rng.standard_normal((n, H, D)) * shape_v(n)[:, None, None])
+    vals = values(cache, mode)
+    cu = np.concatenate([[0], np.cumsum(qlens)])
+    dt, odt = (torch.float16 if x == "f16" else torch.float32 for x in (io, out))
+    q = rng.standard_normal((cu[-1], H * G, D)) + (0.15 * np.sqrt(128 / D) if sink else 0.0)
+    q = torch.from_numpy(q * q_gain).to(dt).cuda()
+    scale = D ** -0.5 / (q_gain * k_gain)
+    got = run(cache, table, q, cu, lens, odt, softmax_scale=scale, window=window)
+    assert kvq().kvq_cache_read_errors(cache) == 0
+    hold(got, *exact_rows(vals, table, q.cpu().numpy(), cu, lens, float(np.float32(scale)), window))
+
+
+CHUNK = ([70, 9], [330, 60])
+PROMPT = ([300], [300])  # more than 128 rows
+PT = ["int8_per_token_head", "fp8_per_token_head", "int4_per_token_head"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT + ["fp8_per_tensor", "nvfp4"])
+@pytest.mark.parametrize("lens", [CHUNK, PROMPT], ids=["chunk", "prompt"])
+def test_weights_keep_their_bits(mode, lens):
+    """fp16 outputs are their exact values rounded, give or take 2^-20 of the weights."""
+    batch(mode, "f16", "f16", 1, 2, 128, *lens, lambda n: np.full(n, 0.4))
