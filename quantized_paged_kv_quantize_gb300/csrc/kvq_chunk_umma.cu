@@ -9,10 +9,12 @@
 // remainder rounded: 2^-22 of a weight.  (One fp16 weight instead is an error of the
 // size of the output's own rounding: 2.9e-4 in the 2-norm where an exact result
 // rounded to fp16 is 2.1e-4 off.)  R is a row's reference, a whole number: the largest
-// y + floor(log2 vs) of a tile met, less kTop, moved (O and l rescaled, exactly) only
-// when a block passes it by more than 2^(kTop + kSlack).  Tiles are taken from the
-// nearest tokens to the farthest: a bias by distance then never moves the reference
-// again.
+// y + floor(log2 vs) of the tokens met that the row sees, less kTop, moved (O and l
+// rescaled, exactly) only when one passes it by more than 2^(kTop + kSlack).  So a
+// row's largest P lies between 2^(kTop - 1 - kEven) and 2^15 whatever the scores, the
+// values and the tokens it does not see, and a P below fp16's range is off by 2^-27 of
+// the largest at most.  Tiles are taken from the nearest tokens to the farthest: a bias
+// by distance then never moves the reference again.
 //
 // Roles (16 warps, one CTA per SM; registers are shared out between the warpgroups):
 //  warps 0-3, 4-7  softmax of block 0 and block 1: thread = row, 64 of its 128
@@ -33,9 +35,9 @@
 // S, the 32 of its P rounded and the 32 of the remainders.
 //
 // Bound by the softmax warps' latency and the dequantization beside the tensor cores:
-// 2048 queries of 64 heads over 32768 nvfp4 tokens take 2.14 ms (1.0 PFLOP/s of the formula;
+// 2048 queries of 64 heads over 32768 nvfp4 tokens take 2.15 ms (1.0 PFLOP/s of the formula;
 // the second product runs twice, and the tensor cores are busy for some 70%), three int8
-// prompts of 700 to 2048 tokens, where a CTA's start and end are half of its time, 133 us.
+// prompts of 700 to 2048 tokens, where a CTA's start and end are half of its time, 138 us.
 // With one fp16 weight they took 1.72 ms and 123 us.
 #include <cuda_fp16.h>
 
@@ -71,12 +73,21 @@ struct Smem {
   static constexpr int V = K + 2 * kOpBytes;
   static constexpr int KS = V + 2 * kOpBytes;                      // [slot][128] key scales times kfac
   static constexpr int VS = KS + kSlots * kTok * 4;                // [slot][128] value scales
-  static constexpr int PAGE = VS + kSlots * kTok * 4;              // [slot][8] page states
+  static constexpr int ES = VS + kSlots * kTok * 4;                // [slot][128] their exponents, as floats
+  static constexpr int PAGE = ES + kSlots * kTok * 4;              // [slot][8] the pages' exponents, in short
   static constexpr int START = PAGE + kSlots * 8 * 4;              // [slot] first token of the tile
   static constexpr int BYTES = START + kSlots * 4;
   static constexpr size_t dynamic() { return BYTES + 128; }
 };
-constexpr int kMissing = INT32_MIN;  // page state: not there; else the exponent of its largest value scale
+// A page of a tile, as two 16-bit numbers: its largest exponent of a value scale above, its
+// smallest, negated, below (0 and 0 in the modes without such scales).  kMissing: not there.
+constexpr int kMissing = (int)0x80008000u;
+__device__ __forceinline__ int exponents(int top, int neg_low) { return (top << 16) | (neg_low & 0xFFFF); }
+__device__ __forceinline__ int both_max(int a, int b) { return (int)__vmaxs2((unsigned)a, (unsigned)b); }
+// Where a tile's exponents lie at most this far apart, a row's reference goes by the
+// largest instead of each token's own: that raises it by as many bits of P at most.
+// Three int8 prompts: 138 us so, 145 us token by token.
+constexpr int kEven = 3;
 
 // D[tmem] (+)= A[smem] B[smem]
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
@@ -133,9 +144,6 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   lo = h2_as_u32(__floats2half2_rn(r.x, r.y));
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
-__device__ __forceinline__ int exponent(float x) {  // floor(log2 x), x > 0, clamped
-  return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
-}
 
 // ---------------------------------------------------------------- dequantization of one page by one warp
 // A lane's packed words of a page: K and V.
@@ -304,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   __shared__ int failed_s;
   float* ksm = reinterpret_cast<float*>(sm + L::KS);
   float* vsm = reinterpret_cast<float*>(sm + L::VS);
+  float* esm = reinterpret_cast<float*>(sm + L::ES);
   int* start_s = reinterpret_cast<int*>(sm + L::START);
   int* page_s = reinterpret_cast<int*>(sm + L::PAGE);
 
@@ -418,9 +427,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         valid[u] = pid[u] >= 0 ? min(16, t.n - page(i, u) * 16) : 0;
         if constexpr (PT) {
           if ((lane & 15) >= valid[u]) sc[u] = 0.0f;
-          (lane < 16 ? ksm : vsm)[slot * kTok + 16 * w + (lane & 15)] = lane < 16 ? sc[u] * kfac : sc[u];
-          const uint32_t top = __reduce_max_sync(kFull, lane >= 16 ? __float_as_uint(fabsf(sc[u])) : 0u);
-          if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : top ? exponent(__uint_as_float(top)) : -100;
+          const int at = slot * kTok + 16 * w + (lane & 15);
+          (lane < 16 ? ksm : vsm)[at] = lane < 16 ? sc[u] * kfac : sc[u];
+          const float e = scale_exponent(sc[u]);
+          if (lane >= 16) esm[at] = e;
+          const bool counts = lane >= 16 && (lane & 15) < valid[u];
+          const int top = __reduce_max_sync(kFull, counts ? (int)e : -32768);
+          const int neg_low = __reduce_max_sync(kFull, counts ? -(int)e : -32768);
+          if (lane == 0) page_s[slot * 8 + w] = exponents(top, neg_low);
         } else {
           if (lane == 0) page_s[slot * 8 + w] = pid[u] < 0 ? kMissing : 0;
         }
@@ -545,8 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       const int4 pg0 = *reinterpret_cast<const int4*>(page_s + slot * 8), pg1 = *reinterpret_cast<const int4*>(page_s + slot * 8 + 4);
       const int pmin = min(min(min(pg0.x, pg0.y), min(pg0.z, pg0.w)), min(min(pg1.x, pg1.y), min(pg1.z, pg1.w)));
       const bool masked = pmin == kMissing || !all_see(a, mine, t0, kTok);
-      // exponent of the tile's largest value scale
-      const float ve = PT ? (float)max(max(max(max(pg0.x, pg0.y), max(pg0.z, pg0.w)), max(max(pg1.x, pg1.y), max(pg1.z, pg1.w))), -100) : 0.0f;
+      float ve = 0.0f;     // exponent of the tile's largest value scale
+      bool apart = false;  // exponents are looked at token by token
+      if constexpr (PT) {
+        const int es = both_max(both_max(both_max(pg0.x, pg0.y), both_max(pg0.z, pg0.w)),
+                                both_max(both_max(pg1.x, pg1.y), both_max(pg1.z, pg1.w)));
+        apart = (es >> 16) + (int)(short)es > kEven;
+        ve = apart ? 0.0f : (float)(es >> 16);
+      }
 
       // Half a tile's scores at a time: P of a half goes over columns of S that have
       // been read.
@@ -554,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       for (int h = 0; h < 2; ++h) {
         const float* ks = ksm + slot * kTok + 64 * h;
         const float* vs = vsm + slot * kTok + 64 * h;
+        const float* es = esm + slot * kTok + 64 * h;
         uint32_t x[64];
         tm_ld(tS + 64 * h, x);
         tm_ld(tS + 64 * h + 32, x + 32);
@@ -612,10 +633,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (PT && apart) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 8)
+          for (int e = 0; e < 64; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(es + e);
+            const float2 y0 = __fadd2_rn(get(x, e), make_float2(f.x, f.y)), y1 = __fadd2_rn(get(x, e + 2), make_float2(f.z, f.w));
+            m4[(e >> 1) & 2] = max3(m4[(e >> 1) & 2], y0.x, y0.y);
+            m4[((e >> 1) & 2) + 1] = max3(m4[((e >> 1) & 2) + 1], y1.x, y1.y);
+          }
+        } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+          for (int e = 0; e < 64; e += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+        }
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + ve;
         if constexpr (RAW) mx = fmaf(mx, kfac, -R);  // kfac > 0; ve = 0
 

@@ -29,8 +29,8 @@ def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 **
 
     A score is an fp32 sum of D products (the products are exact: codes of at most 9 bits times fp16, or times the
     halves of an fp32 value), in steps of 16: 16 roundings (2^-23 where sums are cut off) of sum |q k|, four more of the
-    score itself.  A weight is within that, the exponential (2^-22) and its own bits (`weight`: both), or within 2^-30 of
-    the largest weight x value of the row; the sums over n tokens take n / 16 + 16 steps."""
+    score itself.  A weight is within that, the exponential (2^-22) and its own bits (`weight`: both), or within half
+    of fp16's smallest step, 2^-25, where the row's largest is held at 2^2 at least: 2^-27 of weight x value; the sums over n tokens take n / 16 + 16 steps."""
     H, (Hq, D) = vals.shape[3], q.shape[1:]
     want, tol = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
     for b, n in enumerate(lens):
@@ -54,7 +54,7 @@ def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 **
                 ds = ds + weight + (see.sum() / 16 + 16) * 2.0 ** -23
                 mag = w @ np.abs(vv)  # of every channel
                 tol[cu[b] + i, h] = (w * ds) @ np.abs(vv) + (w @ ds) * mag + \
-                    see.sum() * 2.0 ** -30 * (w * np.abs(vv).max(1)).max()
+                    see.sum() * 2.0 ** -27 * (w * np.abs(vv).max(1)).max()
     return want, tol
 
 
@@ -128,3 +128,26 @@ PT = ["int8_per_token_head", "fp8_per_token_head", "int4_per_token_head"]
 def test_weights_keep_their_bits(mode, lens):
     """fp16 outputs are their exact values rounded, give or take 2^-20 of the weights."""
     batch(mode, "f16", "f16", 1, 2, 128, *lens, lambda n: np.full(n, 0.4))
+
+
+# values by token: a factor that falls, grows or scatters by orders of magnitude
+SHAPES = {
+    "small sink": lambda n: np.where(np.arange(n) == 0, 2.0 ** -14, 1.0),
+    "tiny sink": lambda n: np.where(np.arange(n) == 0, 2.0 ** -22, 1.0),
+    "scattered": lambda n: 10.0 ** (6.0 * np.random.default_rng(n).random(n) - 4.0),
+    "last one large": lambda n: np.where(np.arange(n) == n - 1, 6e3, 1e-2),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("lens", [CHUNK, PROMPT], ids=["chunk", "prompt"])
+def test_value_scales_far_apart_fp16(mode, lens, shape):
+    batch(mode, "f16", "f16", 1, 2, 128, *lens, SHAPES[shape], sink="sink" in shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io,out,lens", [("f16", "f16", CHUNK), ("f16", "f16", PROMPT)])
+def test_large_values_below_the_window(io, out, lens):
+    batch("int8_per_token_head", io, out, 1, 4, 128, *lens, lambda n: np.where(np.arange(n) % 48 < 8, 6e3, 1e-2), window=20)
