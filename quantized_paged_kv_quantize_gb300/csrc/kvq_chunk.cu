@@ -15,12 +15,13 @@
 // S = Q K^T, online softmax in base 2 with the running maximum and sum in fp32,
 // O += P V with fp32 accumulators.  fp32 queries enter as an fp16 hi + lo pair
 // under a power of two per row, P always does (22 bits of each weight), so the
-// result keeps fp32 grade.  Per-token value scales reach P relative to the
-// largest one met so far (a power of two, moved with the maximum), which
-// keeps P inside fp16 whatever the values' magnitude.  Bound by the matrix and
-// conversion instructions, which the pairs double: three int8 prompts of 700 to 2048
-// tokens with 32 fp32 heads of 128 take 484 us (42 GFLOP of the formula); four chunks of
-// 60 to 300 tokens with heads of 32, 18 us, mostly latency.
+// result keeps fp32 grade.  The maximum is that of the score plus the exponent of
+// the value's scale, over the tokens that the row sees: its largest P (a weight
+// times a value scale) then lies between 2^(kTop - 1) and 2^(kTop + 1) whatever the
+// magnitudes, and one below fp16's range is off by 2^-38 of the largest at most.
+// Bound by the matrix and conversion instructions, which the pairs double: three int8
+// prompts of 700 to 2048 tokens with 32 fp32 heads of 128 take 560 us (42 GFLOP of the
+// formula); four chunks of 60 to 300 tokens with heads of 32, 15 us, mostly latency.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -35,6 +36,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16 * kWarps;
+
+constexpr float kTop = 14.0f;      // log2 of a row's largest P
+constexpr float kLowest = -3.4e38f;  // a maximum's start: finite (no inf - inf), below every finite score
 
 template <int D>
 constexpr int kTile = D == 128 ? 32 : 64;  // tokens
@@ -56,9 +60,9 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
   hi = h2_as_u32(h);
   lo = h2_as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
 }
-// floor(log2 x) of a positive x, kept to exponents whose powers are normal
+// floor(log2 x) of a positive x, kept to exponents whose powers are normal both ways
 __device__ __forceinline__ int exponent(float x) {
-  return max(-100, min(100, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
+  return max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127));
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -68,8 +72,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   constexpr int J = D / 8, U = KT * J / kThreads;  // 8-channel units per row; units per thread and side
   constexpr bool PT = kPerTokenScale<MODE>;
   __shared__ __align__(16) __half ks[KT * ST], vs[KT * ST];
-  __shared__ float kscale[KT], vscale[KT];
-  __shared__ int vexp_s[2];
+  __shared__ float kscale[KT], vscale[KT], vexp[KT];  // vexp: floor(log2 vscale)
   __shared__ RowTile tile_s;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
@@ -183,8 +186,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
   float o[D / 8][4];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-  float m[2] = {-1e30f, -1e30f}, l[2] = {0.0f, 0.0f};
-  int vexp = -100;  // exponent that P is held relative to
+  float m[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f};
 
   if (i0 < i1) fetch(i0);
   for (int i = i0; i < i1; ++i) {
@@ -204,12 +206,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
       const int k = tid % KT;
       // an absent token (past the sequence, a missing page) is marked by a negative key scale
       sc[k] = tid < KT && !there ? -1.0f : PT ? psc : 1.0f;
-      if constexpr (PT) {
-        if (tid >= KT) {  // whole warps
-          const int e = __reduce_max_sync(kFull, psc > 0.0f ? exponent(psc) : -100);
-          if (lane == 0) vexp_s[(tid - KT) / 32] = e;
-        }
-      }
+      if (PT && tid >= KT) vexp[k] = scale_exponent(psc);
     }
     __syncthreads();
     if (i + 1 < i1) fetch(i + 1);
@@ -241,32 +238,27 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
       for (int e = 0; e < 4; ++e) {
         const int u = e >> 1, k = 8 * n + 2 * tq + (e & 1), tok = t0 + k;
         const float sc = kscale[k];
-        float x = s[n][e] * qfac[u] * (kfac * sc);
+        float x = s[n][e] * (qfac[u] * (kfac * sc));
         if (a.cap > 0.0f) x = a.cap * tanhf(x * rcap);
         x = x * kLog2e;
         if (a.slopes) x -= slope[u] * fabsf((float)(pos[u] - tok));
         if (sc < 0.0f || (masked && !sees[u](tok))) x = -INFINITY;
         s[n][e] = x;
-        mx[u] = fmaxf(mx[u], x);
+        mx[u] = fmaxf(mx[u], PT ? x + vexp[k] : x);
       }
     }
-    const int ve = PT ? (KT == 64 ? max(vexp_s[0], vexp_s[1]) : vexp_s[0]) : vexp;
-    const int vnew = max(vexp, ve);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       mx[u] = fmaxf(warp_max_xor(mx[u], 1, 2), m[u]);
       const float al = ex2(m[u] - mx[u]);
       l[u] *= al;
-      const float av = al * (PT ? pow2(max(vexp - vnew, -126)) : 1.0f);
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
-        o[n][2 * u] *= av;
-        o[n][2 * u + 1] *= av;
+        o[n][2 * u] *= al;
+        o[n][2 * u + 1] *= al;
       }
       m[u] = mx[u];
     }
-    vexp = vnew;
-    const float vnorm = PT ? pow2(-vexp) : 1.0f;
 
     // ---- P (times the value scale), split in fp16, and O += P V
 #pragma unroll
@@ -279,10 +271,10 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float x = s[n][2 * u + e];
-          p[e] = ex2(x - m[u]);
+          p[e] = ex2(x - (m[u] - kTop));
           l[u] += p[e];
           // a weight of zero stays zero whatever the scale of a token that is not seen
-          if constexpr (PT) p[e] = x == -INFINITY ? 0.0f : p[e] * (vscale[8 * n + 2 * tq + e] * vnorm);
+          if constexpr (PT) p[e] = x == -INFINITY ? 0.0f : p[e] * vscale[8 * n + 2 * tq + e];
         }
         split2(p[0], p[1], ph[f], pl[f]);
       }
@@ -303,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     l[u] += __shfl_xor_sync(kFull, l[u], 1);
     l[u] += __shfl_xor_sync(kFull, l[u], 2);
     if (!real[u]) continue;
-    const float f = PT ? pow2(vexp) : vfac;
+    const float f = vfac;  // (1 with per-token scales)
     if (a.num_splits == 1) {
       const float r = f / l[u];  // (a NaN score makes its row NaN; no token seen: 0)
 #pragma unroll

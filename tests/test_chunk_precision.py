@@ -137,6 +137,19 @@ SHAPES = {
     "scattered": lambda n: 10.0 ** (6.0 * np.random.default_rng(n).random(n) - 4.0),
     "last one large": lambda n: np.where(np.arange(n) == n - 1, 6e3, 1e-2),
 }
+FAR = {"last one huge": lambda n: np.where(np.arange(n) == n - 1, 1e6, 1e-2),
+       "growing": lambda n: 10.0 ** np.linspace(-8.0, 8.0, n)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT)
+@pytest.mark.parametrize("io,out,D", [("f32", "f32", 128), ("f32", "f32", 32), ("f16", "f32", 128), ("f16", "f16", 32)])
+@pytest.mark.parametrize("shape", [*SHAPES, *FAR])
+def test_value_scales_far_apart_mma(mode, io, out, D, shape):
+    """Heavy tokens with small values, and large values that most rows do not see."""
+    if io == "f16" and shape in FAR:
+        pytest.skip("outside fp16")
+    batch(mode, io, out, 1, 2, D, *CHUNK, {**SHAPES, **FAR}[shape], sink="sink" in shape)
 
 
 @pytest.mark.gpu
@@ -148,6 +161,6 @@ def test_value_scales_far_apart_fp16(mode, lens, shape):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("io,out,lens", [("f16", "f16", CHUNK), ("f16", "f16", PROMPT)])
+@pytest.mark.parametrize("io,out,lens", [("f32", "f32", CHUNK), ("f16", "f16", CHUNK), ("f16", "f16", PROMPT)])
 def test_large_values_below_the_window(io, out, lens):
     batch("int8_per_token_head", io, out, 1, 4, 128, *lens, lambda n: np.where(np.arange(n) % 48 < 8, 6e3, 1e-2), window=20)
