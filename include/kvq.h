@@ -280,7 +280,12 @@ kvq_status kvq_decode_workspace_bytes(const kvq_cache* cache, int num_seqs, int 
  * GQA: query head h reads kv head h / (num_q_heads / num_kv_heads), which
  * must divide evenly with a group of at most 8.  KVarN: every seq_len must be
  * a multiple of 128 (whole tiles), the query is rotated by the same
- * normalised Hadamard transform and the output rotated back. */
+ * normalised Hadamard transform and the output rotated back.
+ * INT8, FP8 and INT4 per token and head: a weight times its value's scale is
+ * held in steps of 2^-24 (fp32 io; 2^-26, 2^-28 and 2^-22 with fp16 io) and up to
+ * 65504, so values far below 1 lose bits of their weights and fp32 values whose
+ * scale passes 65504 become infinite.  The single tokens of kvq_chunk_attention are
+ * held relative to their values' scales instead. */
 kvq_status kvq_decode_attention(const kvq_cache* cache, const void* q, const int32_t* block_table,
                                 int max_pages, const int32_t* seq_lens, int num_seqs,
                                 int num_q_heads, int max_seq_len, int mode, float softmax_scale,

@@ -38,7 +38,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16 * kWarps;
 
 constexpr float kTop = 14.0f;      // log2 of a row's largest P
-constexpr float kLowest = -3.4e38f;  // a maximum's start: finite (no inf - inf), below every finite score
 
 template <int D>
 constexpr int kTile = D == 128 ? 32 : 64;  // tokens

@@ -143,13 +143,6 @@ __device__ __forceinline__ RowSees row_sees(const ChunkArgs& a, const TokenRange
   return {a.window > 0 ? max(0, pos - a.window + 1) : 0, pos + 1, r.prefix};
 }
 
-// floor(log2) of a per-token value scale, as the reference of a row's weights counts it.
-// A scale of zero (a slot that no write has filled) counts as 2^-100: its token's weight
-// can still exceed the reference by that much without leaving fp32.
-__device__ __forceinline__ float scale_exponent(float vs) {
-  return (float)max(-100, (int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127);
-}
-
 // Merge of the splits of the row tiles (kvq_chunk.cu); `rows`: of a tile.
 cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int rows, cudaStream_t stream);
 

@@ -486,13 +486,16 @@ __device__ void merge_in_cluster(const DecodeArgs& a, long long b, int kvh, cons
 
 // OPT: single tokens of a chunk attention batch -- the query row comes from
 // cu_q, scores may be capped and biased by distance, and tokens below a window
-// (and past a prefix) are not seen.
+// (and past a prefix) are not seen.  There the running reference is that of the
+// score plus the exponent of the token's value scale, over the tokens seen: P
+// times that scale then reaches 2^(PSHIFT + SLACK + 1) at most, and its pair keeps
+// its bits, whatever the values' magnitude.
 template <int MODE, int D, bool QF32, bool OPT = false>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel(const __grid_constant__ DecodeArgs a,
                                                                const __grid_constant__ CUtensorMap tmap) {
   using C = Cfg<MODE, D>;
   constexpr int KSTEPS = C::KSTEPS, MTILES = C::MTILES;
-  constexpr int PSHIFT = C::pshift(QF32);
+  constexpr int PSHIFT = OPT ? (QF32 ? 14 : 10) : C::pshift(QF32);
   constexpr float SLACK = (float)C::slack(QF32);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ uint64_t bars[kWarps][C::STAGES];
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   float o[MTILES][4];
 #pragma unroll
   for (int i = 0; i < MTILES; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-  float m0 = -1e30f, m1 = -1e30f, l0 = 0.0f, l1 = 0.0f;  // finite start: no inf - inf
+  float m0 = OPT ? kLowest : -1e30f, m1 = m0, l0 = 0.0f, l1 = 0.0f;  // finite start: no inf - inf
   bool timed_out = false;
 
   for (int i = 0; i < my_count; i += 2) {
@@ -748,8 +751,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
     }
     // Lazy reference max: move it (and rescale) only when some score exceeds it
     // by more than SLACK -- rare once the first pages are seen.
-    float bm0 = fmaxf(fmaxf(sA[0].x, sA[1].x), fmaxf(sB[0].x, sB[1].x));  // this thread's max, heads 2tq, 2tq+1
-    float bm1 = fmaxf(fmaxf(sA[0].y, sA[1].y), fmaxf(sB[0].y, sB[1].y));
+    float2 zA[2] = {sA[0], sA[1]}, zB[2] = {sB[0], sB[1]};
+    if constexpr (OPT && kPerToken) {
+      const float eA0 = scale_exponent(vA0), eA8 = scale_exponent(vA8), eB0 = scale_exponent(vB0), eB8 = scale_exponent(vB8);
+      zA[0] = __fadd2_rn(sA[0], make_float2(eA0, eA0));
+      zA[1] = __fadd2_rn(sA[1], make_float2(eA8, eA8));
+      zB[0] = __fadd2_rn(sB[0], make_float2(eB0, eB0));
+      zB[1] = __fadd2_rn(sB[1], make_float2(eB8, eB8));
+    }
+    float bm0 = fmaxf(fmaxf(zA[0].x, zA[1].x), fmaxf(zB[0].x, zB[1].x));  // this thread's max, heads 2tq, 2tq+1
+    float bm1 = fmaxf(fmaxf(zA[0].y, zA[1].y), fmaxf(zB[0].y, zB[1].y));
     if (__any_sync(kFull, (bm0 > m0 + SLACK) | (bm1 > m1 + SLACK))) {
 #pragma unroll
       for (int x = 4; x <= 16; x <<= 1) {

@@ -373,6 +373,16 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the SFU (rel. error ~
   return y;
 }
 
+// floor(log2) of a per-token value scale, as the reference of a row's weights counts it.
+// A scale of zero (a slot that no write has filled) counts as 2^-100: its token's weight
+// can still exceed the reference by that much without leaving fp32.
+__device__ __forceinline__ float scale_exponent(float vs) {
+  return (float)max(-100, (int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127);
+}
+
+// A running maximum's start: finite (no inf - inf), below every finite score.
+constexpr float kLowest = -3.4e38f;
+
 // Capped scores: x = cap tanh(u) of u = score / cap.  Up to |u| = 1/2 by an odd polynomial
 // (least squares on Chebyshev points of [0, 1/4] in u^2: 5.6e-8 of the value), which
 // takes no special-function step; elsewhere by 1 - 2 / (1 + e^2u), whose error is about

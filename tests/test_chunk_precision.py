@@ -119,6 +119,7 @@ def batch(mode, io, out, H, G, D, qlens, lens, shape_v, q_gain=1.0, k_gain=1.0, 
 
 CHUNK = ([70, 9], [330, 60])
 PROMPT = ([300], [300])  # more than 128 rows
+SINGLE = ([1, 1, 1], [1, 300, 1500])
 PT = ["int8_per_token_head", "fp8_per_token_head", "int4_per_token_head"]
 
 
@@ -161,6 +162,27 @@ def test_value_scales_far_apart_fp16(mode, lens, shape):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("io,out,lens", [("f32", "f32", CHUNK), ("f16", "f16", CHUNK), ("f16", "f16", PROMPT)])
+@pytest.mark.parametrize("io,out,lens", [("f32", "f32", CHUNK), ("f16", "f16", CHUNK), ("f16", "f16", PROMPT), ("f16", "f16", SINGLE),
+                                         ("f32", "f32", SINGLE)])
 def test_large_values_below_the_window(io, out, lens):
     batch("int8_per_token_head", io, out, 1, 4, 128, *lens, lambda n: np.where(np.arange(n) % 48 < 8, 6e3, 1e-2), window=20)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT)
+@pytest.mark.parametrize("io,out,D", [("f32", "f32", 128), ("f32", "f32", 32), ("f16", "f32", 128), ("f16", "f16", 128)])
+@pytest.mark.parametrize("size", [1e-12, 1e-4, 1e-2, 1.0, 3e3, 1e7, 1e30])
+def test_single_tokens_values_of_any_size(mode, io, out, D, size):
+    if io == "f16" and not 1e-5 < size < 1e4:
+        pytest.skip("outside fp16")
+    batch(mode, io, out, 2, 2, D, *SINGLE, lambda n: np.full(n, size))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT)
+@pytest.mark.parametrize("io", ["f16", "f32"])
+@pytest.mark.parametrize("shape", [*SHAPES, *FAR])
+def test_single_tokens_value_scales_far_apart(mode, io, shape):
+    if io == "f16" and shape in FAR:
+        pytest.skip("outside fp16")
+    batch(mode, io, "f32", 1, 4, 128, *SINGLE, {**SHAPES, **FAR}[shape], sink="sink" in shape)
