@@ -163,13 +163,29 @@ __device__ __forceinline__ void cvt_pair4_biased(uint32_t w, uint32_t& lo, uint3
 }
 
 // Q as the B operand of S^T = K Q^T: b0 = Q[g][d(j,2tq..2tq+1)], b1 = Q[g][d(j,2tq+8..+9)]
-// with d(j, .) = tq*D/4 + 4j + {0,1} and {2,3}.  Heads >= G are zero.
-template <int D, bool QF32>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, long long b, int kvh, int g, int tq, uint32_t (*qh)[2],
-                                       uint32_t (*ql)[2]) {
+// with d(j, .) = tq*D/4 + 4j + {0,1} and {2,3}.  Heads >= G are zero.  SCALED (fp32
+// queries): the row enters times a power of two that brings its largest value to
+// [1, 2), so that its hi + lo pairs keep their bits whatever its magnitude.  Returns
+// the power of two that undoes it (of head g; 1 otherwise).
+template <int D, bool QF32, bool SCALED>
+__device__ __forceinline__ float load_q(const DecodeArgs& a, long long b, int kvh, int g, int tq, uint32_t (*qh)[2],
+                                        uint32_t (*ql)[2]) {
   constexpr int KSTEPS = D / 16;
   const bool ok = g < a.G;
   const long long row = (b * a.Hq + (long long)kvh * a.G + (ok ? g : 0)) * D + tq * (D / 4);
+  int e = 0;
+  if constexpr (SCALED) {
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KSTEPS; ++j) {
+      const float4 u = ok ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row + 4 * j))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
+    }
+    mx = warp_max_xor(mx, 1, 2);
+    if (mx > 0.0f) e = max(-126, min(126, (int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127));
+  }
+  const float by = __int_as_float((127 - e) << 23);
 #pragma unroll
   for (int j = 0; j < KSTEPS; ++j) {
     float x[4];
@@ -177,6 +193,8 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, long long b, int kvh
       const float4 u = ok ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row + 4 * j))
                           : make_float4(0.f, 0.f, 0.f, 0.f);
       x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      if constexpr (SCALED)
+        for (int i = 0; i < 4; ++i) x[i] *= by;
       __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
       const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
       qh[j][0] = h2_as_u32(h0);
@@ -190,6 +208,7 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, long long b, int kvh
       qh[j][1] = u.y;
     }
   }
+  return __int_as_float((127 + e) << 23);
 }
 
 // S^T = K Q^T for NP staged pages, their k-steps interleaved so the pages'
@@ -598,7 +617,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
   // query fragments: in registers, or one copy in shared memory (C::QSMEM)
   __shared__ uint2 qsm[C::QSMEM ? (QF32 ? 2 : 1) * KSTEPS * 32 : 1];
   uint32_t qh[KSTEPS][2], ql[QF32 ? KSTEPS : 1][2];
-  if (!C::QSMEM || warp == 0) load_q<D, QF32>(a, row, kvh, g, tq, qh, ql);
+  constexpr bool kScaledQ = OPT && QF32;
+  __shared__ float qfac_s[kScaledQ ? 8 : 1];
+  float qfac = 1.0f;  // of head g
+  if (!C::QSMEM || warp == 0) qfac = load_q<D, QF32, kScaledQ>(a, row, kvh, g, tq, qh, ql);
   if constexpr (C::QSMEM) {
     if (warp == 0) {
 #pragma unroll
@@ -606,9 +628,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
         qsm[j * 32 + lane] = make_uint2(qh[j][0], qh[j][1]);
         if constexpr (QF32) qsm[(KSTEPS + j) * 32 + lane] = make_uint2(ql[j][0], ql[j][1]);
       }
+      if (kScaledQ && tq == 0) qfac_s[g] = qfac;
     }
     __syncthreads();
   }
+  float2 qf = make_float2(1.0f, 1.0f);  // heads 2tq, 2tq + 1
+  if constexpr (kScaledQ)
+    qf = C::QSMEM ? make_float2(qfac_s[2 * tq], qfac_s[2 * tq + 1])
+                  : make_float2(__shfl_sync(kFull, qfac, 8 * tq), __shfl_sync(kFull, qfac, 8 * tq + 4));
 
   // Scores in log2 units (with a cap: of the cap): s = c * kfac (FP8 per-tensor, NVFP4: the K tensor scale
   // is uniform) or c * ks[t] * softmax_scale*log2(e) (per-token-head).  The
@@ -696,10 +723,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
     };
     if constexpr (kEarlyRefill) refill();
     // (heads 2tq, 2tq + 1 of a token travel as packed f32x2 pairs)
-    float2 sA[2] = {__fmul2_rn(make_float2(cA[0], cA[1]), make_float2(fA0, fA0)),
-                    __fmul2_rn(make_float2(cA[2], cA[3]), make_float2(fA8, fA8))};  // tokens g, g + 8
-    float2 sB[2] = {__fmul2_rn(make_float2(cB[0], cB[1]), make_float2(fB0, fB0)),
-                    __fmul2_rn(make_float2(cB[2], cB[3]), make_float2(fB8, fB8))};
+    auto factor = [&](float f) { return kScaledQ ? __fmul2_rn(qf, make_float2(f, f)) : make_float2(f, f); };
+    float2 sA[2] = {__fmul2_rn(make_float2(cA[0], cA[1]), factor(fA0)),
+                    __fmul2_rn(make_float2(cA[2], cA[3]), factor(fA8))};  // tokens g, g + 8
+    float2 sB[2] = {__fmul2_rn(make_float2(cB[0], cB[1]), factor(fB0)),
+                    __fmul2_rn(make_float2(cB[2], cB[3]), factor(fB8))};
     if constexpr (OPT) {
       if (a.cap_log2 > 0.0f) {
         // (kfac holds 1 / cap)  One branch for a lane's eight scores: 32 nvfp4 tokens take

@@ -186,3 +186,12 @@ def test_single_tokens_value_scales_far_apart(mode, io, shape):
     if io == "f16" and shape in FAR:
         pytest.skip("outside fp16")
     batch(mode, io, "f32", 1, 4, 128, *SINGLE, {**SHAPES, **FAR}[shape], sink="sink" in shape)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["int8_per_token_head", "fp8_per_token_head", "int4_per_token_head"])
+@pytest.mark.parametrize("D", [32, 128])
+@pytest.mark.parametrize("lens", [CHUNK, SINGLE], ids=["chunk", "single"])
+@pytest.mark.parametrize("size", [1e-12, 1e-5, 1e5, 1e12])
+def test_fp32_queries_of_any_size(mode, D, lens, size):
+    batch(mode, "f32", "f32", 2, 2, D, *lens, lambda n: np.ones(n), q_gain=size, k_gain=1.0 / size)
