@@ -26,6 +26,8 @@
 //    floating-point technique for extending the available precision", 1971),
 //    good to about 2^-44, and rounded once (to odd in fp32, then to fp16).
 //  fp32 rows always take the double-word form.
+// Infinities and NaN go by the formula in plain fp32: their products have no rounding
+// error to carry, and a value that is not rotated meets no other.
 //
 // Bound by instruction issue (71% of the slots; DRAM 30%): about 300 instructions
 // for two fp16 head rows, a third of them the double-word path that 35% of the
@@ -156,6 +158,7 @@ __device__ __forceinline__ DW mean_square_dw(const float2* x, float eps) {
     const DW p{__shfl_xor_sync(kFull, t.h, o), __shfl_xor_sync(kFull, t.l, o)}, u = two_sum(t.h, p.h);
     t = {u.h, (t.l + p.l) + u.l};
   }
+  if (!isfinite(t.h)) return {t.h, 0.0f};
   const DW u = two_sum(t.h * (1.0f / D), eps);
   return quick(u.h, u.l + t.l * (1.0f / D));
 }
@@ -172,8 +175,11 @@ __device__ __forceinline__ float rotate_dw(DW a, DW b, float c, float s, bool on
     t = add(p, r);
   }
   const DW m = two_prod(t.h, rs.h);
-  const float l = m.l + (t.h * rs.l + t.l * rs.h);
-  return isfinite(m.h) && isfinite(l) ? round_dw<F16>(quick(m.h, l)) : m.h;  // an infinite or NaN product has no low word
+  return round_dw<F16>(quick(m.h, m.l + (t.h * rs.l + t.l * rs.h)));
+}
+// The same in plain fp32: what a product with an infinity or a NaN is, which has no low word.
+__device__ __forceinline__ float rotate_plain(float a, float b, float c, float s, bool on, float rs) {
+  return (on ? a * c + b * s : a) * rs;
 }
 
 // The correctly rounded rotated row, as its 16 stored bytes.  x: the lane's
@@ -199,13 +205,17 @@ __device__ __forceinline__ uint4 rotate_row(const float2* x, const float2* w, bo
     rs = __frsqrt_rn(t * (1.0f / D) + eps);
   }
   uint32_t lo[N], bad = 0;
+  float2 finite = make_float2(0.0f, 0.0f);  // stays so
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float2 p = mul2(b[i], rot.s[i]), e = fma2(b[i], rot.s[i], neg2(p));
     const float2 z = mul2z(add2(fma2(a[i], rot.c[i], p), e), dup2(rs), nz);  // not rotated: c = 1, s = 0
     lo[i] = half2_rn(mul2(z, dup2(1.0f - 0x1.6p-21f)));
     bad |= lo[i] != half2_rn(mul2(z, dup2(1.0f + 0x1.6p-21f))) ? 1u << i : 0u;
+    finite = fma2(z, make_float2(0.0f, 0.0f), finite);
   }
+  const bool wild = !(finite.x + finite.y == 0.0f);  // a value is infinite or NaN, by itself or through its neighbour here
+  if (wild) bad = (1u << N) - 1;
   if (__any_sync(kFull, bad != 0)) {
     const DW r = norm ? rsqrt_dw(mean_square_dw<D, 8>(x, eps)) : DW{1.0f, 0.0f};
 #pragma unroll
@@ -214,6 +224,16 @@ __device__ __forceinline__ uint4 rotate_row(const float2* x, const float2* w, bo
         lo[i] = half2_rn(make_float2(
             rotate_dw<true>({a[i].x, 0.0f}, {b[i].x, 0.0f}, rot.c[i].x, rot.s[i].x, rot.on, r),
             rotate_dw<true>({a[i].y, 0.0f}, {b[i].y, 0.0f}, rot.c[i].y, rot.s[i].y, rot.on, r)));
+    if (wild) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x0 = rotate_plain(a[i].x, b[i].x, rot.c[i].x, rot.s[i].x, rot.on, r.h);
+        const float x1 = rotate_plain(a[i].y, b[i].y, rot.c[i].y, rot.s[i].y, rot.on, r.h);
+        const uint32_t p = half2_rn(make_float2(x0, x1));
+        if (!isfinite(x0)) lo[i] = prmt(lo[i], p, 0x3254u);
+        if (!isfinite(x1)) lo[i] = prmt(lo[i], p, 0x7610u);
+      }
+    }
   }
   return make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
@@ -229,8 +249,11 @@ __device__ __forceinline__ uint4 rotate_row(const float2* x, const float2* w, bo
   for (int i = 0; i < 4; ++i) {
     const DW b = rot.pairs ? a[i ^ 1]
                            : DW{__shfl_sync(kFull, a[i].h, rot.partner), __shfl_sync(kFull, a[i].l, rot.partner)};
-    const float2 c = rot.c[i >> 1], s = rot.s[i >> 1];
-    z[i] = __float_as_uint(rotate_dw<false>(a[i], b, (i & 1) ? c.y : c.x, (i & 1) ? s.y : s.x, rot.on, r));
+    const float2 c2 = rot.c[i >> 1], s2 = rot.s[i >> 1];
+    const float c = (i & 1) ? c2.y : c2.x, s = (i & 1) ? s2.y : s2.x;
+    float v = rotate_dw<false>(a[i], b, c, s, rot.on, r);
+    if (!isfinite(v)) v = rotate_plain(a[i].h, b.h, c, s, rot.on, r.h);
+    z[i] = __float_as_uint(v);
   }
   return make_uint4(z[0], z[1], z[2], z[3]);
 }
