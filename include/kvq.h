@@ -225,7 +225,8 @@ kvq_status kvq_cache_read(const kvq_cache* cache, const int32_t* slot_mapping, i
  * call are distinct, a negative slot writes nothing to the cache, a slot past
  * the pool sets KVQ_DEVERR_SLOT_RANGE.  The rotated rows are the correctly
  * rounded values of the formula (evaluated to about 2^-44 where fp32 does not
- * settle the rounding).
+ * settle the rounding; fp32 results below 2^-90 only to 2^-22).  Infinities and
+ * NaN follow the formula by IEEE rules; values past rot_dim meet no others.
  * All pointers are device pointers, 16-byte aligned (positions, slot_mapping: 4). */
 typedef struct {
   const void* q;      /* io_dtype, token t's heads at q + t * q_stride: [num_q_heads][head_dim] */

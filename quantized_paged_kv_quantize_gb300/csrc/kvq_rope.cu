@@ -27,7 +27,9 @@
 //    good to about 2^-44, and rounded once (to odd in fp32, then to fp16).
 //  fp32 rows always take the double-word form.
 // Infinities and NaN go by the formula in plain fp32: their products have no rounding
-// error to carry, and a value that is not rotated meets no other.
+// error to carry, and a value that is not rotated meets no other.  An fp32 row whose mean
+// square leaves [2^-80, 2^96], where the low words of squares and roots would leave fp32,
+// is normed times a power of two (a norm is the same for it).
 //
 // Bound by instruction issue (71% of the slots; DRAM 30%): about 300 instructions
 // for two fp16 head rows, a third of them the double-word path that 35% of the
@@ -240,11 +242,28 @@ __device__ __forceinline__ uint4 rotate_row(const float2* x, const float2* w, bo
 template <int D>
 __device__ __forceinline__ uint4 rotate_row(const float2* x, const float2* w, bool norm, float eps,
                                             const Rotation<4>& rot, float2) {  // fp32
-  const DW r = norm ? rsqrt_dw(mean_square_dw<D, 4>(x, eps)) : DW{1.0f, 0.0f};
+  DW r{1.0f, 0.0f};
+  float by = 1.0f;
+  if (norm) {
+    DW ms = mean_square_dw<D, 4>(x, eps);
+    if (__any_sync(kFull, !(ms.h >= 0x1p-80f && ms.h <= 0x1p96f))) {
+      float top = fmaxf(fmaxf(fabsf(x[0].x), fabsf(x[0].y)), fmaxf(fabsf(x[1].x), fabsf(x[1].y)));
+#pragma unroll
+      for (int o = 1; o < D / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      // the larger exponent of the row and of eps's root
+      const int e = max((int)(__float_as_uint(top) >> 23) - 127,
+                        eps > 0.0f ? ((int)(__float_as_uint(eps) >> 23) - 127) >> 1 : -126);
+      if (isfinite(top)) by = __int_as_float((127 - max(-126, min(126, e))) << 23);
+      const float2 scaled[2] = {make_float2(x[0].x * by, x[0].y * by), make_float2(x[1].x * by, x[1].y * by)};
+      ms = mean_square_dw<D, 4>(scaled, eps * by * by);
+    }
+    r = rsqrt_dw(ms);
+  }
   uint32_t z[4];
   DW a[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = (i & 1) ? two_prod(x[i >> 1].y, w[i >> 1].y) : two_prod(x[i >> 1].x, w[i >> 1].x);
+  for (int i = 0; i < 4; ++i)
+    a[i] = (i & 1) ? two_prod(x[i >> 1].y * by, w[i >> 1].y) : two_prod(x[i >> 1].x * by, w[i >> 1].x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const DW b = rot.pairs ? a[i ^ 1]

@@ -1,5 +1,5 @@
-"""kvq_norm_rope_write on rows with infinities and NaN, in the rotated
-part of a row and behind it."""
+"""kvq_norm_rope_write on rows with infinities and NaN, and on fp32 rows whose
+squares leave fp32's range."""
 import numpy as np
 import pytest
 import torch
@@ -66,3 +66,27 @@ def test_infinities_and_nan(io, D, rot, interleaved, norm):
         near = ((z * (1 - 2.0 ** -40)).astype(io) != (z * (1 + 2.0 ** -40)).astype(io)) & np.isfinite(z)
     same = (got == want) | (np.isnan(got) & np.isnan(want)) | near
     assert same.all(), f"{(~same).sum()} of {same.size} values differ from the formula"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, True), (0, False)])
+@pytest.mark.parametrize("size", [2.0 ** -125, 2.0 ** -110, 2.0 ** -70, 1e-12, 1e12, 2.0 ** 70, 2.0 ** 110])
+def test_fp32_rows_of_any_size(rot, interleaved, size):
+    """The squares of 2^+-70 leave fp32's range; the normed rows are of size 1."""
+    rng = np.random.default_rng(3)
+    x = (rng.standard_normal((9, 2, 128)) * size).astype(np.float32)
+    x[4, 1] = 0.0  # with eps 0: 0 / 0
+    w = (1.0 + 0.2 * rng.standard_normal(128)).astype(np.float32)
+    tab = table(rot)
+    pos = rng.integers(0, 50, 9).astype(np.int32)
+    for eps in (1e-6, 1e-30, 0.0):
+        got = rotate(x, w, pos, tab, rot, interleaved, eps)
+        z = formula(x, w, tab[pos], rot, interleaved, eps)
+        assert np.isnan(got[4, 1]).all() if eps == 0.0 else (got[4, 1] == 0.0).all()
+        got[4, 1] = z[4, 1] = 0.0
+        near = (z * (1 - 2.0 ** -40)).astype(np.float32) != (z * (1 + 2.0 ** -40)).astype(np.float32)
+        normal = (np.abs(z) > 2.0 ** -90) | (z == 0)  # below it the low words of the products leave fp32
+        bad = (got != z.astype(np.float32)) & ~near & normal
+        assert not bad.any(), f"{bad.sum()} values are not the rounded formula"
+        # the smallest step, 2^-149, of x w and of the rotated value, times 1 / sqrt(eps) = 2^10 where nothing is scaled
+        assert (np.abs(got - z) <= 2.0 ** -22 * np.abs(z) + 4 * 2.0 ** -139).all()
