@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
   float kfac = OPT && a.cap > 0.0f ? a.scale / a.cap : a.scale * kLog2e, vfac = 1.0f;
   if constexpr (!PT) {
     kfac *= *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
+    if (kfac == 0.0f) kfac = 0x1p-126f;  // (a masked score times it stays -inf)
     vfac = *reinterpret_cast<const float*>(a.pool + kHdrVScaleOffset);
   }
 

@@ -207,3 +207,18 @@ def test_the_output_type_changes_nothing_else(mode, qlens, lens):
     q = torch.from_numpy(np.random.default_rng(2).standard_normal((cu[-1], 8, 128))).half().cuda()
     half, full = (run(cache, table, q, cu, lens, dt) for dt in (torch.float16, torch.float32))
     assert torch.equal(full.half(), half)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["fp8_per_tensor", "nvfp4"])
+@pytest.mark.parametrize("qlens,lens", [([300, 40], [900, 40]), ([1, 1], [500, 3])])
+def test_a_score_factor_that_underflows(mode, qlens, lens):
+    """softmax_scale times the keys' tensor scale below fp32: all scores 0, each row the mean of the values that it sees."""
+    cache, table, _ = build(mode, "f16", 1, 128, lens)
+    ks, vs = header_scales(cache)
+    kvq().kvq_cache_set_tensor_scales(cache, 1e-30, vs)
+    vals = values(cache, mode)
+    cu = np.concatenate([[0], np.cumsum(qlens)])
+    q = torch.from_numpy(np.random.default_rng(2).standard_normal((cu[-1], 2, 128))).half().cuda()
+    got = run(cache, table, q, cu, lens, torch.float32, softmax_scale=1e-30)
+    hold(got, *exact_rows(vals, table, q.cpu().numpy(), cu, lens, 1e-30))
