@@ -343,7 +343,8 @@ typedef struct {
  * and the workspace bytes the call needs for these sizes (0 with one part).
  * max_q_len and max_seq_len are host upper bounds of the chunks and of
  * seq_lens; of `options` (NULL: none) only window and whether prefix_lens is
- * given matter. */
+ * given matter.  Fewer rows may be split into more parts and need more bytes: a
+ * workspace for batches of several sizes is the largest of their plans. */
 kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int num_q_heads, int max_q_len,
                           int max_seq_len, const kvq_attention_options* options, int* num_splits,
                           size_t* workspace_bytes);
