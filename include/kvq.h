@@ -363,7 +363,9 @@ kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int
  * Pages that lie wholly below every window (and past the prefix) are not read,
  * and their block_table entries not looked at.  Calls that may overlap on the
  * GPU need a workspace each.
- * Weights meet the values as pairs of fp16 numbers (2^-22 of a weight).
+ * Weights meet the values as pairs of fp16 numbers (2^-22 of a weight), held
+ * relative to the largest weight times value scale that the row sees, whatever the
+ * magnitudes.  (The value scales of one sequence may be 2^100 apart.)
  * KVarN is not supported (KVQ_ERR_UNSUPPORTED): its open tile lies outside the
  * pages.  A token whose stored value codes or scale are not finite may make every
  * output of its sequence's chunk NaN, those of queries before it too. */

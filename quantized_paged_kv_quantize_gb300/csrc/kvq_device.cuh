@@ -374,12 +374,12 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the SFU (rel. error ~
 }
 
 // floor(log2) of a per-token value scale, as the reference of a row's weights counts it.
-// A scale of zero (a slot that no write has filled) counts as 2^-100: its token's weight
-// can still exceed the reference by that much without leaving fp32.
+// The smallest scale that a write stores is 1e-8 / 448, above 2^-36; a scale of zero (a slot
+// that no write has filled) counts as 2^-40, so that its token's weight and sums of many stay
+// far inside fp32.
 __device__ __forceinline__ float scale_exponent(float vs) {
-  return (float)max(-100, (int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127);
+  return (float)max(-40, (int)((__float_as_uint(vs) >> 23) & 0xFFu) - 127);
 }
-
 // A running maximum's start: finite (no inf - inf), below every finite score.
 constexpr float kLowest = -3.4e38f;
 

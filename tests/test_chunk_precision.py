@@ -24,7 +24,7 @@ def values(cache, mode):
                        *header_scales(cache))
 
 
-def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 ** -20):
+def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 ** -20, slopes=None, prefix=None):
     """The formula in 64 bits and, for every output, a bound on its error.
 
     A score is an fp32 sum of D products (the products are exact: codes of at most 9 bits times fp16, or times the
@@ -39,7 +39,7 @@ def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 **
         m = cu[b + 1] - cu[b]
         for i in range(m):
             p = n - m + i
-            see = (t <= p) & ((t > p - window) if window else True)
+            see = ((t <= p) & ((t > p - window) if window else True)) | (t < (0 if prefix is None else prefix[b]))
             for h in range(Hq):
                 x = q[cu[b] + i, h].astype(np.float64)
                 kk, vv = k[see, h // (Hq // H)], v[see, h // (Hq // H)]
@@ -48,6 +48,9 @@ def exact_rows(vals, table, q, cu, lens, scale, window=0, cap=0.0, weight=2.0 **
                 if cap:
                     s = cap * np.tanh(s / cap)
                     ds = ds + 2.0 ** -22 * cap
+                if slopes is not None:
+                    far = float(slopes[h]) * np.abs(p - t[see])
+                    s, ds = s - far, ds + 4 * 2.0 ** -23 * far
                 w = np.exp(s - s.max())
                 w /= w.sum()
                 want[cu[b] + i, h] = w @ vv
@@ -222,3 +225,32 @@ def test_a_score_factor_that_underflows(mode, qlens, lens):
     q = torch.from_numpy(np.random.default_rng(2).standard_normal((cu[-1], 2, 128))).half().cuda()
     got = run(cache, table, q, cu, lens, torch.float32, softmax_scale=1e-30)
     hold(got, *exact_rows(vals, table, q.cpu().numpy(), cu, lens, 1e-30))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", PT)
+@pytest.mark.parametrize("io,lens", [("f16", CHUNK), ("f16", PROMPT), ("f16", SINGLE), ("f32", CHUNK), ("f32", SINGLE)])
+@pytest.mark.parametrize("cap,window,alibi,pre", [(4.0, 0, False, False), (0.0, 0, True, False), (0.0, 40, False, True), (4.0, 40, True, True)])
+def test_options_with_scattered_values(mode, io, lens, cap, window, alibi, pre):
+    """Caps, biases, windows and prefixes over values six orders of magnitude apart and slots of zero scale."""
+    qlens, lens = lens
+    cache, table, _ = build(mode, io, 1, 128, lens)
+    cache.pool[256:].zero_()
+    rng = np.random.default_rng(5)
+    for b, n in enumerate(lens):
+        k, v = rng.standard_normal((2, n, 1, 128))
+        v *= SHAPES["scattered"](n)[:, None, None]
+        keep = np.arange(n) % 29 != 28  # the others' slots stay zero: zero scores, zero values
+        t = np.arange(n)[keep]
+        slots = torch.from_numpy((table[b, t // 16] * 16 + t % 16).astype(np.int32)).cuda()
+        kvq().kvq_quantize_write(cache, *(torch.from_numpy(x[keep]).to(cache.io_dtype).cuda() for x in (k, v)), slots)
+    vals = values(cache, mode)
+    cu = np.concatenate([[0], np.cumsum(qlens)])
+    q = torch.from_numpy(rng.standard_normal((cu[-1], 2, 128))).to(cache.io_dtype).cuda()
+    slopes = np.array([0.25, 2.0 ** -6], np.float32) if alibi else None
+    prefix = np.array([n // 3 for n in lens], np.int32) if pre else None
+    got = run(cache, table, q, cu, lens, torch.float32, logit_cap=cap, window=window,
+              alibi_slopes=None if slopes is None else torch.from_numpy(slopes).cuda(),
+              prefix_lens=None if prefix is None else torch.from_numpy(prefix).cuda())
+    assert kvq().kvq_cache_read_errors(cache) == 0
+    hold(got, *exact_rows(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5, window, cap, slopes=slopes, prefix=prefix))
