@@ -18,7 +18,7 @@
 // result keeps fp32 grade.  The maximum is that of the score plus the exponent of
 // the value's scale, over the tokens that the row sees: its largest P (a weight
 // times a value scale) then lies between 2^(kTop - 1) and 2^(kTop + 1) whatever the
-// magnitudes, and one below fp16's range is off by 2^-38 of the largest at most.
+// magnitudes (it is rounded up to a whole number, so that no rescale rounds), and one below fp16's range is off by 2^-38 of the largest at most.
 // Bound by the matrix and conversion instructions, which the pairs double: three int8
 // prompts of 700 to 2048 tokens with 32 fp32 heads of 128 take 560 us (42 GFLOP of the
 // formula); four chunks of 60 to 300 tokens with heads of 32, 15 us, mostly latency.
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      mx[u] = fmaxf(warp_max_xor(mx[u], 1, 2), m[u]);
+      mx[u] = fmaxf(ceilf(warp_max_xor(mx[u], 1, 2)), m[u]);  // whole: the rescale is exact
       const float al = ex2(m[u] - mx[u]);
       l[u] *= al;
 #pragma unroll

@@ -795,6 +795,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<MODE, D>::MINB) decode_kernel
         bm0 = fmaxf(bm0, __shfl_xor_sync(kFull, bm0, x));
         bm1 = fmaxf(bm1, __shfl_xor_sync(kFull, bm1, x));
       }
+      if constexpr (OPT) {  // whole: the rescale, and PSHIFT less it, are exact
+        bm0 = ceilf(bm0);
+        bm1 = ceilf(bm1);
+      }
       const float n0 = fmaxf(m0, bm0), n1 = fmaxf(m1, bm1);
       const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // m starts at a finite -1e30
       m0 = n0;
