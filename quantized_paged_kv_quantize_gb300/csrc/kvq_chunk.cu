@@ -20,8 +20,8 @@
 // times a value scale) then lies between 2^(kTop - 1) and 2^(kTop + 1) whatever the
 // magnitudes (it is rounded up to a whole number, so that no rescale rounds), and one below fp16's range is off by 2^-38 of the largest at most.
 // Bound by the matrix and conversion instructions, which the pairs double: three int8
-// prompts of 700 to 2048 tokens with 32 fp32 heads of 128 take 560 us (42 GFLOP of the
-// formula); four chunks of 60 to 300 tokens with heads of 32, 15 us, mostly latency.
+// prompts of 700 to 2048 tokens with 32 fp32 heads of 128 take 480 us (42 GFLOP of the
+// formula); four chunks of 60 to 300 tokens with heads of 32, 18 us, mostly latency.
 #include <cuda_fp16.h>
 
 #include <algorithm>

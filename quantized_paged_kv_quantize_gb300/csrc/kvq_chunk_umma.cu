@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       // The blocks take turns: O += P V of one item, then S of the same block's next
       // (after the products that read P from the same columns).  A second issuing
       // warp, one for each block, mixes the blocks' products and was slower
-      // (2048 queries over 32768 nvfp4 tokens: 2.10 against 1.74 ms).
+      // (2048 queries over 32768 nvfp4 tokens, one fp16 weight: 2.10 against 1.74 ms).
       ok = wait(&bar.q_full, 0);
       for (int k = -2; k < items && ok; ++k) {
         const int b = k & 1;
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
         }
         if constexpr (OPT) {
           if (a.cap > 0.0f) {
-            // (the factors hold 1 / cap)  16 short chunks take 131 us with the polynomial,
-            // 142 us with the other form alone and 90 us without a cap.
+            // (the factors hold 1 / cap)  16 short chunks take 147 us with the polynomial,
+            // 163 us with the other form alone and 104 us without a cap.
             const SoftCap cap{a.cap * kLog2e};
             float t4[4] = {};
 #pragma unroll
