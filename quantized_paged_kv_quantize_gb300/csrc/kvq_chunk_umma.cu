@@ -36,9 +36,10 @@
 //
 // Bound by the softmax warps' latency and the dequantization beside the tensor cores:
 // 2048 queries of 64 heads over 32768 nvfp4 tokens take 2.15 ms (1.0 PFLOP/s of the formula;
-// the second product runs twice, and the tensor cores are busy for some 70%), three int8
+// the second product runs twice, and the tensor cores are busy for 63%), three int8
 // prompts of 700 to 2048 tokens, where a CTA's start and end are half of its time, 138 us.
-// With one fp16 weight they took 1.72 ms and 123 us.
+// With one fp16 weight they took 1.72 ms and 123 us.  Per-token scales cost their loads and
+// products: int8 on the long chunk 3.83 ms.
 #include <cuda_fp16.h>
 
 #include <algorithm>

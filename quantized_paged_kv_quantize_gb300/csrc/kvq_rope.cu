@@ -31,7 +31,7 @@
 // square leaves [2^-80, 2^96], where the low words of squares and roots would leave fp32,
 // is normed times a power of two (a norm is the same for it).
 //
-// Bound by instruction issue (71% of the slots; DRAM 30%): about 300 instructions
+// Bound by instruction issue (73% of the slots; DRAM 33%): about 300 instructions
 // for two fp16 head rows, a third of them the double-word path that 35% of the
 // warps take.  8191 tokens of 64 + 2 x 8 int8 heads: 105 us (3.3 TB/s of the rows in
 // and out and the packed bytes).
