@@ -1,6 +1,6 @@
 // kvq_chunk.cu -- attention of ragged chunks of new tokens over the packed
 // paged cache (kvq_chunk_attention): the plan, the merge of split token ranges,
-// and the mma.sync kernel that takes fp32 queries and head_dim 32.
+// and the mma.sync kernel that takes fp32 queries or outputs and head_dim 32.
 //
 // For query i of a sequence's m new tokens, at position p = n - m + i:
 //   s_t = scale q . k_t,  s_t = cap tanh(s_t / cap),  s_t -= slope_h |p - t|
@@ -406,9 +406,10 @@ cudaError_t launch_chunk_combine(const kvq_cache* c, const ChunkArgs& a, int row
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The tcgen05 kernel takes fp16 queries at head_dim 128.  (The cache alone decides, so
-// that the plan, which knows no output type, is that of the kernel that runs.)
-bool chunk_on_umma(const kvq_cache* c) { return c->cfg.head_dim == 128 && c->cfg.io_dtype == KVQ_F16; }
+// The tcgen05 kernel takes fp16 in and out at head_dim 128.
+bool chunk_on_umma(const kvq_cache* c, int out_dtype) {
+  return c->cfg.head_dim == 128 && c->cfg.io_dtype == KVQ_F16 && out_dtype == KVQ_F16;
+}
 
 // Splits of the token ranges, and the workspace.  The lengths are on the device:
 // every tile of rows is taken to see max_seq_len tokens (a window bounds what
@@ -429,10 +430,10 @@ ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_he
     p.workspace_bytes = p.decode.workspace_bytes;
     return p;
   }
-  const bool umma = chunk_on_umma(c);
+  const bool umma = chunk_on_umma(c, KVQ_F16);
   const int rows = umma ? kUmmaRows : kRows;
   // tokens a CTA takes at a time: the tcgen05 kernel runs two tiles at once for up to 128 rows
-  const int kt = !umma ? (D == 128 ? kTile<128> : kTile<32>) : (long long)max_q_len * G <= 128 ? 256 : 128;
+  const int kt = !umma ? kTile<32> : (long long)max_q_len * G <= 128 ? 256 : 128;
   const long long slots = (umma ? 1ll : 4ll) * num_sms();  // CTAs side by side
   constexpr long long kCost = 4;                         // start-up, merge and partials of a CTA, in such tiles
   long long len = max_seq_len;
@@ -490,7 +491,7 @@ cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkC
   a.out_span = Span{o, o + rows * D * (a.out_f32 ? 4 : 2)};
   uint8_t* w = static_cast<uint8_t*>(k.workspace);
   a.ws_span = Span{w, w ? w + plan.workspace_bytes : nullptr};
-  if (chunk_on_umma(c)) {
+  if (chunk_on_umma(c, k.out_dtype)) {
     cudaError_t e = launch_chunk_umma(c, a, stream);
     if (e != cudaSuccess || a.num_splits == 1) return e;
     return launch_chunk_combine(c, a, kUmmaRows, stream);

@@ -1,6 +1,6 @@
 // kvq_chunk_umma.cu -- chunk attention on the 5th-generation tensor cores
-// (tcgen05, scores, weights and accumulators in tensor memory) for fp16 queries at
-// head_dim 128, all 16-token-page modes.
+// (tcgen05, scores, weights and accumulators in tensor memory) for fp16 queries
+// and outputs at head_dim 128, all 16-token-page modes.
 //
 // Mathematics (kvq_chunk.cu has the operator's definition).  With codes K, V
 // (exact in fp16) and scales apart, one 128 x 128 block of (row, token) pairs is
@@ -779,13 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
       }
       if ((!two || blk == 0) && row < ((t.count + 31) & ~31)) {  // whole warps
         // Rows leave through shared memory (Q's place, free now), so that each store
-        // of a warp writes two whole rows of 256 bytes: 128 halves, or 64 floats of an
-        // fp32 output or of a partial result.  Thread by row, 16 bytes each, a store
-        // touches 32 half sectors.
+        // of a warp writes two whole rows of 256 bytes: 128 halves, or 64 of a partial
+        // result's floats.  Thread by row, 16 bytes each, a store touches 32 half sectors.
         const int rel = (rr / a.G - t.r0 / a.G) * a.Hq + kvh * a.G + rr % a.G;
         const long long q_base = (long long)(t.q0 + t.r0 / a.G) * a.Hq;
         const float g = a.num_splits > 1 ? vfac : vfac / l;
-        const bool wide = a.num_splits > 1 || a.out_f32;
         const int rows = min(32, t.count - (row - lane));
         uint8_t* stage = sm + L::Q + warp * kStageBytes;
         auto flush = [&](auto store) {
@@ -819,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * g;  // (a NaN score makes its row NaN)
-          if (!wide) {
+          if (a.num_splits == 1) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
               *reinterpret_cast<uint4*>(stage + lane * kStageRow + 64 * c + 2 * e) =
@@ -831,14 +829,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_umma_kernel(const __grid_co
               *reinterpret_cast<float4*>(stage + lane * kStageRow + 128 * (c & 1) + 4 * e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             if (c & 1)
               flush([&](long long qrow, int j, uint4 x) {
-                if (a.num_splits > 1)
-                  st_chk(reinterpret_cast<uint4*>(a.ws_o + (qrow * a.num_splits + split) * kD + 64 * (c >> 1)) + j, x, a.ws_span, a.pool);
-                else
-                  st_chk(reinterpret_cast<uint4*>(static_cast<float*>(a.out) + qrow * kD + 64 * (c >> 1)) + j, x, a.out_span, a.pool);
+                st_chk(reinterpret_cast<uint4*>(a.ws_o + (qrow * a.num_splits + split) * kD + 64 * (c >> 1)) + j, x, a.ws_span, a.pool);
               });
           }
         }
-        if (!wide)
+        if (a.num_splits == 1)
           flush([&](long long qrow, int j, uint4 x) {
             st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + qrow * kD) + j, x, a.out_span, a.pool);
           });

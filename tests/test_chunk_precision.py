@@ -201,18 +201,6 @@ def test_fp32_queries_of_any_size(mode, D, lens, size):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("mode", ["int8_per_token_head", "nvfp4"])
-@pytest.mark.parametrize("qlens,lens", [([300, 40], [900, 40]), ([300, 300], [300, 300]), ([8] * 100, [130] * 100), ([1, 1], [500, 3])])
-def test_the_output_type_changes_nothing_else(mode, qlens, lens):
-    """fp32 outputs of fp16 queries take the kernel, and the parts, that the plan was made for."""
-    cache, table, _ = build(mode, "f16", 1, 128, lens)
-    cu = np.concatenate([[0], np.cumsum(qlens)])
-    q = torch.from_numpy(np.random.default_rng(2).standard_normal((cu[-1], 8, 128))).half().cuda()
-    half, full = (run(cache, table, q, cu, lens, dt) for dt in (torch.float16, torch.float32))
-    assert torch.equal(full.half(), half)
-
-
-@pytest.mark.gpu
 @pytest.mark.parametrize("mode", ["fp8_per_tensor", "nvfp4"])
 @pytest.mark.parametrize("qlens,lens", [([300, 40], [900, 40]), ([1, 1], [500, 3])])
 def test_a_score_factor_that_underflows(mode, qlens, lens):
