@@ -339,8 +339,9 @@ typedef struct {
   const int32_t* prefix_lens;  /* device [num_seqs], or NULL */
 } kvq_attention_options;
 
-/* Plan of a chunk attention: the parts a sequence's token range is split into,
- * and the workspace bytes the call needs for these sizes (0 with one part).
+/* Plan of a chunk attention: the parts a sequence's token range is split into
+ * (for outputs of the cache's io_dtype), and the workspace bytes the call needs for
+ * these sizes with either output type (0 where neither has more than one part).
  * max_q_len and max_seq_len are host upper bounds of the chunks and of
  * seq_lens; of `options` (NULL: none) only window and whether prefix_lens is
  * given matter.  Fewer rows may be split into more parts and need more bytes: a

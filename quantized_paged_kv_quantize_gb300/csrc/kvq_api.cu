@@ -509,7 +509,8 @@ kvq_status kvq_chunk_plan(const kvq_cache* cache, int total_q, int num_seqs, int
   kvq_status s = check_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len, options);
   if (s) return s;
   const kvq::ChunkPlan p = kvq::plan_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len,
-                                           options ? options->window : 0, options && options->prefix_lens);
+                                           options ? options->window : 0, options && options->prefix_lens,
+                                           cache->cfg.io_dtype);
   if (num_splits) *num_splits = p.num_splits;
   if (workspace_bytes) *workspace_bytes = p.workspace_bytes;
   return KVQ_OK;
@@ -539,7 +540,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_
   k.window = options ? options->window : 0;
   k.prefix_lens = options ? options->prefix_lens : nullptr;
   const kvq::ChunkPlan p = kvq::plan_chunk(cache, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len, k.window,
-                                           k.prefix_lens != nullptr);
+                                           k.prefix_lens != nullptr, out_dtype);
   if (p.workspace_bytes > 0) {
     if (!workspace || workspace_bytes < p.workspace_bytes)
       return fail(KVQ_ERR_CAPACITY, "workspace needs %zu bytes, got %zu", p.workspace_bytes,

@@ -411,16 +411,43 @@ bool chunk_on_umma(const kvq_cache* c, int out_dtype) {
   return c->cfg.head_dim == 128 && c->cfg.io_dtype == KVQ_F16 && out_dtype == KVQ_F16;
 }
 
-// Splits of the token ranges, and the workspace.  The lengths are on the device:
-// every tile of rows is taken to see max_seq_len tokens (a window bounds what
-// it sees).  A plan of s splits is estimated at
+// Splits of the token ranges.  The lengths are on the device: every tile of rows is
+// taken to see max_seq_len tokens (a window bounds what it sees).  A plan of s splits is
+// estimated at
 //   ceil(units s / slots) waves x (token tiles / s + cost of a CTA)
 // as for the decode kernels; more splits than one are worth their partials'
 // way through memory only where a wave is not full or its last one is ragged.
+int chunk_parts(bool umma, int D, int G, int Hkv, int total_q, int num_seqs, int max_q_len, int max_seq_len, int window,
+                bool has_prefix) {
+  const int rows = umma ? kUmmaRows : kRows;
+  // tokens a CTA takes at a time: the tcgen05 kernel runs two tiles at once for up to 128 rows
+  const int kt = !umma ? (D == 128 ? kTile<128> : kTile<32>) : (long long)max_q_len * G <= 128 ? 256 : 128;
+  const long long slots = (umma ? 1ll : 4ll) * num_sms();  // CTAs side by side
+  const long long cost_cta = !umma && D == 128 ? 8 : 4;    // start-up, merge and partials of a CTA, in such tiles
+  long long len = max_seq_len;
+  if (window > 0 && !has_prefix) len = std::min<long long>(len, (long long)window + max_q_len + kt);
+  const long long tiles = (len + kt - 1) / kt;
+  const long long per_seq = ((long long)max_q_len * G + rows - 1) / rows;
+  long long units = ((long long)total_q * G + rows - 1) / rows + num_seqs / 2;
+  units = std::min(units, per_seq * num_seqs) * Hkv;
+  long long best = -1;
+  int parts = 1;
+  for (long long s = 1; s <= 32 && s <= std::max(1ll, tiles); ++s) {
+    const long long cost = (units * s + slots - 1) / slots * ((tiles + s - 1) / s + cost_cta);
+    if (best < 0 || cost < best) {
+      best = cost;
+      parts = (int)s;
+    }
+  }
+  return parts;
+}
+
+// The splits are those of the kernel that the output's type chooses; the workspace, which
+// a caller asks for without naming that type, serves the other one too.
 ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_heads, int max_q_len, int max_seq_len,
-                     int window, bool has_prefix) {
+                     int window, bool has_prefix, int out_dtype) {
   ChunkPlan p;
-  const int D = c->cfg.head_dim, G = num_q_heads / c->cfg.num_kv_heads;
+  const int D = c->cfg.head_dim, Hkv = c->cfg.num_kv_heads;
   if (max_q_len <= 1 && num_seqs <= 65535) {  // single tokens: the decode kernels (one grid row per sequence)
     int len = max_seq_len;
     if (window > 0 && !has_prefix) len = (int)std::min<long long>(len, (long long)window + 15);
@@ -430,28 +457,13 @@ ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_he
     p.workspace_bytes = p.decode.workspace_bytes;
     return p;
   }
-  const bool umma = chunk_on_umma(c, KVQ_F16);
-  const int rows = umma ? kUmmaRows : kRows;
-  // tokens a CTA takes at a time: the tcgen05 kernel runs two tiles at once for up to 128 rows
-  const int kt = !umma ? kTile<32> : (long long)max_q_len * G <= 128 ? 256 : 128;
-  const long long slots = (umma ? 1ll : 4ll) * num_sms();  // CTAs side by side
-  constexpr long long kCost = 4;                         // start-up, merge and partials of a CTA, in such tiles
-  long long len = max_seq_len;
-  if (window > 0 && !has_prefix) len = std::min<long long>(len, (long long)window + max_q_len + kt);
-  const long long tiles = (len + kt - 1) / kt;
-  const long long per_seq = ((long long)max_q_len * G + rows - 1) / rows;
-  long long units = ((long long)total_q * G + rows - 1) / rows + num_seqs / 2;
-  units = std::min(units, per_seq * num_seqs) * c->cfg.num_kv_heads;
-  long long best = -1;
-  for (long long s = 1; s <= 32 && s <= std::max(1ll, tiles); ++s) {
-    const long long cost = (units * s + slots - 1) / slots * ((tiles + s - 1) / s + kCost);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.num_splits = (int)s;
-    }
-  }
-  if (p.num_splits > 1)
-    p.workspace_bytes = (size_t)total_q * num_q_heads * p.num_splits * (D + 2) * sizeof(float);
+  auto parts = [&](int out) {
+    return chunk_parts(chunk_on_umma(c, out), D, num_q_heads / Hkv, Hkv, total_q, num_seqs, max_q_len, max_seq_len, window,
+                       has_prefix);
+  };
+  p.num_splits = parts(out_dtype);
+  const int most = std::max(parts(KVQ_F16), parts(KVQ_F32));
+  if (most > 1) p.workspace_bytes = (size_t)total_q * num_q_heads * most * (D + 2) * sizeof(float);
   return p;
 }
 

@@ -71,7 +71,7 @@ struct ChunkCall {
   float scale, cap;
 };
 ChunkPlan plan_chunk(const kvq_cache* c, int total_q, int num_seqs, int num_q_heads, int max_q_len, int max_seq_len,
-                     int window, bool has_prefix);
+                     int window, bool has_prefix, int out_dtype);
 cudaError_t launch_chunk(const kvq_cache* c, const ChunkPlan& plan, const ChunkCall& k, cudaStream_t stream);
 
 // num_seqs counts sequences; each has num_queries query rows (multi-query decode).

@@ -242,3 +242,21 @@ def test_options_with_scattered_values(mode, io, lens, cap, window, alibi, pre):
               prefix_lens=None if prefix is None else torch.from_numpy(prefix).cuda())
     assert kvq().kvq_cache_read_errors(cache) == 0
     hold(got, *exact_rows(vals, table, q.cpu().numpy(), cu, lens, 128 ** -0.5, window, cap, slopes=slopes, prefix=prefix))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,G,qlens,n", [(1, 8, [8] * 100, 4000), (2, 3, [40] * 7, 900), (8, 4, [700], 700), (1, 1, [300, 2], 9000)])
+def test_the_workspace_serves_both_output_types(H, G, qlens, n):
+    """fp32 outputs of fp16 queries take the kernel that fp32 queries take, in as many parts, so they need as much."""
+    K = kvq()
+    need = []
+    for dt in (torch.float16, torch.float32):
+        cfg = K.make_config(1, 16, H, 128, "int8_per_token_head", dt)
+        cache = K.kvq_cache_alloc(cfg, torch.zeros(K.kvq_cache_bytes(cfg), dtype=torch.uint8, device="cuda"))
+        need.append(K.kvq_chunk_plan(cache, sum(qlens), len(qlens), H * G, max_q_len=max(qlens), max_seq_len=n)[2])
+    assert need[0] >= need[1]
+    cache, table, _ = build("int8_per_token_head", "f16", H, 128, [n])
+    q = torch.zeros(sum(qlens), H * G, 128, device="cuda", dtype=torch.float16)
+    cu = np.concatenate([[0], np.cumsum(qlens)])
+    for dt in (torch.float16, torch.float32):  # (guarded workspaces of just the planned size)
+        run(cache, np.repeat(table, len(qlens), 0), q, cu, [n] * len(qlens), dt)
