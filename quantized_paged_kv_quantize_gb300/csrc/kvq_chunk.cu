@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_chunk.cuh"
 #include "kvq_unpack.cuh"
@@ -260,9 +261,9 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     }
 
     // ---- P (times the value scale), split in fp16, and O += P V
+    uint32_t ph[KT / 16][4], pl[KT / 16][4];
 #pragma unroll
     for (int j = 0; j < KT / 16; ++j) {
-      uint32_t ph[4], pl[4];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const int n = 2 * j + (f >> 1), u = f & 1;
@@ -275,18 +276,38 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
           // a weight of zero stays zero whatever the scale of a token that is not seen
           if constexpr (PT) p[e] = x == -INFINITY ? 0.0f : p[e] * vscale[8 * n + 2 * tq + e];
         }
-        split2(p[0], p[1], ph[f], pl[f]);
-      }
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        uint32_t b[4];
-        ldsm4_t(b, vs + (16 * j + (lane & 15)) * ST + 16 * n + 8 * (lane >> 4));
-        mma16816(o[2 * n], ph, b[0], b[1]);
-        mma16816(o[2 * n + 1], ph, b[2], b[3]);
-        mma16816(o[2 * n], pl, b[0], b[1]);
-        mma16816(o[2 * n + 1], pl, b[2], b[3]);
+        split2(p[0], p[1], ph[j][f], pl[j][f]);
       }
     }
+    // The products cut their sums off, up to 2^-23 of O at each.  Over a range of more than
+    // 2048 tokens a tile's are summed from zero and added to O with rounding (1024 queries
+    // over 32768 tokens: 7e-7 instead of 1e-5 of the result, 6% slower); in a shorter one
+    // the cuts come to 128 x 2^-23 where all values have one sign, and 1e-6 as a rule.
+    auto pv = [&](auto anew) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        float c0[4] = {}, c1[4] = {};
+        float *x0 = anew ? c0 : o[2 * n], *x1 = anew ? c1 : o[2 * n + 1];
+#pragma unroll
+        for (int j = 0; j < KT / 16; ++j) {
+          uint32_t b[4];
+          ldsm4_t(b, vs + (16 * j + (lane & 15)) * ST + 16 * n + 8 * (lane >> 4));
+          mma16816(x0, ph[j], b[0], b[1]);
+          mma16816(x1, ph[j], b[2], b[3]);
+          mma16816(x0, pl[j], b[0], b[1]);
+          mma16816(x1, pl[j], b[2], b[3]);
+        }
+        if (anew) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * n][e] += c0[e];
+            o[2 * n + 1][e] += c1[e];
+          }
+        }
+      }
+    };
+    if ((i1 - i0) * KT > 2048) pv(std::true_type{});
+    else pv(std::false_type{});
   }
 
 #pragma unroll

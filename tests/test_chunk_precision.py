@@ -260,3 +260,23 @@ def test_the_workspace_serves_both_output_types(H, G, qlens, n):
     cu = np.concatenate([[0], np.cumsum(qlens)])
     for dt in (torch.float16, torch.float32):  # (guarded workspaces of just the planned size)
         run(cache, np.repeat(table, len(qlens), 0), q, cu, [n] * len(qlens), dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["int8_per_token_head", "fp8_per_tensor"])
+@pytest.mark.parametrize("io,D,m", [("f16", 128, 40), ("f32", 128, 40), ("f32", 32, 40)])
+def test_sums_over_many_tokens(mode, io, D, m):
+    """fp32 means over 20000 values near 1: at most 256 of a row's additions in a row are cut off, by 2^-23 of a sum that
+    grows evenly, which makes 128 x 2^-23; weights and the other additions are within 2^-18."""
+    H, B, n = 8, 20, 20000  # enough rows that a range is not split much; all sequences read the same pages
+    K = kvq()
+    cache, table, _ = build(mode, io, H, D, [n])
+    K.kvq_cache_set_tensor_scales(cache, 1.0, 2.0 / 448)
+    v = 1.0 + 0.1 * np.random.default_rng(1).standard_normal((n, H, D))
+    store(cache, table, 0, np.zeros((n, H, D)), v)
+    vals = values(cache, mode)[1][table[0, np.arange(n) // 16], np.arange(n) % 16]
+    q = torch.randn(B * m, 2 * H, D, device="cuda").to(cache.io_dtype)
+    got = run(cache, np.repeat(table, B, 0), q, np.arange(0, B * m + 1, m), [n] * B, torch.float32)
+    want = (np.cumsum(vals, 0) / np.arange(1, n + 1)[:, None, None])[n - m:]
+    err = np.abs(got.double().cpu().numpy().reshape(B, m, H, 2, D) - want[None, :, :, None]) / want[None, :, :, None]
+    assert err.max() <= 128 * 2.0 ** -23 + 2.0 ** -18, f"{err.max():.3g}"
