@@ -85,9 +85,9 @@ typedef enum { KVQ_F16 = 0, KVQ_F32 = 1 } kvq_dtype;
 #define KVQ_DEVERR_SEQ_LEN 0x8u      /* a seq_len above max_seq_len or max_pages * page_size */
 #define KVQ_DEVERR_TIMEOUT 0x10u     /* a bounded wait on a copy ran out (work skipped) */
 #define KVQ_DEVERR_SEQ_ID 0x20u      /* kvq_kvarn_append: a seq_id outside [0, num_seqs) */
-#define KVQ_DEVERR_POSITION 0x80u    /* kvq_norm_rope_write: a position outside [0, max_position) */
-#define KVQ_DEVERR_QUERY_RANGE 0x100u /* kvq_chunk_attention: cu_q_lens of a sequence not an ascending range of at
-                                        most max_q_len rows of the batch */
+#define KVQ_DEVERR_POSITION 0x80u    /* kvq_norm_rope_write, kvq_latent_write: a position outside [0, max_position) */
+#define KVQ_DEVERR_QUERY_RANGE 0x100u /* kvq_chunk_attention and the latent calls: cu_q_lens (or cu_k_lens) of a
+                                        sequence not an ascending range of at most max_q_len rows of the batch */
 #define KVQ_DEVERR_BOUNDS 0x40u      /* debug build only: a store fell outside the buffer its
                                         arguments describe (skipped); see kvq_debug_build */
 
@@ -378,6 +378,154 @@ kvq_status kvq_chunk_attention(const kvq_cache* cache, const void* q, int total_
                                int num_q_heads, int max_q_len, int max_seq_len, int mode, float softmax_scale,
                                const kvq_attention_options* options, void* out, int out_dtype, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ---- Latent caches ---------------------------------------------------------
+ * A cache of one latent vector c_t (latent_dim values) and one rotated key part
+ * r_t (rope_dim values) per token, shared by all query heads: with head h's
+ * up-projections U_h (keys) and W_h (values), k_th = [U_h c_t, r_t] and
+ * v_th = W_h c_t.  Attention reads it in either of two forms:
+ *   absorbed   q' = [U_h^T q_h, q_rope]; scores q' . [c_t, r_t], outputs sum p_t c_t,
+ *              which W_h takes to the head's values: kvq_latent_attention, over the
+ *              paged latents, keys and values at once;
+ *   expanded   the heads' own keys and values: kvq_latent_prompt_attention, over dense
+ *              rows (kvq_latent_read gives the latents that a context has cached).
+ * The latents are quantized as a row of kvq_quantize_write is, one scale per token
+ * (or per tensor, or per 16 values); the rotary part is held in fp16.
+ *
+ * Pool layout: the 256-byte header, then one block per page of 16 tokens:
+ *   FP8 per-tensor  : codes[16][L] e4m3 | rope[16][R] f16
+ *   INT8 / FP8 PTH  : codes[16][L]      | rope[16][R] f16 | scale[16] f32
+ *   NVFP4, 4over6   : codes[16][L/2]    | rope[16][R] f16 | s_b[16][L/16] e4m3
+ * NVFP4 codes: the even index in the low nibble.  The header is that of the other
+ * pools, the tensor scale at byte 16, the device error word at byte 12. */
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;  /* 16 */
+  int32_t latent_dim; /* L: 256 or 512 */
+  int32_t rope_dim;   /* R: 64 */
+  int32_t mode;       /* kvq_mode: FP8 per-tensor, INT8 or FP8 per-token(-head), NVFP4, NVFP4 4over6 */
+  int32_t io_dtype;   /* kvq_dtype of the rows written and of the queries */
+} kvq_latent_config;
+
+typedef struct kvq_latent kvq_latent;
+
+/* As kvq_cache_bytes, kvq_cache_alloc, kvq_cache_free and kvq_cache_read_errors; the
+ * conventions on pointers, streams and errors are the same.  The handle is of its own
+ * type: the calls above do not take it. */
+kvq_status kvq_latent_bytes(const kvq_latent_config* cfg, size_t* bytes);
+kvq_status kvq_latent_alloc(const kvq_latent_config* cfg, void* dev_buf, size_t bytes, kvq_latent** out);
+kvq_status kvq_latent_free(kvq_latent* cache);
+kvq_status kvq_latent_read_errors(kvq_latent* cache, uint32_t* flags, int clear, void* stream);
+
+/* The per-tensor scale of FP8 per-tensor (s) and the NVFP4 modes (s_t), on `stream`: a
+ * host value (finite, > 0), or from a device amax (kvq_tensor_amax): amax/448, amax/2688,
+ * 1 for 0. */
+kvq_status kvq_latent_set_scale(kvq_latent* cache, float scale, void* stream);
+kvq_status kvq_latent_set_scale_from_amax(kvq_latent* cache, const float* dev_amax, void* stream);
+
+/* Norm, rotation and quantized write of new tokens in one pass.  For token i
+ *   c = x w / sqrt(mean(x^2) + eps)   (c = x where latent_weight is NULL)
+ * and the rotary parts of its key and of its queries' heads are rotated by the table
+ * row of its position, in half-split or interleaved pairs, as by kvq_norm_rope_write
+ * with rot_dim = rope_dim.  Every result is the correctly rounded value in io_dtype;
+ * the latent codes are those of that rounded row, and the key part is rounded from
+ * there to fp16 (io_dtype fp32; beyond 65504 it becomes infinite).
+ * The slots of one call are distinct; a negative slot writes nothing to the cache, one
+ * past the pool sets KVQ_DEVERR_SLOT_RANGE; a position outside [0, max_position) skips its
+ * token (all of its rows stay as they were) and sets KVQ_DEVERR_POSITION.  Rows and strides
+ * are multiples of 16 bytes, in elements of io_dtype.  An output may be its own input. */
+typedef struct {
+  const void* latent;        /* [latent_dim] of token i at latent + i * latent_stride */
+  const void* k_rope;        /* [rope_dim] at k_rope + i * k_rope_stride */
+  const void* q_rope;        /* [rope_dim] of head h at q_rope + i * q_stride + h * q_head_stride, or NULL */
+  void* q_rope_out;          /* likewise, by q_out_stride and q_out_head_stride: e.g. the tails of the absorbed
+                                queries' rows; with q_rope only */
+  int64_t latent_stride;
+  int64_t k_rope_stride;
+  int64_t q_stride, q_head_stride;
+  int64_t q_out_stride, q_out_head_stride;
+  const void* latent_weight; /* [latent_dim] io_dtype, or NULL: no norm */
+  const int32_t* positions;  /* [num_tokens] */
+  const float* cos_sin;      /* [max_position][rope_dim]: rope_dim/2 cosines, then rope_dim/2 sines */
+  const int32_t* slot_mapping; /* [num_tokens], or NULL: the cache is not written */
+  void* latent_out;          /* [num_tokens][latent_dim] io_dtype, dense, or NULL */
+  void* k_rope_out;          /* [num_tokens][rope_dim] io_dtype, dense, or NULL */
+  int32_t num_tokens;
+  int32_t num_q_heads;       /* of q_rope */
+  int32_t max_position;
+  int32_t interleaved;
+  float eps;                 /* >= 0 */
+} kvq_latent_rows;
+kvq_status kvq_latent_write(kvq_latent* cache, const kvq_latent_rows* r, int mode, void* stream);
+
+/* The values the cache holds at `slot_mapping`, as by kvq_cache_read: latent_out
+ * [num_tokens][latent_dim] and rope_out [num_tokens][rope_dim] in out_dtype; either may
+ * be NULL. */
+kvq_status kvq_latent_read(const kvq_latent* cache, const int32_t* slot_mapping, int num_tokens, void* latent_out,
+                           void* rope_out, int out_dtype, void* stream);
+
+/* Absorbed attention of ragged chunks of queries (a chunk of one is a decode step) over
+ * the paged latents, which already hold the chunks' own tokens.  Query i of a
+ * sequence's m stands at position seq_len - m + i and attends to the tokens up to it, or,
+ * with causal = 0, to all of the sequence's tokens:
+ *   s_t = softmax_scale (q[0..L) . c_t + q[L..L+R) . r_t),  out = sum softmax(s)_t c_t
+ *  q            device [total_q][num_q_heads][latent_dim + rope_dim], io_dtype
+ *  cu_q_lens    device int32 [num_seqs + 1], as for kvq_chunk_attention
+ *  block_table  device int32 [num_seqs][max_pages]
+ *  seq_lens     device int32 [num_seqs], at most max_seq_len <= max_pages * 16
+ *  out          device [total_q][num_q_heads][latent_dim], out_dtype
+ *  lse          device fp32 [total_q][num_q_heads]: log(sum exp(s_t)), or NULL
+ * A query that sees no token: out 0, lse -infinity.  Rows of no sequence are neither
+ * read nor written.  A page id outside the pool drops its tokens (KVQ_DEVERR_PAGE_RANGE).
+ * The workspace of the plan (0 bytes where no range is split) belongs to one call at a
+ * time; for batches of several sizes it is the largest of their plans.  total_q *
+ * num_q_heads < 2^31.
+ * fp16 queries and outputs go to the tensor cores: codes are exact there, and a weight
+ * times its token's scale is one fp16 number, held relative to the largest that its row
+ * has met (in steps of 2^-29 of that one at most): half a step, 2^-11, of a weight, as the
+ * output's own rounding is of the output.  fp32 queries or
+ * outputs are computed in fp32 throughout, without the tensor cores, for small work.
+ * A token whose codes or scale are not finite may make every output of its chunk NaN. */
+kvq_status kvq_latent_plan(const kvq_latent* cache, int total_q, int num_seqs, int num_q_heads, int max_q_len,
+                           int max_seq_len, int* num_splits, size_t* workspace_bytes);
+kvq_status kvq_latent_attention(const kvq_latent* cache, const void* q, int total_q, const int32_t* cu_q_lens,
+                                const int32_t* block_table, int max_pages, const int32_t* seq_lens, int num_seqs,
+                                int num_q_heads, int max_q_len, int max_seq_len, int mode, float softmax_scale,
+                                int causal, void* out, int out_dtype, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Expanded attention of ragged prompts, or of the last tokens of longer contexts, over
+ * dense keys and values of each head (head_dim 128 and the shared rotary part; values of
+ * 128).  With n keys of a sequence, query i of its m stands at n - m + i; causal as above:
+ *   s_t = softmax_scale (q[0..128) . k_t + q[128..128+R) . r_t),  out = sum softmax(s)_t v_t
+ *  q            [total_q][num_q_heads][128 + rope_dim], dense
+ *  k, v         [128] of head h of row j at k + j * k_stride + h * k_head_stride (v likewise):
+ *               slices of one projection's rows; strides in elements, multiples of 16 bytes
+ *  k_rope       [rope_dim] of row j at k_rope + j * k_rope_stride
+ *  cu_q_lens, cu_k_lens  device int32 [num_seqs + 1]: a sequence's rows of q, and of k, v and
+ *               k_rope.  A sequence whose entries are not ascending ranges of at most max_q_len
+ *               and max_k_len rows inside [0, total_q] and [0, total_k] is skipped and sets
+ *               KVQ_DEVERR_QUERY_RANGE in the cache's error word.
+ *  out          [total_q][num_q_heads][128], out_dtype;  lse as above
+ * All device pointers, io_dtype of `cache`, whose pages are not read.  Queries that see no
+ * key, other rows and the two ways of computing are as for kvq_latent_attention. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* k_rope;
+  const void* v;
+  int64_t k_stride, k_head_stride;
+  int64_t v_stride, v_head_stride;
+  int64_t k_rope_stride;
+  const int32_t* cu_q_lens;
+  const int32_t* cu_k_lens;
+  void* out;
+  float* lse;
+  int32_t total_q, total_k, num_seqs, num_q_heads, max_q_len, max_k_len;
+  int32_t causal, out_dtype;
+  float softmax_scale;
+} kvq_latent_prompt;
+kvq_status kvq_latent_prompt_attention(const kvq_latent* cache, const kvq_latent_prompt* p, void* stream);
 
 /* ---- KVarN open tiles ---------------------------------------------------
  * [P2] 注意事项: a KVarN tile is exactly one 128-token page, and the backend

@@ -25,6 +25,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE
 PER_FILE = {
     "kvq_write.cu": ["-fmad=false"],
     "kvq_rope.cu": ["-fmad=false"],
+    "kvq_latent_write.cu": ["-fmad=false"],
 }
 
 

@@ -14,9 +14,10 @@
 #include "kvq_internal.h"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
 
+namespace kvq {
 kvq_status fail(kvq_status code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -28,8 +29,13 @@ kvq_status fail(kvq_status code, const char* fmt, ...) {
 kvq_status cuda_fail(cudaError_t e, const char* what) {
   return fail(KVQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+}  // namespace kvq
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using kvq::aligned;
+using kvq::cuda_fail;
+using kvq::fail;
+
+namespace {
 
 bool valid_mode(int m) {
   return m == KVQ_FP8_PER_TENSOR || m == KVQ_INT8_PER_TOKEN_HEAD || m == KVQ_FP8_PER_TOKEN_HEAD || m == KVQ_NVFP4 ||

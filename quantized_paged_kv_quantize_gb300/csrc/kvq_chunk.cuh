@@ -49,10 +49,13 @@ inline long long chunk_tile_bound(int total_q, int B, int G, int rows) {
 // A sequence whose cu_q entries are not an ascending range of at most
 // max_q_len rows inside the batch is flagged (by the CTAs with `flag`) and has
 // no tiles; a seq_len outside its bounds is flagged and clamped.
-__device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int rows, bool flag) {
+// tokens(b): the sequence's tokens, checked against `lim` here; skip(b, flag) is true for a
+// sequence that has no tiles.
+template <class Tokens, class Skip>
+__device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int rows, bool flag, int lim, Tokens tokens,
+                                             Skip skip) {
   const int lane = threadIdx.x & 31;
   RowTile t{-1, 0, 0, 0, 0, 0, 0};
-  const int lim = (int)min((long long)a.max_seq_len, (long long)a.max_pages * 16);
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
@@ -60,11 +63,11 @@ __device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int 
     if (b < a.B) {  // (all loads at once)
       q0 = __ldg(a.cu_q + b);
       const int q1 = __ldg(a.cu_q + b + 1);
-      n = __ldg(a.seq_lens + b);
+      n = tokens(b);
       if (a.prefix_lens) prefix = __ldg(a.prefix_lens + b);
       if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > a.max_q_len) {
         if (flag) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_QUERY_RANGE);
-      } else {
+      } else if (!skip(b, flag)) {
         m = q1 - q0;
         tiles = (int)(((long long)m * a.G + rows - 1) / rows);
       }
@@ -96,6 +99,11 @@ __device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int 
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return t;
+}
+__device__ __forceinline__ RowTile find_tile(const ChunkArgs& a, int index, int rows, bool flag) {
+  return find_tile(
+      a, index, rows, flag, (int)min((long long)a.max_seq_len, (long long)a.max_pages * 16),
+      [&](int b) { return __ldg(a.seq_lens + b); }, [](int, bool) { return false; });
 }
 
 // The KV tiles (of `kt` tokens) that some row of a CTA sees, as up to two runs

@@ -33,6 +33,11 @@ struct DecodePlan {
 
 int num_sms();
 
+// The message of kvq_last_error (kvq_api.cu); returns `code`.
+kvq_status fail(kvq_status code, const char* fmt, ...);
+kvq_status cuda_fail(cudaError_t e, const char* what);
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
 cudaError_t launch_write(const kvq_cache* c, const void* k, const void* v, const int32_t* slots,
                          int num_tokens, cudaStream_t stream);
 cudaError_t launch_kvarn_append(const kvq_cache* c, const void* k, const void* v, const int32_t* slots,

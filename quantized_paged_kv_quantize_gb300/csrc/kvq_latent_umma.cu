@@ -1,0 +1,621 @@
+// kvq_latent_umma.cu -- absorbed latent attention on the 5th-generation tensor cores
+// (tcgen05): fp16 queries and outputs.
+//
+// Mathematics.  All rows (query x head) of a sequence read the same tokens, so a CTA takes
+// N = 16, 32 or 64 of them against tiles of 128 tokens, transposed: with codes C (exact in
+// fp16; NVFP4 codes times their block scales) and rotary parts R of the tile's tokens,
+//   Sc = C Qc^T,  Sr = R Qr^T            [128 tokens][N rows], fp32
+//   y  = (Sc ks_t + Sr) scale log2(e)    (ks_t: the token's scale)
+//   P  = 2^(y - M) ks_t,  l += 2^(y - M),  O^T += C^T P   [L channels][N rows], fp32
+// The tile of codes in shared memory is the key operand and, read with tokens along K, the
+// value operand: it is dequantized once.  P is one fp16 number to a weight: 2^-11 of it at
+// most, an error of the size of the output's own rounding (the pair of numbers that
+// kvq_chunk_umma.cu takes would need twice the value products).  M is a row's reference, a
+// whole number: the largest y + floor(log2 ks) met so far less kTop, moved (O and l with it,
+// exactly) only when a token passes it by more than 2^(kTop + kSlack); so P stays between
+// fp16's limits whatever the scores and scales, and what falls below their steps of 2^-24 is at
+// most 2^-29 of the row's largest.  Sums are fp32 in tensor memory, cut off (not rounded) by the
+// products: up to 2^-23 of O at each 16 tokens.
+//
+// Shared memory bounds the products: an operand pair of 128 x 16 and N x 16 halves takes
+// 32 + N / 4 cycles at 128 bytes a cycle (measured 48.3 for N = 64, 39.3 for 16) where the
+// multiplications take N / 2, and the dequantized tile is written once through the same
+// port.  The rotary part goes through tensor memory instead (32 cycles at N = 64), which
+// also leaves room for P.
+//
+// Roles (20 warps, one CTA per SM):
+//  warps 0-7    softmax: thread = token of the tile and half of the rows;
+//  warps 8-15   dequantization: a warp has one page of the tile, its packed words in
+//               registers one tile ahead; 128 channels of the tile are one entry of a ring;
+//  warp 16      issues the products (17-19 only fill its warpgroup).
+// The ring's entries are released by the value products, 128 channels at a time, so the
+// next tile is dequantized and its scores begin while these run.  Where ring and tensor
+// memory hold more than a tile (fewer rows, L = 256), its first scores go before them.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kvq_latent.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kTok = 128;
+constexpr int kThreads = 640;
+constexpr int kDequantWarp = 8, kIssueWarp = 16;
+// Registers a thread (the launch gives 96): 256 x 112 + 256 x 104 + 128 x 48 <= 640 x 96.
+constexpr int kRegsSoftmax = 112, kRegsDequant = 104, kRegsIssue = 48;
+constexpr int kEntry = kTok * 128 * 2;     // one ring entry: 128 tokens x 128 channels of fp16
+constexpr int kLbo = 128, kSbo = 2048;     // core matrices (8 tokens x 16 bytes): along channels, along tokens
+constexpr int kScaleTiles = 4;             // tiles whose scales are kept
+constexpr float kTop = 6.0f, kSlack = 8.0f;
+
+template <int L, int N>
+struct Shape {
+  static constexpr int NB = L / 128;                   // ring entries of a tile
+  static constexpr int C = N / 2;                      // rows of a softmax thread
+  static constexpr int QCH = (L + kLatentRope) / 8;    // 16-byte chunks of a query row
+  static constexpr int QSBO = QCH * 128;               // Q: 8 rows of a chunk together, chunks 128 bytes apart
+  static constexpr int Q = 0;
+  static constexpr int P = Q + N / 8 * QSBO;
+  static constexpr int SC = P + kTok * N * 2;          // [tile % 4][128] scales
+  static constexpr int M = SC + kScaleTiles * kTok * 4;  // [2][N] references
+  static constexpr int SEES = M + 2 * N * 4;           // [N] tokens a row sees
+  static constexpr int RED = SEES + N * 4;             // [4][N]
+  static constexpr int F = RED + 4 * N * 4;            // [N] output factors
+  static constexpr int REST = (F + N * 4 + 127) / 128 * 128;
+  static constexpr int FIT = (227 * 1024 - 1024 - 128 - REST) / kEntry;
+  static constexpr int SLOTS = FIT < 6 ? FIT : 6;
+  static constexpr int RING = REST;
+  static constexpr int BYTES = RING + SLOTS * kEntry;
+  static constexpr size_t dynamic() { return BYTES + 128; }
+  // tensor memory: score buffers (latent, rotary), O^T by 128 channels, rotary operands of two tiles
+  static constexpr int SB = NB * N + 64 + 4 * N <= 512 ? 2 : 1;
+  static constexpr int TO = SB * 2 * N, TR = TO + NB * N;
+  // entries of the next tile whose scores go before this tile's value products
+  static constexpr int PRE = SB == 2 ? (SLOTS - NB < NB ? SLOTS - NB : NB) : 0;
+  static_assert(SLOTS >= NB && TR + 64 <= 512, "fits");
+};
+
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, 1u << 20); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// A warp-wide maximum of floats through whole numbers in the same order (NaN: largest or
+// smallest, by its sign; its row is NaN by its weights).
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x), r = __reduce_max_sync(kFull, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(r ^ ((r >> 31) & 0x7fffffff));
+}
+
+// A lane's packed words of one ring entry (a page's 16 tokens x 128 channels): one-byte
+// codes in four loads, token (lane & 7) + 8 (r & 1), channels 16 c .. with
+// c = (lane >> 3) + 4 (r >> 1); E2M1 codes in two, token (lane & 7) + 8 r, channels
+// 32 (lane >> 3) .., with the two block scales as bytes 0 and 1.
+template <int MODE>
+struct Words {
+  static constexpr int N = kLatentFour<MODE> ? 2 : 4;
+  uint4 w[N];
+  uint32_t s[kLatentFour<MODE> ? N : 1];
+};
+// Tokens from `valid` on are zero: their codes must not reach a product.
+template <int MODE, int L>
+__device__ __forceinline__ void load_words(const uint8_t* page, int j, int lane, int valid, Words<MODE>& x) {
+  using PG = LatentPage<MODE, L>;
+  const int a = lane & 7, b = lane >> 3;
+#pragma unroll
+  for (int r = 0; r < Words<MODE>::N; ++r) {
+    const int tok = kLatentFour<MODE> ? a + 8 * r : a + 8 * (r & 1);
+    x.w[r] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kLatentFour<MODE>) x.s[r] = 0u;
+    if (tok < valid) {
+      if constexpr (kLatentFour<MODE>) {
+        x.w[r] = __ldg(reinterpret_cast<const uint4*>(page + tok * PG::CODES + 64 * j + 16 * b));
+        x.s[r] = __ldg(reinterpret_cast<const uint16_t*>(page + PG::SCALES + tok * (L / 16) + 8 * j + 2 * b));
+      } else {
+        x.w[r] = __ldg(reinterpret_cast<const uint4*>(page + tok * PG::CODES + 128 * j + 16 * (b + 4 * (r >> 1))));
+      }
+    }
+  }
+}
+// Into the ring entry at `op`, page `pg` of the tile: channel chunk c of token t at
+// (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring lanes fill one core matrix.
+template <int MODE>
+__device__ __forceinline__ void store_words(const Words<MODE>& x, uint8_t* op, int pg, int lane) {
+  const int a = lane & 7, b = lane >> 3;
+#pragma unroll
+  for (int r = 0; r < Words<MODE>::N; ++r) {
+    const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
+    constexpr int HALVES = kLatentFour<MODE> ? 2 : 1;  // sixteen codes each
+    const int group = kLatentFour<MODE> ? r : (r & 1);
+    uint8_t* p = op + (2 * pg + group) * kSbo + a * 16 + (kLatentFour<MODE> ? 4 * b : 2 * (b + 4 * (r >> 1))) * kLbo;
+#pragma unroll
+    for (int u = 0; u < HALVES; ++u) {
+      uint32_t h[8];
+      latent_codes16<MODE>(in + 2 * u, kLatentFour<MODE> ? x.s[r] >> (8 * u) : 0u, h);
+      *reinterpret_cast<uint4*>(p + 2 * u * kLbo) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(p + (2 * u + 1) * kLbo) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+  }
+}
+
+struct Bars {
+  uint64_t q_full, full[6], free[6], rope_full[2], rope_free[2], s_full[2], p_full, p_free;
+};
+
+template <int MODE, int L, int N>
+__global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_constant__ LatentArgs a) {
+  using S = Shape<L, N>;
+  using PG = LatentPage<MODE, L>;
+  constexpr int NB = S::NB, C = S::C;
+  constexpr bool PT = kLatentTokenScale<MODE>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  __shared__ Bars bar;
+  __shared__ uint32_t tmem_s;
+  __shared__ RowTile tile_s;
+  __shared__ int failed_s;
+  float* sc_s = reinterpret_cast<float*>(sm + S::SC);
+  float* m_s = reinterpret_cast<float*>(sm + S::M);
+  int* sees_s = reinterpret_cast<int*>(sm + S::SEES);
+  float* red_s = reinterpret_cast<float*>(sm + S::RED);
+  float* f_s = reinterpret_cast<float*>(sm + S::F);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, split = blockIdx.y;
+  if (warp == 0) {
+    const RowTile t = find_tile(a, blockIdx.x, N, blockIdx.x == 0 && split == 0);
+    if (lane == 0) tile_s = t;
+  } else if (warp == 1) {
+    if (elect_one()) {
+      for (int i = 0; i < 6; ++i) {
+        mbar_init(&bar.full[i], 8);
+        mbar_init(&bar.free[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.rope_full[i], 8);
+        mbar_init(&bar.rope_free[i], 1);
+        mbar_init(&bar.s_full[i], 2);
+      }
+      mbar_init(&bar.q_full, 8);
+      mbar_init(&bar.p_full, 8);
+      mbar_init(&bar.p_free, 1);
+      failed_s = 0;
+      mbar_fence_init();
+    }
+    __syncwarp();
+  } else if (warp == kIssueWarp) {
+    tmem_alloc(&tmem_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const RowTile t = tile_s;
+  if (t.seq < 0) {  // no such tile
+    if (warp == kIssueWarp) tmem_dealloc(tmem_s, 512);
+    return;
+  }
+  const int fewest = latent_sees(a, t, t.r0), most = latent_sees(a, t, t.r0 + t.count - 1);
+  const int tiles = (most + kTok - 1) / kTok;
+  const int i0 = (int)((long long)tiles * split / a.num_splits);
+  const int n = (int)((long long)tiles * (split + 1) / a.num_splits) - i0;  // this CTA's tiles
+  const uint32_t tb = tmem_s;
+  bool ok = true;
+
+  if (warp >= kDequantWarp && warp < kIssueWarp) {
+    // ------------------------------------------------------------ dequantization
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
+    // This warp's page is number pg of the tile; its rotary rows are 32 channels (half hf) of
+    // the 32 tokens whose lanes of tensor memory it reaches: pages 2 quad and 2 quad + 1.
+    const int quad = warp & 3, hf = (warp - kDequantWarp) >> 2, pg = 2 * quad + hf;
+    // lane's page id of tile i: that of page 2 quad in lanes 0-15, of the next in 16-31
+    auto page_id = [&](int i) -> int {
+      const int page = (i0 + i) * 8 + 2 * quad + (lane >> 4);
+      return i < n && page * 16 < most ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page) : -1;
+    };
+    auto checked = [&](int id, int i) -> int {
+      const int page = (i0 + i) * 8 + 2 * quad + (lane >> 4);
+      if (i < n && page * 16 < most && (id < 0 || id >= a.num_pages)) {
+        if ((lane & 15) == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
+        return -1;
+      }
+      return id;
+    };
+    Words<MODE> words[NB];
+    uint4 rope[4];
+    float sc = -1.0f;   // this page's token `lane` (lanes 0-15): its scale, -1 where it is not there
+    const uint8_t* page = nullptr;
+    int valid = 0;
+    auto open_tile = [&](int id, int i) {  // the page, its valid tokens, its rotary rows and scales
+      const int mine = __shfl_sync(kFull, id, hf * 16);
+      page = a.pool + kHeaderBytes + (size_t)max(mine, 0) * a.block_bytes;
+      valid = mine < 0 ? 0 : min(16, most - ((i0 + i) * 8 + pg) * 16);
+      const int rtok = lane & 15;
+      const bool there = id >= 0 && ((i0 + i) * 8 + 2 * quad + (lane >> 4)) * 16 + rtok < most;
+      const uint4* rp = reinterpret_cast<const uint4*>(a.pool + kHeaderBytes + (size_t)max(id, 0) * a.block_bytes + PG::ROPE +
+                                                       rtok * kLatentRope * 2 + hf * 64);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rope[e] = there ? __ldg(rp + e) : make_uint4(0u, 0u, 0u, 0u);
+      sc = -1.0f;
+      if (lane < valid) sc = PT ? __ldg(reinterpret_cast<const float*>(page + PG::SCALES) + lane) : 1.0f;
+    };
+    int id = checked(page_id(0), 0), ahead = page_id(1);
+    open_tile(id, 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load_words<MODE, L>(page, j, lane, valid, words[j]);
+    int slot = 0, round = 0;
+    for (int i = 0; i < n; ++i) {
+      const int buf = i & 1;
+      if (i >= 2 && ok) ok = wait(&bar.rope_free[buf], ((i >> 1) - 1) & 1);
+      if (!__all_sync(kFull, ok)) break;
+      tc_fence_after();
+      {
+        uint32_t r[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          r[4 * e] = rope[e].x;
+          r[4 * e + 1] = rope[e].y;
+          r[4 * e + 2] = rope[e].z;
+          r[4 * e + 3] = rope[e].w;
+        }
+        tmem_st<16>(tb + S::TR + 32 * buf + 16 * hf + ((uint32_t)(32 * quad) << 16), r);
+      }
+      // The scales' last readers, the softmax of tile i - 4, are done: its value products came
+      // after them and have released the entries that tile i - 1 was stored to.
+      if (lane < 16) sc_s[(i & (kScaleTiles - 1)) * kTok + pg * 16 + lane] = sc;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
+      id = checked(ahead, i + 1);
+      ahead = page_id(i + 2);
+      open_tile(id, i + 1);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
+        if (!__all_sync(kFull, ok)) break;
+        store_words<MODE>(words[j], sm + S::RING + slot * kEntry, pg, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.full[slot]);
+        load_words<MODE, L>(page, j, lane, valid, words[j]);  // of tile i + 1
+        if (++slot == S::SLOTS) {
+          slot = 0;
+          ++round;
+        }
+      }
+    }
+  } else if (warp >= kIssueWarp) {
+    // ------------------------------------------------------------ products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kIssueWarp && n > 0) {
+      constexpr uint32_t kIdescS = umma_idesc_f16(128, N), kIdescO = umma_idesc_f16(128, N) | (1u << 15) | (1u << 16);
+      const uint64_t dq = umma_sdesc(smem_u32(sm + S::Q), kLbo, S::QSBO);
+      const uint64_t dk = umma_sdesc(smem_u32(sm + S::RING), kLbo, kSbo);      // tokens x channels
+      const uint64_t dv = umma_sdesc(smem_u32(sm + S::RING), kSbo, kLbo);      // channels x tokens: the same bytes, MN-major
+      const uint64_t dp = umma_sdesc(smem_u32(sm + S::P), N * 16, 128);        // rows x tokens, MN-major
+      int kslot = 0, kround = 0, vslot = 0;
+      auto scores = [&](int i, int j) {  // of 128 channels
+        if (ok) ok = wait(&bar.full[kslot], kround & 1);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t D = tb + (S::SB == 2 ? (i & 1) * 2 * N : 0);
+          const uint64_t A = dk + (uint64_t)kslot * (kEntry >> 4), B = dq + (uint64_t)j * ((16 * kLbo) >> 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            umma_f16_ss(D, A + e * ((2 * kLbo) >> 4), B + e * ((2 * kLbo) >> 4), kIdescS, (j > 0 || e > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        if (++kslot == S::SLOTS) {
+          kslot = 0;
+          ++kround;
+        }
+      };
+      auto rotary = [&](int i) {
+        const int buf = i & 1, sb = S::SB == 2 ? i & 1 : 0;
+        if (ok) ok = wait(&bar.rope_full[buf], (i >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t B = dq + (uint64_t)NB * ((16 * kLbo) >> 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            umma_f16_ts(tb + sb * 2 * N + N, tb + S::TR + 32 * buf + 8 * e, B + e * ((2 * kLbo) >> 4), kIdescS, e > 0 ? 1u : 0u);
+          tc_commit(&bar.rope_free[buf]);
+          tc_commit(&bar.s_full[sb]);
+          mbar_arrive(&bar.s_full[sb]);  // passes on the scales that came with the rotary rows
+        }
+        __syncwarp();
+      };
+      ok = wait(&bar.q_full, 0);
+      for (int j = 0; j < NB; ++j) scores(0, j);
+      rotary(0);
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        if (more) {
+#pragma unroll 1
+          for (int j = 0; j < S::PRE; ++j) scores(i + 1, j);
+          if (S::PRE == NB) rotary(i + 1);
+        }
+        if (ok) ok = wait(&bar.p_full, i & 1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < NB; ++j) {
+          if (elect_one()) {
+            const uint64_t A = dv + (uint64_t)vslot * (kEntry >> 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              umma_f16_ss(tb + S::TO + j * N, A + e * ((2 * kSbo) >> 4), dp + e * ((2 * N * 16) >> 4), kIdescO,
+                          (i > 0 || e > 0) ? 1u : 0u);
+            tc_commit(&bar.free[vslot]);
+            if (j == NB - 1) tc_commit(&bar.p_free);
+          }
+          __syncwarp();
+          if (++vslot == S::SLOTS) vslot = 0;
+        }
+        if (more) {
+#pragma unroll 1
+          for (int j = S::PRE; j < NB; ++j) scores(i + 1, j);
+          if (S::PRE < NB) rotary(i + 1);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const long long row0 = latent_row(a, t, 0, t.r0);  // rows of a tile lie one after the other
+    // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows
+    for (int it = tid; it < N * S::QCH; it += 256) {
+      const int r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (r < t.count) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + (row0 + r) * (L + kLatentRope)) + c);
+      *reinterpret_cast<uint4*>(sm + S::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * S::QSBO) = x;
+    }
+    if (tid < N) {
+      m_s[tid] = 0.0f;
+      sees_s[tid] = tid < t.count ? latent_sees(a, t, t.r0 + tid) : 0;
+    }
+    fence_proxy_async_smem();  // Q is read by the tensor core
+    softmax_sync();
+    if (lane == 0) mbar_arrive(&bar.q_full);
+
+    const int half = warp >> 2, quad = warp & 3, tok = 32 * quad + lane, col = half * C;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const float one = a.scale * kLog2e;
+    const float tensor = PT ? 1.0f : *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
+    float l[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) l[c] = 0.0f;
+    int flip = 0;
+    uint32_t fresh = C == 32 ? kFull : (1u << C) - 1;  // this thread's rows that have met no score yet: their reference is 0
+    for (int i = 0; i < n; ++i) {
+      const int sb = S::SB == 2 ? i & 1 : 0;
+      if (ok) ok = wait(&bar.s_full[sb], (S::SB == 2 ? i >> 1 : i) & 1);
+      ok = __all_sync(kFull, ok);
+      tc_fence_after();
+      float y[C];
+      const float sc = sc_s[(i & (kScaleTiles - 1)) * kTok + tok];
+      {
+        uint32_t xc[C], xr[C];
+        tmem_ld<C>(tb + sb * 2 * N + col + lanes, xc);
+        tmem_ld<C>(tb + sb * 2 * N + N + col + lanes, xr);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(xc[c]), "+r"(xr[c]));  // (no use before the wait)
+        const float2 ks = make_float2(one * (PT ? sc : tensor), one * (PT ? sc : tensor)), one2 = make_float2(one, one);
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float2 r = __fmul2_rn(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), one2);
+          const float2 v = __ffma2_rn(make_float2(__uint_as_float(xc[c]), __uint_as_float(xc[c + 1])), ks, r);
+          y[c] = v.x;
+          y[c + 1] = v.y;
+        }
+      }
+      const int tk = (i0 + i) * kTok + tok;
+      const bool masked = (i0 + i + 1) * kTok > fewest;
+      if (sc < 0.0f) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] = -INFINITY;
+      } else if (masked) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (tk >= sees_s[col + c]) y[c] = -INFINITY;
+      }
+      const float ex = PT ? scale_exponent(sc) : 0.0f;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(m_s + flip * N + col + c);
+        const float2 u = __fadd2_rn(make_float2(y[c], y[c + 1]), make_float2(-m.x, -m.y));
+        const float2 v = __fadd2_rn(make_float2(y[c + 2], y[c + 3]), make_float2(-m.z, -m.w));
+        y[c] = u.x;
+        y[c + 1] = u.y;
+        y[c + 2] = v.x;
+        y[c + 3] = v.y;
+        mx = fmaxf(mx, fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y)));
+      }
+      // P of the last tile, and O, are free once its value products are done
+      if (i > 0 && ok) ok = wait(&bar.p_free, (i - 1) & 1);
+      ok = __all_sync(kFull, ok);
+      tc_fence_after();
+      bool moves = mx + ex > kTop + kSlack;
+      if (fresh) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) moves |= ((fresh >> c) & 1u) && y[c] > -INFINITY;
+      }
+      if (softmax_any(moves)) {
+        // References move: to each row's largest y + ex of the tile, over its 128 tokens.
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float w = warp_max(y[c] + ex);
+          if (lane == 0) red_s[quad * N + col + c] = w;
+        }
+        softmax_sync();
+#pragma unroll
+        for (int c0 = 0; c0 < C; c0 += 8) {
+          float al[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int k = col + c0 + c;
+            const float top = fmaxf(fmaxf(red_s[k], red_s[N + k]), fmaxf(red_s[2 * N + k], red_s[3 * N + k]));
+            const bool first = ((fresh >> (c0 + c)) & 1u) && top > -INFINITY;
+            const float to = ceilf(top) - kTop, up = first ? to : fmaxf(to, 0.0f);
+            if (first) fresh &= ~(1u << (c0 + c));
+            if (quad == 0 && lane == 0) m_s[(flip ^ 1) * N + k] = m_s[flip * N + k] + up;
+            al[c] = first ? 1.0f : exp2f(-up);  // (a first score: nothing accumulated yet)
+            y[c0 + c] -= up;
+            l[c0 + c] *= al[c];
+          }
+          if (i > 0) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              uint32_t v[8];
+              tmem_ld<8>(tb + S::TO + j * N + col + c0 + lanes, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 8; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * al[c]);
+              tmem_st<8>(tb + S::TO + j * N + col + c0 + lanes, v);
+            }
+          }
+        }
+        tmem_wait_st();
+        flip ^= 1;
+        softmax_sync();
+      }
+      const float vs = PT ? sc : 1.0f;
+      uint8_t* prow = sm + S::P + (tok >> 3) * (N * 16) + (tok & 7) * 16 + (col >> 3) * 128;
+#pragma unroll
+      for (int c = 0; c < C; c += 8) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float2 w = make_float2(ex2(y[c + e]), ex2(y[c + e + 1]));
+          l[c + e] += w.x;
+          l[c + e + 1] += w.y;
+          if (PT) {
+            w = __fmul2_rn(w, make_float2(vs, vs));
+            if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
+              if (y[c + e] == -INFINITY) w.x = 0.0f;
+              if (y[c + e + 1] == -INFINITY) w.y = 0.0f;
+            }
+          }
+          p[e / 2] = h2_as_u32(__floats2half2_rn(w.x, w.y));
+        }
+        *reinterpret_cast<uint4*>(prow + (c >> 3) * 128) = make_uint4(p[0], p[1], p[2], p[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full);
+    }
+
+    // ------------------------------------------------------------ outputs
+    if (n > 0 && ok) ok = wait(&bar.p_free, (n - 1) & 1);
+    tc_fence_after();
+    if (!ok) failed_s = 1;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float x = l[c];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+      if (lane == 0) red_s[quad * N + col + c] = x;
+    }
+    softmax_sync();
+    const bool failed = failed_s != 0;
+    if (failed && tid == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_TIMEOUT);
+    if (tid < N) {
+      const float sum = red_s[tid] + red_s[N + tid] + red_s[2 * N + tid] + red_s[3 * N + tid];
+      const float m = m_s[flip * N + tid];
+      f_s[tid] = sum == 0.0f ? 0.0f : a.num_splits > 1 ? tensor : tensor / sum;  // (a NaN score makes its row NaN)
+      if (tid < t.count && !failed) {
+        const long long row = row0 + tid;
+        if (a.num_splits > 1)
+          st_chk(reinterpret_cast<float2*>(a.ws_ml) + row * a.num_splits + split, make_float2(sum == 0.0f ? -INFINITY : m, sum),
+                 a.ws_span, a.pool);
+        else if (a.lse)
+          st_chk(a.lse + row, sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e), a.lse_span, a.pool);
+      }
+    }
+    softmax_sync();
+    // O^T: a lane has a channel, so a warp's store is 32 neighbouring channels of a row
+    if (!failed && (n > 0 || a.num_splits == 1)) {
+#pragma unroll 1
+      for (int j = 0; j < NB; ++j) {
+        uint32_t v[C];
+        if (n > 0) {
+          tmem_ld<C>(tb + S::TO + j * N + col + lanes, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < C; ++c) asm volatile("" : "+r"(v[c]));
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (col + c >= t.count) break;
+          const float f = f_s[col + c];
+          const float x = n > 0 && f != 0.0f ? __uint_as_float(v[c]) * f : 0.0f;
+          const long long row = row0 + col + c;
+          const int ch = 128 * j + tok;
+          if (a.num_splits > 1) st_chk(a.ws_o + (row * a.num_splits + split) * L + ch, x, a.ws_span, a.pool);
+          else st_chk(static_cast<__half*>(a.out) + row * L + ch, __float2half_rn(x), a.out_span, a.pool);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssueWarp) tmem_dealloc(tb, 512);
+}
+
+template <int MODE, int L, int N>
+cudaError_t launch(const LatentArgs& a, cudaStream_t s) {
+  auto kern = latent_umma_kernel<MODE, L, N>;
+  constexpr size_t smem = Shape<L, N>::dynamic();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, N), a.num_splits), kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <int L, int N>
+cudaError_t launch_mode(int mode, const LatentArgs& a, cudaStream_t s) {
+  switch (mode) {
+    case KVQ_FP8_PER_TENSOR: return launch<KVQ_FP8_PER_TENSOR, L, N>(a, s);
+    case KVQ_INT8_PER_TOKEN_HEAD: return launch<KVQ_INT8_PER_TOKEN_HEAD, L, N>(a, s);
+    case KVQ_FP8_PER_TOKEN_HEAD: return launch<KVQ_FP8_PER_TOKEN_HEAD, L, N>(a, s);
+    case KVQ_NVFP4:
+    case KVQ_NVFP4_4OVER6: return launch<KVQ_NVFP4, L, N>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <int L>
+cudaError_t launch_rows(int mode, const LatentArgs& a, cudaStream_t s) {
+  const int rows = latent_umma_rows(a.max_q_len, a.Hq);
+  return rows == 16 ? launch_mode<L, 16>(mode, a, s) : rows == 32 ? launch_mode<L, 32>(mode, a, s) : launch_mode<L, 64>(mode, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_umma(const kvq_latent* c, const LatentArgs& a, cudaStream_t s) {
+  return c->cfg.latent_dim == 512 ? launch_rows<512>(c->cfg.mode, a, s) : launch_rows<256>(c->cfg.mode, a, s);
+}
+
+}  // namespace kvq

@@ -42,6 +42,9 @@ EXPORTED = [
     "kvq_decode_multi_plan", "kvq_decode_multi_workspace_bytes", "kvq_decode_attention_multi",
     "kvq_debug_build", "kvq_debug_bounds_selftest", "kvq_tensor_error_stats",
     "kvq_cache_read", "kvq_norm_rope_write", "kvq_chunk_plan", "kvq_chunk_attention",
+    "kvq_latent_bytes", "kvq_latent_alloc", "kvq_latent_free", "kvq_latent_read_errors", "kvq_latent_set_scale",
+    "kvq_latent_set_scale_from_amax", "kvq_latent_write", "kvq_latent_read", "kvq_latent_plan", "kvq_latent_attention",
+    "kvq_latent_prompt_attention",
 ]
 
 
@@ -74,12 +77,40 @@ class AttentionOptions(ctypes.Structure):
                 ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
+class LatentConfig(ctypes.Structure):
+    """kvq_latent_config."""
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("mode", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
+class LatentRows(ctypes.Structure):
+    """kvq_latent_rows: the arguments of kvq_latent_write."""
+    _fields_ = [("latent", ctypes.c_void_p), ("k_rope", ctypes.c_void_p), ("q_rope", ctypes.c_void_p),
+                ("q_rope_out", ctypes.c_void_p), ("latent_stride", ctypes.c_int64), ("k_rope_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("q_out_head_stride", ctypes.c_int64), ("latent_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("cos_sin", ctypes.c_void_p), ("slot_mapping", ctypes.c_void_p), ("latent_out", ctypes.c_void_p),
+                ("k_rope_out", ctypes.c_void_p), ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("max_position", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LatentPrompt(ctypes.Structure):
+    """kvq_latent_prompt: the arguments of kvq_latent_prompt_attention."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("k_rope", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("k_rope_stride", ctypes.c_int64), ("cu_q_lens", ctypes.c_void_p),
+                ("cu_k_lens", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("max_k_len", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libkvq.so is not built ({LIB_PATH}); run __graft_entry__.build()")
     L = ctypes.CDLL(LIB_PATH)
     vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
-    cfgp = ctypes.POINTER(CacheConfig)
+    cfgp, lcfgp = ctypes.POINTER(CacheConfig), ctypes.POINTER(LatentConfig)
     sig = {
         "kvq_last_error": (ctypes.c_char_p, []),
         "kvq_version": (i32, []),
@@ -112,6 +143,18 @@ def _load():
                                  ctypes.POINTER(sz)]),
         "kvq_chunk_attention": (i32, [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32,
                                       ctypes.POINTER(AttentionOptions), vp, i32, vp, sz, vp]),
+        "kvq_latent_bytes": (i32, [lcfgp, ctypes.POINTER(sz)]),
+        "kvq_latent_alloc": (i32, [lcfgp, vp, sz, ctypes.POINTER(vp)]),
+        "kvq_latent_free": (i32, [vp]),
+        "kvq_latent_read_errors": (i32, [vp, ctypes.POINTER(ctypes.c_uint32), i32, vp]),
+        "kvq_latent_set_scale": (i32, [vp, f32, vp]),
+        "kvq_latent_set_scale_from_amax": (i32, [vp, vp, vp]),
+        "kvq_latent_write": (i32, [vp, ctypes.POINTER(LatentRows), i32, vp]),
+        "kvq_latent_read": (i32, [vp, vp, i32, vp, vp, i32, vp]),
+        "kvq_latent_plan": (i32, [vp, i32, i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(sz)]),
+        "kvq_latent_attention": (i32, [vp, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, i32, vp, i32, vp, vp, sz,
+                                       vp]),
+        "kvq_latent_prompt_attention": (i32, [vp, ctypes.POINTER(LatentPrompt), vp]),
         "kvq_kvarn_append": (i32, [vp, vp, vp, vp, vp, i32, vp, i32, vp]),
         "kvq_kvarn_decode_workspace_bytes": (i32, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
         "kvq_kvarn_decode_attention": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, f32, vp, vp, i32, vp, sz, vp]),
@@ -524,3 +567,185 @@ def kvq_chunk_attention(cache: "KVCache", q, cu_q_lens, block_table, seq_lens, o
         cache.cfg.mode if mode is None else _mode(mode), D ** -0.5 if softmax_scale is None else softmax_scale, opt,
         _take(out, "out", cache, odt, shape), _FLOATS[odt], None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.nbytes, _stream_of(cache, stream)))
+
+
+# ---- latent caches
+class LatentCache:
+    """A latent cache's descriptor bound to a caller-owned device pool (a uint8 tensor)."""
+
+    def __init__(self, cfg: LatentConfig, pool: torch.Tensor, handle: int):
+        self.cfg = cfg
+        self.pool = pool
+        self.latent_handle = handle  # (not `handle`: the calls of the other caches do not take it)
+        self.device = pool.get_device()
+        self.io_dtype = torch.float16 if cfg.io_dtype == KVQ_F16 else torch.float32
+        self.latent_dim, self.rope_dim = cfg.latent_dim, cfg.rope_dim
+
+    @property
+    def mode(self) -> int:
+        return self.cfg.mode
+
+    def free(self):
+        if self.latent_handle:
+            _lib.kvq_latent_free(self.latent_handle)
+            self.latent_handle = 0
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def make_latent_config(num_pages: int, page_size: int, latent_dim: int, rope_dim: int, mode, io_dtype=KVQ_F16) -> LatentConfig:
+    return LatentConfig(num_pages, page_size, latent_dim, rope_dim, _mode(mode), _dtype_code(io_dtype))
+
+
+def kvq_latent_bytes(cfg: LatentConfig) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.kvq_latent_bytes(ctypes.byref(cfg), ctypes.byref(out)))
+    return out.value
+
+
+def kvq_latent_alloc(cfg: LatentConfig, pool: torch.Tensor) -> LatentCache:
+    h = ctypes.c_void_p()
+    _check(_lib.kvq_latent_alloc(ctypes.byref(cfg), _ptr(pool), pool.numel() * pool.element_size(), ctypes.byref(h)))
+    return LatentCache(cfg, pool, h.value)
+
+
+def kvq_latent_free(cache: LatentCache):
+    cache.free()
+
+
+def kvq_latent_read_errors(cache: LatentCache, clear: bool = True, stream=None) -> int:
+    flags = ctypes.c_uint32()
+    _check(_lib.kvq_latent_read_errors(cache.latent_handle, ctypes.byref(flags), int(clear), _stream_of(cache, stream)))
+    return flags.value
+
+
+def kvq_latent_set_scale(cache: LatentCache, scale: float, stream=None):
+    _check(_lib.kvq_latent_set_scale(cache.latent_handle, scale, _stream_of(cache, stream)))
+
+
+def kvq_latent_set_scale_from_amax(cache: LatentCache, amax: torch.Tensor, stream=None):
+    _check(_lib.kvq_latent_set_scale_from_amax(cache.latent_handle, _take(amax, "amax", cache, torch.float32, (1,)),
+                                               _stream_of(cache, stream)))
+
+
+def _take_rows(t, name: str, cache, dtype, shape) -> tuple:
+    """The data pointer and leading strides (elements) of `t`, whose last dimension is contiguous: slices of wider rows."""
+    have = t.shape
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
+        raise ValueError(f"{name}: shape {tuple(have)}, expected {tuple('*' if w is None else w for w in shape)}")
+    if t.get_device() != cache.device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {cache.pool.device}")
+    if have[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (t.data_ptr(), *(0 if n <= 1 else s for n, s in zip(have[:-1], t.stride())))
+
+
+def kvq_latent_write(cache: LatentCache, latent, k_rope, positions, cos_sin, *, slot_mapping=None, q_rope=None,
+                     q_rope_out=None, latent_weight=None, latent_out=None, k_rope_out=None, eps: float = 1e-6,
+                     interleaved: bool = False, mode=None, stream=None):
+    """RMS norm (where latent_weight [L] is given) of latent [n][L], rotation of k_rope [n][R] and of q_rope [n][Hq][R]
+    (into q_rope_out [n][Hq][R]) by the table row cos_sin[positions[i]] (fp32 [max_position][R]: cosines, then sines),
+    each rounded once; with slot_mapping, latents and key parts are quantized into the cache.  latent, k_rope, q_rope
+    and q_rope_out may be slices of wider rows (strides that are multiples of 16 bytes)."""
+    dt, L, R = cache.io_dtype, cache.latent_dim, cache.rope_dim
+    n = latent.shape[0]
+    Hq = 0 if q_rope is None else q_rope.shape[1]
+    if (q_rope is None) != (q_rope_out is None):
+        raise ValueError("q_rope and q_rope_out go together")
+    lat, lat_s = _take_rows(latent, "latent", cache, dt, (n, L))
+    kr, kr_s = _take_rows(k_rope, "k_rope", cache, dt, (n, R))
+    q, q_s, q_h = (None, 0, 0) if q_rope is None else _take_rows(q_rope, "q_rope", cache, dt, (n, Hq, R))
+    o, o_s, o_h = (None, 0, 0) if q_rope is None else _take_rows(q_rope_out, "q_rope_out", cache, dt, (n, Hq, R))
+    if Hq == 0:
+        q = o = None
+    r = LatentRows(
+        lat, kr, q, o, lat_s, kr_s, q_s, q_h, o_s, o_h,
+        None if latent_weight is None else _take(latent_weight, "latent_weight", cache, dt, (L,)),
+        _take(positions, "positions", cache, torch.int32, (n,)),
+        _take(cos_sin, "cos_sin", cache, torch.float32, (cos_sin.shape[0], R)),
+        None if slot_mapping is None else _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,)),
+        None if latent_out is None else _take(latent_out, "latent_out", cache, dt, (n, L)),
+        None if k_rope_out is None else _take(k_rope_out, "k_rope_out", cache, dt, (n, R)),
+        n, Hq, cos_sin.shape[0], interleaved, eps)
+    _check(_lib.kvq_latent_write(cache.latent_handle, ctypes.byref(r), cache.cfg.mode if mode is None else _mode(mode),
+                                 _stream_of(cache, stream)))
+
+
+def kvq_latent_read(cache: LatentCache, slot_mapping, latent_out=None, rope_out=None, *, stream=None):
+    """The rows the cache holds at `slot_mapping` (int32 [n]): latent_out [n][L] and rope_out [n][R], both fp16 or both
+    fp32 (either may be None); rows of negative slots stay as they were."""
+    out = latent_out if latent_out is not None else rope_out
+    if out is None:
+        raise ValueError("latent_out and rope_out are both None")
+    n, dt = slot_mapping.shape[0], out.dtype
+    if dt not in _FLOATS:
+        raise ValueError(f"latent_out: dtype {dt}, expected float16 or float32")
+    _check(_lib.kvq_latent_read(
+        cache.latent_handle, _take(slot_mapping, "slot_mapping", cache, torch.int32, (n,)), n,
+        None if latent_out is None else _take(latent_out, "latent_out", cache, dt, (n, cache.latent_dim)),
+        None if rope_out is None else _take(rope_out, "rope_out", cache, dt, (n, cache.rope_dim)),
+        _FLOATS[dt], _stream_of(cache, stream)))
+
+
+def kvq_latent_plan(cache: LatentCache, total_q: int, num_seqs: int, num_q_heads: int, *, max_q_len: int, max_seq_len: int):
+    """(parts of a token range, workspace bytes) of a kvq_latent_attention call of these sizes."""
+    ns, ws = ctypes.c_int(), ctypes.c_size_t()
+    _check(_lib.kvq_latent_plan(cache.latent_handle, total_q, num_seqs, num_q_heads, max_q_len, max_seq_len,
+                                ctypes.byref(ns), ctypes.byref(ws)))
+    return ns.value, ws.value
+
+
+def kvq_latent_attention(cache: LatentCache, q, cu_q_lens, block_table, seq_lens, out, *, max_q_len: int, max_seq_len: int,
+                         softmax_scale: float, causal: bool = True, lse=None, workspace=None, mode=None, stream=None):
+    """Absorbed attention: q [total_q][Hq][L + R] against the paged latents and rotary parts, out [total_q][Hq][L] in the
+    latent space; sequence b's queries are rows cu_q_lens[b] .. cu_q_lens[b + 1] - 1, the last of its seq_lens[b] tokens.
+    causal false: every query sees all of them.  lse: fp32 [total_q][Hq], or None.  block_table: int32 [B][max_pages]."""
+    i32 = torch.int32
+    total, Hq = q.shape[0], q.shape[1]
+    B, pages = block_table.shape
+    odt = out.dtype
+    if odt not in _FLOATS:
+        raise ValueError(f"out: dtype {odt}, expected float16 or float32")
+    if workspace is not None and workspace.get_device() != cache.device:
+        raise ValueError(f"workspace: on {workspace.device}, the cache is on {cache.pool.device}")
+    _check(_lib.kvq_latent_attention(
+        cache.latent_handle, _take(q, "q", cache, cache.io_dtype, (total, Hq, cache.latent_dim + cache.rope_dim)), total,
+        _take(cu_q_lens, "cu_q_lens", cache, i32, (B + 1,)), _take(block_table, "block_table", cache, i32, (B, pages)), pages,
+        _take(seq_lens, "seq_lens", cache, i32, (B,)), B, Hq, max_q_len, max_seq_len,
+        cache.cfg.mode if mode is None else _mode(mode), softmax_scale, int(causal),
+        _take(out, "out", cache, odt, (total, Hq, cache.latent_dim)), _FLOATS[odt],
+        None if lse is None else _take(lse, "lse", cache, torch.float32, (total, Hq)),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_of(cache, stream)))
+
+
+LATENT_HEAD = 128  # an expanded head's key channels beside the rotary ones, and its values
+
+
+def kvq_latent_prompt_attention(cache: LatentCache, q, k, k_rope, v, cu_q_lens, cu_k_lens, out, *, max_q_len: int,
+                                max_k_len: int, softmax_scale: Optional[float] = None, causal: bool = True, lse=None,
+                                stream=None):
+    """Expanded attention of ragged prompts: q [total_q][Hq][128 + R] against k [total_k][Hq][128] and the shared k_rope
+    [total_k][R], values v [total_k][Hq][128], out [total_q][Hq][128]; sequence b has rows cu_q_lens[b] .. of q, the last
+    of its rows cu_k_lens[b] .. of k, k_rope and v (which may be slices of wider rows, strides multiples of 16 bytes)."""
+    i32, dt, D = torch.int32, cache.io_dtype, LATENT_HEAD
+    total, Hq = q.shape[0], q.shape[1]
+    S, B = k_rope.shape[0], cu_q_lens.shape[0] - 1
+    if out.dtype not in _FLOATS:
+        raise ValueError(f"out: dtype {out.dtype}, expected float16 or float32")
+    kp, k_s, k_h = _take_rows(k, "k", cache, dt, (S, Hq, D))
+    vp, v_s, v_h = _take_rows(v, "v", cache, dt, (S, Hq, D))
+    rp, r_s = _take_rows(k_rope, "k_rope", cache, dt, (S, cache.rope_dim))
+    p = LatentPrompt(
+        _take(q, "q", cache, dt, (total, Hq, D + cache.rope_dim)), kp, rp, vp, k_s, k_h, v_s, v_h, r_s,
+        _take(cu_q_lens, "cu_q_lens", cache, i32, (B + 1,)), _take(cu_k_lens, "cu_k_lens", cache, i32, (B + 1,)),
+        _take(out, "out", cache, out.dtype, (total, Hq, D)),
+        None if lse is None else _take(lse, "lse", cache, torch.float32, (total, Hq)), total, S, B, Hq, max_q_len, max_k_len,
+        int(causal), _FLOATS[out.dtype], (D + cache.rope_dim) ** -0.5 if softmax_scale is None else softmax_scale)
+    _check(_lib.kvq_latent_prompt_attention(cache.latent_handle, ctypes.byref(p), _stream_of(cache, stream)))
