@@ -23,11 +23,12 @@
 // port.  The rotary part goes through tensor memory instead (32 cycles at N = 64), which
 // also leaves room for P.
 //
-// Roles (20 warps, one CTA per SM):
-//  warps 0-7    softmax: thread = token of the tile and half of the rows;
-//  warps 8-15   dequantization: a warp has one page of the tile, its packed words in
-//               registers one tile ahead; 128 channels of the tile are one entry of a ring;
-//  warp 16      issues the products (17-19 only fill its warpgroup).
+// Roles (28 warps, one CTA per SM):
+//  warps 0-15   softmax: thread = token of the tile and a quarter of the rows;
+//  warps 16-23  dequantization: a warp has one page of the tile; 128 channels of the tile
+//               are one entry of a ring, loaded some entries ahead, converted before the
+//               wait for it and stored after;
+//  warp 24      issues the products (25-27 only fill its warpgroup).
 // The ring's entries are released by the value products, 128 channels at a time, so the
 // next tile is dequantized and its scores begin while these run.  Where ring and tensor
 // memory hold more than a tile (fewer rows, L = 256), its first scores go before them.
@@ -42,10 +43,8 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128;
-constexpr int kThreads = 640;
-constexpr int kDequantWarp = 8, kIssueWarp = 16;
-// Registers a thread (the launch gives 96): 256 x 112 + 256 x 104 + 128 x 48 <= 640 x 96.
-constexpr int kRegsSoftmax = 112, kRegsDequant = 104, kRegsIssue = 48;
+constexpr int kThreads = 896, kSoftmax = 512;
+constexpr int kDequantWarp = 16, kIssueWarp = 24;
 constexpr int kEntry = kTok * 128 * 2;     // one ring entry: 128 tokens x 128 channels of fp16
 constexpr int kLbo = 128, kSbo = 2048;     // core matrices (8 tokens x 16 bytes): along channels, along tokens
 constexpr int kScaleTiles = 4;             // tiles whose scales are kept
@@ -53,17 +52,24 @@ constexpr float kTop = 6.0f, kSlack = 8.0f;
 
 template <int L, int N>
 struct Shape {
+  // Registers a thread (the launch gives 72): 512 softmax + 256 dequant + 128 issue <= 896 x 72.
+  static constexpr int RS = N == 64 ? 72 : 56, RD = N == 64 ? 88 : 112, RI = N == 64 ? 40 : 56;
+  static_assert(512 * RS + 256 * RD + 128 * RI <= 896 * 72, "registers");
+  // Ring entries that a dequantizing warp has loaded ahead: with 64 rows the products take
+  // longer than the loads, with fewer the loads are what there is to wait for.
+  static constexpr int AHEAD = N == 64 ? 2 : L / 128;
   static constexpr int NB = L / 128;                   // ring entries of a tile
-  static constexpr int C = N / 2;                      // rows of a softmax thread
+  static constexpr int C = N / 4;                      // rows of a softmax thread
   static constexpr int QCH = (L + kLatentRope) / 8;    // 16-byte chunks of a query row
   static constexpr int QSBO = QCH * 128;               // Q: 8 rows of a chunk together, chunks 128 bytes apart
   static constexpr int Q = 0;
   static constexpr int P = Q + N / 8 * QSBO;
   static constexpr int SC = P + kTok * N * 2;          // [tile % 4][128] scales
-  static constexpr int M = SC + kScaleTiles * kTok * 4;  // [2][N] references
-  static constexpr int SEES = M + 2 * N * 4;           // [N] tokens a row sees
+  static constexpr int M = SC + kScaleTiles * kTok * 4;  // [N] references
+  static constexpr int SEES = M + N * 4;               // [N] tokens a row sees
   static constexpr int RED = SEES + N * 4;             // [4][N]
-  static constexpr int F = RED + 4 * N * 4;            // [N] output factors
+  static constexpr int UP = RED + 4 * N * 4;           // [N] what a reference moves by
+  static constexpr int F = UP + N * 4;                 // [N] the factor that goes with it; at the end, the output's
   static constexpr int REST = (F + N * 4 + 127) / 128 * 128;
   static constexpr int FIT = (227 * 1024 - 1024 - 128 - REST) / kEntry;
   static constexpr int SLOTS = FIT < 6 ? FIT : 6;
@@ -89,11 +95,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mb
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }  // warps 0-15
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 512, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)x)
       : "memory");
@@ -136,24 +142,32 @@ __device__ __forceinline__ void load_words(const uint8_t* page, int j, int lane,
     }
   }
 }
-// Into the ring entry at `op`, page `pg` of the tile: channel chunk c of token t at
-// (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring lanes fill one core matrix.
+// The words as fp16: eight chunks of 16 bytes, in the order that store_chunks takes.
 template <int MODE>
-__device__ __forceinline__ void store_words(const Words<MODE>& x, uint8_t* op, int pg, int lane) {
-  const int a = lane & 7, b = lane >> 3;
+__device__ __forceinline__ void convert(const Words<MODE>& x, uint4* out) {
 #pragma unroll
   for (int r = 0; r < Words<MODE>::N; ++r) {
     const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
     constexpr int HALVES = kLatentFour<MODE> ? 2 : 1;  // sixteen codes each
-    const int group = kLatentFour<MODE> ? r : (r & 1);
-    uint8_t* p = op + (2 * pg + group) * kSbo + a * 16 + (kLatentFour<MODE> ? 4 * b : 2 * (b + 4 * (r >> 1))) * kLbo;
 #pragma unroll
     for (int u = 0; u < HALVES; ++u) {
       uint32_t h[8];
       latent_codes16<MODE>(in + 2 * u, kLatentFour<MODE> ? x.s[r] >> (8 * u) : 0u, h);
-      *reinterpret_cast<uint4*>(p + 2 * u * kLbo) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(p + (2 * u + 1) * kLbo) = make_uint4(h[4], h[5], h[6], h[7]);
+      out[2 * (HALVES * r + u)] = make_uint4(h[0], h[1], h[2], h[3]);
+      out[2 * (HALVES * r + u) + 1] = make_uint4(h[4], h[5], h[6], h[7]);
     }
+  }
+}
+// Into the ring entry at `op`, page `pg` of the tile: channel chunk c of token t at
+// (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring lanes fill one core matrix.
+template <int MODE>
+__device__ __forceinline__ void store_chunks(const uint4* x, uint8_t* op, int pg, int lane) {
+  uint8_t* p = op + 2 * pg * kSbo + (lane & 7) * 16 + (kLatentFour<MODE> ? 4 : 2) * (lane >> 3) * kLbo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = kLatentFour<MODE> ? i >> 2 : i >> 1;  // load
+    const int at = kLatentFour<MODE> ? r * kSbo + (i & 3) * kLbo : (r & 1) * kSbo + (8 * (r >> 1) + (i & 1)) * kLbo;
+    *reinterpret_cast<uint4*>(p + at) = x[i];
   }
 }
 
@@ -173,10 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   __shared__ uint32_t tmem_s;
   __shared__ RowTile tile_s;
   __shared__ int failed_s;
+  __shared__ uint32_t fresh_s[2];  // rows 0-31, 32-63: no score met yet
   float* sc_s = reinterpret_cast<float*>(sm + S::SC);
   float* m_s = reinterpret_cast<float*>(sm + S::M);
   int* sees_s = reinterpret_cast<int*>(sm + S::SEES);
   float* red_s = reinterpret_cast<float*>(sm + S::RED);
+  float* up_s = reinterpret_cast<float*>(sm + S::UP);
   float* f_s = reinterpret_cast<float*>(sm + S::F);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, split = blockIdx.y;
@@ -194,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
         mbar_init(&bar.rope_free[i], 1);
         mbar_init(&bar.s_full[i], 2);
       }
-      mbar_init(&bar.q_full, 8);
-      mbar_init(&bar.p_full, 8);
+      mbar_init(&bar.q_full, 16);
+      mbar_init(&bar.p_full, 16);
       mbar_init(&bar.p_free, 1);
       failed_s = 0;
       mbar_fence_init();
@@ -222,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
 
   if (warp >= kDequantWarp && warp < kIssueWarp) {
     // ------------------------------------------------------------ dequantization
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::RD));
     // This warp's page is number pg of the tile; its rotary rows are 32 channels (half hf) of
     // the 32 tokens whose lanes of tensor memory it reaches: pages 2 quad and 2 quad + 1.
     const int quad = warp & 3, hf = (warp - kDequantWarp) >> 2, pg = 2 * quad + hf;
@@ -239,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       }
       return id;
     };
-    Words<MODE> words[NB];
+    Words<MODE> words[S::AHEAD];
     uint4 rope[4];
     float sc = -1.0f;   // this page's token `lane` (lanes 0-15): its scale, -1 where it is not there
-    const uint8_t* page = nullptr;
-    int valid = 0;
+    const uint8_t *page = nullptr, *now = nullptr;  // of the tile opened last, and of the one being stored
+    int valid = 0, valid_now = 0;
     auto open_tile = [&](int id, int i) {  // the page, its valid tokens, its rotary rows and scales
       const int mine = __shfl_sync(kFull, id, hf * 16);
       page = a.pool + kHeaderBytes + (size_t)max(mine, 0) * a.block_bytes;
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     int id = checked(page_id(0), 0), ahead = page_id(1);
     open_tile(id, 0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) load_words<MODE, L>(page, j, lane, valid, words[j]);
+    for (int j = 0; j < S::AHEAD; ++j) load_words<MODE, L>(page, j, lane, valid, words[j]);
     int slot = 0, round = 0;
     for (int i = 0; i < n; ++i) {
       const int buf = i & 1;
@@ -285,18 +301,23 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
+      now = page;
+      valid_now = valid;
       id = checked(ahead, i + 1);
       ahead = page_id(i + 2);
       open_tile(id, i + 1);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
+        uint4 h[8];
+        convert<MODE>(words[j % S::AHEAD], h);
         if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
         if (!__all_sync(kFull, ok)) break;
-        store_words<MODE>(words[j], sm + S::RING + slot * kEntry, pg, lane);
+        store_chunks<MODE>(h, sm + S::RING + slot * kEntry, pg, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.full[slot]);
-        load_words<MODE, L>(page, j, lane, valid, words[j]);  // of tile i + 1
+        if (j + S::AHEAD < NB) load_words<MODE, L>(now, j + S::AHEAD, lane, valid_now, words[j % S::AHEAD]);
+        else load_words<MODE, L>(page, j + S::AHEAD - NB, lane, valid, words[j % S::AHEAD]);  // of tile i + 1
         if (++slot == S::SLOTS) {
           slot = 0;
           ++round;
@@ -305,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     }
   } else if (warp >= kIssueWarp) {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::RI));
     if (warp == kIssueWarp && n > 0) {
       constexpr uint32_t kIdescS = umma_idesc_f16(128, N), kIdescO = umma_idesc_f16(128, N) | (1u << 15) | (1u << 16);
       const uint64_t dq = umma_sdesc(smem_u32(sm + S::Q), kLbo, S::QSBO);
@@ -382,38 +403,47 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::RS));
     const long long row0 = latent_row(a, t, 0, t.r0);  // rows of a tile lie one after the other
     // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows
-    for (int it = tid; it < N * S::QCH; it += 256) {
-      const int r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (r < t.count) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + (row0 + r) * (L + kLatentRope)) + c);
-      *reinterpret_cast<uint4*>(sm + S::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * S::QSBO) = x;
+    constexpr int QN = (N * S::QCH + kSoftmax - 1) / kSoftmax;
+    {
+      uint4 x[QN];  // (all loads in flight at once)
+#pragma unroll
+      for (int u = 0; u < QN; ++u) {
+        const int it = tid + u * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < t.count) x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + (row0 + r) * (L + kLatentRope)) + c);
+      }
+#pragma unroll
+      for (int u = 0; u < QN; ++u) {
+        const int it = tid + u * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
+        if (r < N) *reinterpret_cast<uint4*>(sm + S::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * S::QSBO) = x[u];
+      }
     }
     if (tid < N) {
       m_s[tid] = 0.0f;
       sees_s[tid] = tid < t.count ? latent_sees(a, t, t.r0 + tid) : 0;
     }
+    if (tid < 2) fresh_s[tid] = kFull;
     fence_proxy_async_smem();  // Q is read by the tensor core
     softmax_sync();
     if (lane == 0) mbar_arrive(&bar.q_full);
 
-    const int half = warp >> 2, quad = warp & 3, tok = 32 * quad + lane, col = half * C;
+    const int quad = warp & 3, tok = 32 * quad + lane, col = (warp >> 2) * C;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const float one = a.scale * kLog2e;
     const float tensor = PT ? 1.0f : *reinterpret_cast<const float*>(a.pool + kHdrKScaleOffset);
-    float l[C];
+    float2 l[C / 2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) l[c] = 0.0f;
-    int flip = 0;
-    uint32_t fresh = C == 32 ? kFull : (1u << C) - 1;  // this thread's rows that have met no score yet: their reference is 0
+    for (int c = 0; c < C / 2; ++c) l[c] = make_float2(0.0f, 0.0f);
+    uint32_t fresh = (1u << C) - 1;  // this thread's rows that have met no score yet: their reference is 0
     for (int i = 0; i < n; ++i) {
       const int sb = S::SB == 2 ? i & 1 : 0;
       if (ok) ok = wait(&bar.s_full[sb], (S::SB == 2 ? i >> 1 : i) & 1);
       ok = __all_sync(kFull, ok);
       tc_fence_after();
-      float y[C];
+      float2 y[C / 2];
       const float sc = sc_s[(i & (kScaleTiles - 1)) * kTok + tok];
       {
         uint32_t xc[C], xr[C];
@@ -426,102 +456,117 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < C; c += 2) {
           const float2 r = __fmul2_rn(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), one2);
-          const float2 v = __ffma2_rn(make_float2(__uint_as_float(xc[c]), __uint_as_float(xc[c + 1])), ks, r);
-          y[c] = v.x;
-          y[c + 1] = v.y;
+          y[c / 2] = __ffma2_rn(make_float2(__uint_as_float(xc[c]), __uint_as_float(xc[c + 1])), ks, r);
         }
       }
       const int tk = (i0 + i) * kTok + tok;
       const bool masked = (i0 + i + 1) * kTok > fewest;
       if (sc < 0.0f) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) y[c] = -INFINITY;
+        for (int c = 0; c < C / 2; ++c) y[c] = make_float2(-INFINITY, -INFINITY);
       } else if (masked) {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (tk >= sees_s[col + c]) y[c] = -INFINITY;
+        for (int c = 0; c < C; c += 4) {
+          const int4 s = *reinterpret_cast<const int4*>(sees_s + col + c);
+          if (tk >= s.x) y[c / 2].x = -INFINITY;
+          if (tk >= s.y) y[c / 2].y = -INFINITY;
+          if (tk >= s.z) y[c / 2 + 1].x = -INFINITY;
+          if (tk >= s.w) y[c / 2 + 1].y = -INFINITY;
+        }
       }
       const float ex = PT ? scale_exponent(sc) : 0.0f;
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(m_s + flip * N + col + c);
-        const float2 u = __fadd2_rn(make_float2(y[c], y[c + 1]), make_float2(-m.x, -m.y));
-        const float2 v = __fadd2_rn(make_float2(y[c + 2], y[c + 3]), make_float2(-m.z, -m.w));
-        y[c] = u.x;
-        y[c + 1] = u.y;
-        y[c + 2] = v.x;
-        y[c + 3] = v.y;
-        mx = fmaxf(mx, fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y)));
+        const float4 m = *reinterpret_cast<const float4*>(m_s + col + c);
+        y[c / 2] = __fadd2_rn(y[c / 2], make_float2(-m.x, -m.y));
+        y[c / 2 + 1] = __fadd2_rn(y[c / 2 + 1], make_float2(-m.z, -m.w));
+        mx = fmaxf(mx, fmaxf(fmaxf(y[c / 2].x, y[c / 2].y), fmaxf(y[c / 2 + 1].x, y[c / 2 + 1].y)));
+      }
+      bool moves = mx + ex > kTop + kSlack;
+      if (fresh) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) moves |= ((fresh >> c) & 1u) && (c & 1 ? y[c / 2].y : y[c / 2].x) > -INFINITY;
       }
       // P of the last tile, and O, are free once its value products are done
       if (i > 0 && ok) ok = wait(&bar.p_free, (i - 1) & 1);
       ok = __all_sync(kFull, ok);
       tc_fence_after();
-      bool moves = mx + ex > kTop + kSlack;
-      if (fresh) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) moves |= ((fresh >> c) & 1u) && y[c] > -INFINITY;
-      }
       if (softmax_any(moves)) {
         // References move: to each row's largest y + ex of the tile, over its 128 tokens.
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const float w = warp_max(y[c] + ex);
+          const float w = warp_max((c & 1 ? y[c / 2].y : y[c / 2].x) + ex);
           if (lane == 0) red_s[quad * N + col + c] = w;
         }
         softmax_sync();
-#pragma unroll
-        for (int c0 = 0; c0 < C; c0 += 8) {
-          float al[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int k = col + c0 + c;
-            const float top = fmaxf(fmaxf(red_s[k], red_s[N + k]), fmaxf(red_s[2 * N + k], red_s[3 * N + k]));
-            const bool first = ((fresh >> (c0 + c)) & 1u) && top > -INFINITY;
+        if (warp < (N + 31) / 32) {
+          bool still = false;
+          if (tid < N) {
+            const float top = fmaxf(fmaxf(red_s[tid], red_s[N + tid]), fmaxf(red_s[2 * N + tid], red_s[3 * N + tid]));
+            const bool was = (fresh_s[warp] >> lane) & 1u, first = was && top > -INFINITY;
             const float to = ceilf(top) - kTop, up = first ? to : fmaxf(to, 0.0f);
-            if (first) fresh &= ~(1u << (c0 + c));
-            if (quad == 0 && lane == 0) m_s[(flip ^ 1) * N + k] = m_s[flip * N + k] + up;
-            al[c] = first ? 1.0f : exp2f(-up);  // (a first score: nothing accumulated yet)
-            y[c0 + c] -= up;
-            l[c0 + c] *= al[c];
+            still = was && !first;
+            m_s[tid] += up;
+            up_s[tid] = up;
+            f_s[tid] = first ? 1.0f : exp2f(-up);  // (a first score: nothing accumulated yet)
           }
-          if (i > 0) {
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              uint32_t v[8];
-              tmem_ld<8>(tb + S::TO + j * N + col + c0 + lanes, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 8; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * al[c]);
-              tmem_st<8>(tb + S::TO + j * N + col + c0 + lanes, v);
-            }
-          }
+          const uint32_t left = __ballot_sync(kFull, still);
+          if (lane == 0) fresh_s[warp] = left;
         }
-        tmem_wait_st();
-        flip ^= 1;
         softmax_sync();
-      }
-      const float vs = PT ? sc : 1.0f;
-      uint8_t* prow = sm + S::P + (tok >> 3) * (N * 16) + (tok & 7) * 16 + (col >> 3) * 128;
+        fresh = (fresh_s[col >> 5] >> (col & 31)) & ((1u << C) - 1);
+        float2 f[C / 2];
+        bool any = false;
 #pragma unroll
-      for (int c = 0; c < C; c += 8) {
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float2 w = make_float2(ex2(y[c + e]), ex2(y[c + e + 1]));
-          l[c + e] += w.x;
-          l[c + e + 1] += w.y;
-          if (PT) {
-            w = __fmul2_rn(w, make_float2(vs, vs));
-            if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
-              if (y[c + e] == -INFINITY) w.x = 0.0f;
-              if (y[c + e + 1] == -INFINITY) w.y = 0.0f;
-            }
-          }
-          p[e / 2] = h2_as_u32(__floats2half2_rn(w.x, w.y));
+        for (int c = 0; c < C; c += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(up_s + col + c), g = *reinterpret_cast<const float4*>(f_s + col + c);
+          y[c / 2] = __fadd2_rn(y[c / 2], make_float2(-u.x, -u.y));
+          y[c / 2 + 1] = __fadd2_rn(y[c / 2 + 1], make_float2(-u.z, -u.w));
+          f[c / 2] = make_float2(g.x, g.y);
+          f[c / 2 + 1] = make_float2(g.z, g.w);
+          any |= g.x != 1.0f || g.y != 1.0f || g.z != 1.0f || g.w != 1.0f;
         }
-        *reinterpret_cast<uint4*>(prow + (c >> 3) * 128) = make_uint4(p[0], p[1], p[2], p[3]);
+        if (i > 0 && any) {  // (the same for all tokens)
+#pragma unroll
+          for (int c = 0; c < C / 2; ++c) l[c] = __fmul2_rn(l[c], f[c]);
+#pragma unroll 1
+          for (int j = 0; j < NB; ++j) {
+            uint32_t v[C];
+            tmem_ld<C>(tb + S::TO + j * N + col + lanes, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < C; c += 2) {
+              asm volatile("" : "+r"(v[c]), "+r"(v[c + 1]));
+              const float2 o = __fmul2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f[c / 2]);
+              v[c] = __float_as_uint(o.x);
+              v[c + 1] = __float_as_uint(o.y);
+            }
+            tmem_st<C>(tb + S::TO + j * N + col + lanes, v);
+          }
+          tmem_wait_st();
+        }
+      }
+      uint32_t p[C / 2];
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) {
+        float2 w = make_float2(ex2(y[c].x), ex2(y[c].y));
+        l[c] = __fadd2_rn(l[c], w);
+        if (PT) {
+          w = __fmul2_rn(w, make_float2(sc, sc));
+          if (masked) {  // a weight of zero stays zero whatever the scale of a token that is not seen
+            if (y[c].x == -INFINITY) w.x = 0.0f;
+            if (y[c].y == -INFINITY) w.y = 0.0f;
+          }
+        }
+        p[c] = h2_as_u32(__floats2half2_rn(w.x, w.y));
+      }
+      uint8_t* prow = sm + S::P + (tok >> 3) * (N * 16) + (tok & 7) * 16 + (col >> 3) * 128 + (col & 7) * 2;
+      if constexpr (C >= 8) {
+#pragma unroll
+        for (int c = 0; c < C / 2; c += 4) *reinterpret_cast<uint4*>(prow + (c >> 2) * 128) = make_uint4(p[c], p[c + 1], p[c + 2], p[c + 3]);
+      } else {
+        *reinterpret_cast<uint2*>(prow) = make_uint2(p[0], p[1]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -535,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     if (!ok) failed_s = 1;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float x = l[c];
+      float x = c & 1 ? l[c / 2].y : l[c / 2].x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
       if (lane == 0) red_s[quad * N + col + c] = x;
@@ -545,20 +590,23 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     if (failed && tid == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_TIMEOUT);
     if (tid < N) {
       const float sum = red_s[tid] + red_s[N + tid] + red_s[2 * N + tid] + red_s[3 * N + tid];
-      const float m = m_s[flip * N + tid];
       f_s[tid] = sum == 0.0f ? 0.0f : a.num_splits > 1 ? tensor : tensor / sum;  // (a NaN score makes its row NaN)
       if (tid < t.count && !failed) {
         const long long row = row0 + tid;
         if (a.num_splits > 1)
-          st_chk(reinterpret_cast<float2*>(a.ws_ml) + row * a.num_splits + split, make_float2(sum == 0.0f ? -INFINITY : m, sum),
+          st_chk(reinterpret_cast<float2*>(a.ws_ml) + row * a.num_splits + split, make_float2(sum == 0.0f ? -INFINITY : m_s[tid], sum),
                  a.ws_span, a.pool);
         else if (a.lse)
-          st_chk(a.lse + row, sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e), a.lse_span, a.pool);
+          st_chk(a.lse + row, sum == 0.0f ? -INFINITY : (m_s[tid] + log2f(sum)) * (1.0f / kLog2e), a.lse_span, a.pool);
       }
     }
     softmax_sync();
-    // O^T: a lane has a channel, so a warp's store is 32 neighbouring channels of a row
     if (!failed && (n > 0 || a.num_splits == 1)) {
+      // O^T: a lane has a channel.  Partials leave as 32 neighbouring floats of a row to a
+      // warp's store; fp16 rows go through shared memory (the ring is free) and leave 16
+      // bytes a lane.
+      constexpr int OROW = L * 2 + 16;
+      uint8_t* stage = sm + S::RING;
 #pragma unroll 1
       for (int j = 0; j < NB; ++j) {
         uint32_t v[C];
@@ -568,16 +616,27 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
 #pragma unroll
           for (int c = 0; c < C; ++c) asm volatile("" : "+r"(v[c]));
         }
+        const int ch = 128 * j + tok;
+        float* po = a.ws_o + ((row0 + col) * a.num_splits + split) * L + ch;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          if (col + c >= t.count) break;
           const float f = f_s[col + c];
           const float x = n > 0 && f != 0.0f ? __uint_as_float(v[c]) * f : 0.0f;
-          const long long row = row0 + col + c;
-          const int ch = 128 * j + tok;
-          if (a.num_splits > 1) st_chk(a.ws_o + (row * a.num_splits + split) * L + ch, x, a.ws_span, a.pool);
-          else st_chk(static_cast<__half*>(a.out) + row * L + ch, __float2half_rn(x), a.out_span, a.pool);
+          if (a.num_splits == 1) {
+            *reinterpret_cast<__half*>(stage + (col + c) * OROW + 2 * ch) = __float2half_rn(x);
+          } else if (col + c < t.count) {
+            st_chk(po, x, a.ws_span, a.pool);
+            po += (long long)a.num_splits * L;
+          }
         }
+      }
+      if (a.num_splits == 1) {
+        softmax_sync();
+        __half* out = static_cast<__half*>(a.out) + row0 * L;
+#pragma unroll 4
+        for (int it = tid; it < t.count * (L / 8); it += kSoftmax)
+          st_chk(reinterpret_cast<uint4*>(out) + it, *reinterpret_cast<const uint4*>(stage + it / (L / 8) * OROW + it % (L / 8) * 16),
+                 a.out_span, a.pool);
       }
     }
   }
