@@ -23,12 +23,14 @@
 // port.  The rotary part goes through tensor memory instead (32 cycles at N = 64), which
 // also leaves room for P.
 //
-// Roles (28 warps, one CTA per SM):
+// Roles (32 warps, one CTA per SM):
 //  warps 0-15   softmax: thread = token of the tile and a quarter of the rows;
-//  warps 16-23  dequantization: a warp has one page of the tile; 128 channels of the tile
-//               are one entry of a ring, loaded some entries ahead, converted before the
-//               wait for it and stored after;
-//  warp 24      issues the products (25-27 only fill its warpgroup).
+//  warps 16-23  dequantization, in teams: 128 channels of the tile are one entry of a ring,
+//               and a team takes every second or fourth entry.  A warp's loads in flight are
+//               those of its next entry alone: a wait for some of a warp's loads would wait
+//               for later ones too;
+//  warps 24-27  the tokens' rotary parts (into tensor memory) and scales, one tile ahead;
+//  warp 28      issues the products (29-31 only fill its warpgroup).
 // The ring's entries are released by the value products, 128 channels at a time, so the
 // next tile is dequantized and its scores begin while these run.  Where ring and tensor
 // memory hold more than a tile (fewer rows, L = 256), its first scores go before them.
@@ -43,21 +45,27 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128;
-constexpr int kThreads = 896, kSoftmax = 512;
-constexpr int kDequantWarp = 16, kIssueWarp = 24;
+constexpr int kThreads = 1024, kSoftmax = 512;
+constexpr int kDequantWarp = 16, kRopeWarp = 24, kIssueWarp = 28;
 constexpr int kEntry = kTok * 128 * 2;     // one ring entry: 128 tokens x 128 channels of fp16
-constexpr int kLbo = 128, kSbo = 2048;     // core matrices (8 tokens x 16 bytes): along channels, along tokens
+// An entry holds its 64-channel halves one after the other, each as 128-byte rows of tokens
+// with the 16-byte chunks of row t at chunk ^ (t % 8): the 128-byte swizzle of both a
+// K-major (tokens x channels) and an MN-major (channels x tokens) operand.
+constexpr int kHalf = kEntry / 2, kGroup = 1024;  // bytes of a half; of 8 tokens in it
+constexpr int kLbo = 128;                  // Q, unswizzled core matrices (8 rows x 16 bytes): along channels
 constexpr int kScaleTiles = 4;             // tiles whose scales are kept
 constexpr float kTop = 6.0f, kSlack = 8.0f;
 
 template <int L, int N>
 struct Shape {
-  // Registers a thread (the launch gives 72): 512 softmax + 256 dequant + 128 issue <= 896 x 72.
-  static constexpr int RS = N == 64 ? 72 : 56, RD = N == 64 ? 88 : 112, RI = N == 64 ? 40 : 56;
-  static_assert(512 * RS + 256 * RD + 128 * RI <= 896 * 72, "registers");
-  // Ring entries that a dequantizing warp has loaded ahead: with 64 rows the products take
-  // longer than the loads, with fewer the loads are what there is to wait for.
-  static constexpr int AHEAD = N == 64 ? 2 : L / 128;
+  // Teams of dequantizing warps: with 64 rows the products take longer than the loads, with
+  // fewer the loads are what there is to wait for, and a whole tile is in flight.
+  static constexpr int TEAMS = N == 64 ? 2 : L / 128;
+  static constexpr int WARPS = 8 / TEAMS, PAGES = TEAMS;  // of a team; of a warp
+  // Registers a thread (the launch gives 64).
+  static constexpr int RS = N == 64 ? 72 : TEAMS == 2 ? 64 : 48, RD = N == 64 ? 72 : TEAMS == 2 ? 80 : 112,
+                       RR = N == 64 ? 40 : TEAMS == 2 ? 56 : 48, RI = N == 64 ? 40 : TEAMS == 2 ? 40 : 48;
+  static_assert(512 * RS + 256 * RD + 128 * RR + 128 * RI <= 1024 * 64, "registers");
   static constexpr int NB = L / 128;                   // ring entries of a tile
   static constexpr int C = N / 4;                      // rows of a softmax thread
   static constexpr int QCH = (L + kLatentRope) / 8;    // 16-byte chunks of a query row
@@ -70,12 +78,12 @@ struct Shape {
   static constexpr int RED = SEES + N * 4;             // [4][N]
   static constexpr int UP = RED + 4 * N * 4;           // [N] what a reference moves by
   static constexpr int F = UP + N * 4;                 // [N] the factor that goes with it; at the end, the output's
-  static constexpr int REST = (F + N * 4 + 127) / 128 * 128;
-  static constexpr int FIT = (227 * 1024 - 1024 - 128 - REST) / kEntry;
+  static constexpr int REST = (F + N * 4 + 1023) / 1024 * 1024;
+  static constexpr int FIT = (227 * 1024 - 1024 - 1024 - REST) / kEntry;
   static constexpr int SLOTS = FIT < 6 ? FIT : 6;
   static constexpr int RING = REST;
   static constexpr int BYTES = RING + SLOTS * kEntry;
-  static constexpr size_t dynamic() { return BYTES + 128; }
+  static constexpr size_t dynamic() { return BYTES + 1024; }
   // tensor memory: score buffers (latent, rotary), O^T by 128 channels, rotary operands of two tiles
   static constexpr int SB = NB * N + 64 + 4 * N <= 512 ? 2 : 1;
   static constexpr int TO = SB * 2 * N, TR = TO + NB * N;
@@ -84,6 +92,7 @@ struct Shape {
   static_assert(SLOTS >= NB && TR + 64 <= 512, "fits");
 };
 
+constexpr uint64_t kSwizzle128 = 2ull << 61;  // of a shared-memory matrix descriptor
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -112,10 +121,29 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(r ^ ((r >> 31) & 0x7fffffff));
 }
 
+// Bytes that no other warp of the SM reads.  What a load costs the SM's data port goes by
+// the lines that eight neighbouring lanes touch: 128 bytes at a time where the eight read
+// one line, 16 where they read eight.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+__device__ __forceinline__ void load32_once(const void* p, uint32_t* r) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+template <int R>
+__device__ __forceinline__ void set_registers() {  // (the launch gives 64)
+  if constexpr (R > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 // A lane's packed words of one ring entry (a page's 16 tokens x 128 channels): one-byte
-// codes in four loads, token (lane & 7) + 8 (r & 1), channels 16 c .. with
-// c = (lane >> 3) + 4 (r >> 1); E2M1 codes in two, token (lane & 7) + 8 r, channels
-// 32 (lane >> 3) .., with the two block scales as bytes 0 and 1.
+// codes in four loads, token (lane >> 3) + 4 r, channels 16 (lane & 7) ..; E2M1 codes in
+// two, token (lane >> 2) + 8 r, channels 32 (lane & 3) .., with the two block scales as
+// bytes 0 and 1.
 template <int MODE>
 struct Words {
   static constexpr int N = kLatentFour<MODE> ? 2 : 4;
@@ -126,18 +154,17 @@ struct Words {
 template <int MODE, int L>
 __device__ __forceinline__ void load_words(const uint8_t* page, int j, int lane, int valid, Words<MODE>& x) {
   using PG = LatentPage<MODE, L>;
-  const int a = lane & 7, b = lane >> 3;
 #pragma unroll
   for (int r = 0; r < Words<MODE>::N; ++r) {
-    const int tok = kLatentFour<MODE> ? a + 8 * r : a + 8 * (r & 1);
+    const int tok = kLatentFour<MODE> ? (lane >> 2) + 8 * r : (lane >> 3) + 4 * r;
     x.w[r] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (kLatentFour<MODE>) x.s[r] = 0u;
     if (tok < valid) {
       if constexpr (kLatentFour<MODE>) {
-        x.w[r] = __ldg(reinterpret_cast<const uint4*>(page + tok * PG::CODES + 64 * j + 16 * b));
-        x.s[r] = __ldg(reinterpret_cast<const uint16_t*>(page + PG::SCALES + tok * (L / 16) + 8 * j + 2 * b));
+        x.w[r] = load_once(page + tok * PG::CODES + 64 * j + 16 * (lane & 3));
+        x.s[r] = __ldg(reinterpret_cast<const uint16_t*>(page + PG::SCALES + tok * (L / 16) + 8 * j + 2 * (lane & 3)));
       } else {
-        x.w[r] = __ldg(reinterpret_cast<const uint4*>(page + tok * PG::CODES + 128 * j + 16 * (b + 4 * (r >> 1))));
+        x.w[r] = load_once(page + tok * PG::CODES + 128 * j + 16 * (lane & 7));
       }
     }
   }
@@ -158,16 +185,26 @@ __device__ __forceinline__ void convert(const Words<MODE>& x, uint4* out) {
     }
   }
 }
-// Into the ring entry at `op`, page `pg` of the tile: channel chunk c of token t at
-// (t % 8) 16 + c kLbo + (t / 8) kSbo.  Eight neighbouring lanes fill one core matrix.
+// Into the ring entry at `op`, page `pg` of the tile.  The eight lanes of a store's phase
+// have one token (E2M1: two) and every second chunk of both halves (one in four); the
+// second half's lanes take their chunks in another order, so that the eight differ.
 template <int MODE>
 __device__ __forceinline__ void store_chunks(const uint4* x, uint8_t* op, int pg, int lane) {
-  uint8_t* p = op + 2 * pg * kSbo + (lane & 7) * 16 + (kLatentFour<MODE> ? 4 : 2) * (lane >> 3) * kLbo;
+  constexpr bool FOUR = kLatentFour<MODE>;
+  const int half = FOUR ? (lane >> 1) & 1 : (lane >> 2) & 1;
+  const int chunk = FOUR ? 4 * (lane & 1) : 2 * (lane & 3);  // the lane's first
+  uint8_t* p = op + half * kHalf + 2 * pg * kGroup;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = kLatentFour<MODE> ? i >> 2 : i >> 1;  // load
-    const int at = kLatentFour<MODE> ? r * kSbo + (i & 3) * kLbo : (r & 1) * kSbo + (8 * (r >> 1) + (i & 1)) * kLbo;
-    *reinterpret_cast<uint4*>(p + at) = x[i];
+    if constexpr (FOUR) {
+      const int tok = (lane >> 2) + 8 * (i >> 2), k = (i & 3) ^ (2 * half);
+      const uint4 v = half ? x[i ^ 2] : x[i];
+      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + (tok & 7) * 128 + (((chunk + k) ^ (tok & 7)) << 4)) = v;
+    } else {
+      const int tok = (lane >> 3) + 4 * (i >> 1), k = (i & 1) ^ half;
+      const uint4 v = half ? x[i ^ 1] : x[i];
+      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + (tok & 7) * 128 + (((chunk + k) ^ (tok & 7)) << 4)) = v;
+    }
   }
 }
 
@@ -182,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   constexpr int NB = S::NB, C = S::C;
   constexpr bool PT = kLatentTokenScale<MODE>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
   __shared__ RowTile tile_s;
@@ -202,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   } else if (warp == 1) {
     if (elect_one()) {
       for (int i = 0; i < 6; ++i) {
-        mbar_init(&bar.full[i], 8);
+        mbar_init(&bar.full[i], S::WARPS);
         mbar_init(&bar.free[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar.rope_full[i], 8);
+        mbar_init(&bar.rope_full[i], 4);
         mbar_init(&bar.rope_free[i], 1);
         mbar_init(&bar.s_full[i], 2);
       }
@@ -236,114 +273,121 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   const uint32_t tb = tmem_s;
   bool ok = true;
 
-  if (warp >= kDequantWarp && warp < kIssueWarp) {
+  // page id of the tile's page pg; -1 past the last token, or where it lies outside the pool
+  auto page_id = [&](int i, int pg) -> int {
+    const int page = (i0 + i) * 8 + pg;
+    return i < n && page * 16 < most ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page) : -1;
+  };
+  auto page_at = [&](int id) { return a.pool + kHeaderBytes + (size_t)max(id, 0) * a.block_bytes; };
+  auto outside = [&](int id) { return id < 0 || id >= a.num_pages; };
+
+  if (warp >= kDequantWarp && warp < kRopeWarp) {
     // ------------------------------------------------------------ dequantization
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::RD));
-    // This warp's page is number pg of the tile; its rotary rows are 32 channels (half hf) of
-    // the 32 tokens whose lanes of tensor memory it reaches: pages 2 quad and 2 quad + 1.
-    const int quad = warp & 3, hf = (warp - kDequantWarp) >> 2, pg = 2 * quad + hf;
-    // lane's page id of tile i: that of page 2 quad in lanes 0-15, of the next in 16-31
-    auto page_id = [&](int i) -> int {
-      const int page = (i0 + i) * 8 + 2 * quad + (lane >> 4);
-      return i < n && page * 16 < most ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page) : -1;
-    };
-    auto checked = [&](int id, int i) -> int {
-      const int page = (i0 + i) * 8 + 2 * quad + (lane >> 4);
-      if (i < n && page * 16 < most && (id < 0 || id >= a.num_pages)) {
-        if ((lane & 15) == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
-        return -1;
+    set_registers<S::RD>();
+    const int team = (warp - kDequantWarp) / S::WARPS, first = (warp - kDequantWarp) % S::WARPS;
+    Words<MODE> words[S::PAGES];  // of pages first, first + WARPS, ..
+    int ids = page_id(0, lane & 7), ahead = page_id(1, lane & 7);  // the tile's eight, lane by lane, and the next tile's
+    auto load = [&](int id8, int i, int j) {
+#pragma unroll
+      for (int u = 0; u < S::PAGES; ++u) {
+        const int pg = first + S::WARPS * u, id = __shfl_sync(kFull, id8, pg);
+        const int valid = outside(id) ? 0 : min(16, most - ((i0 + i) * 8 + pg) * 16);
+        load_words<MODE, L>(page_at(valid > 0 ? id : 0), j, lane, valid, words[u]);
       }
-      return id;
     };
-    Words<MODE> words[S::AHEAD];
-    uint4 rope[4];
-    float sc = -1.0f;   // this page's token `lane` (lanes 0-15): its scale, -1 where it is not there
-    const uint8_t *page = nullptr, *now = nullptr;  // of the tile opened last, and of the one being stored
-    int valid = 0, valid_now = 0;
-    auto open_tile = [&](int id, int i) {  // the page, its valid tokens, its rotary rows and scales
-      const int mine = __shfl_sync(kFull, id, hf * 16);
-      page = a.pool + kHeaderBytes + (size_t)max(mine, 0) * a.block_bytes;
-      valid = mine < 0 ? 0 : min(16, most - ((i0 + i) * 8 + pg) * 16);
-      const int rtok = lane & 15;
-      const bool there = id >= 0 && ((i0 + i) * 8 + 2 * quad + (lane >> 4)) * 16 + rtok < most;
-      const uint4* rp = reinterpret_cast<const uint4*>(a.pool + kHeaderBytes + (size_t)max(id, 0) * a.block_bytes + PG::ROPE +
-                                                       rtok * kLatentRope * 2 + hf * 64);
+    load(ids, 0, team);
+    int slot = team, round = 0;
+    for (int i = 0; i < n; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) rope[e] = there ? __ldg(rp + e) : make_uint4(0u, 0u, 0u, 0u);
-      sc = -1.0f;
-      if (lane < valid) sc = PT ? __ldg(reinterpret_cast<const float*>(page + PG::SCALES) + lane) : 1.0f;
+      for (int j0 = 0; j0 < NB; j0 += S::TEAMS) {
+        uint4 h[8];
+        convert<MODE>(words[0], h);
+        if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
+        if (!__all_sync(kFull, ok)) break;
+        uint8_t* op = sm + S::RING + slot * kEntry;
+#pragma unroll
+        for (int u = 0; u < S::PAGES; ++u) {
+          if (u > 0) convert<MODE>(words[u], h);
+          store_chunks<MODE>(h, op, first + S::WARPS * u, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.full[slot]);
+        if (j0 + S::TEAMS < NB) {
+          load(ids, i, j0 + S::TEAMS + team);
+        } else {
+          load(ahead, i + 1, team);
+          ids = ahead;
+          ahead = page_id(i + 2, lane & 7);
+        }
+        slot += S::TEAMS;
+        if (slot >= S::SLOTS) {
+          slot -= S::SLOTS;
+          ++round;
+        }
+      }
+    }
+  } else if (warp >= kRopeWarp && warp < kIssueWarp) {
+    // ------------------------------------------------------------ rotary parts and scales
+    set_registers<S::RR>();
+    // thread = token of the tile, whose lane of tensor memory its warp reaches
+    const int quad = warp & 3, tok = 32 * quad + lane;
+    uint32_t rope[32];
+    float sc = -1.0f;  // the token's scale, -1 where it is not there
+    auto load = [&](int i, int id) {
+      const bool seen = i < n && (i0 + i) * kTok + tok < most, there = seen && !outside(id);
+      if (seen && !there && (lane & 15) == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
+      const uint8_t* page = page_at(there ? id : 0);
+      const uint8_t* row = page + PG::ROPE + (tok & 15) * kLatentRope * 2;
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) rope[e + k] = 0u;
+        if (there) load32_once(row + 4 * e, rope + e);
+      }
+      sc = !there ? -1.0f : PT ? __ldg(reinterpret_cast<const float*>(page + PG::SCALES) + (tok & 15)) : 1.0f;
     };
-    int id = checked(page_id(0), 0), ahead = page_id(1);
-    open_tile(id, 0);
-#pragma unroll
-    for (int j = 0; j < S::AHEAD; ++j) load_words<MODE, L>(page, j, lane, valid, words[j]);
-    int slot = 0, round = 0;
+    int ahead = page_id(1, tok >> 4);
+    load(0, page_id(0, tok >> 4));
     for (int i = 0; i < n; ++i) {
       const int buf = i & 1;
       if (i >= 2 && ok) ok = wait(&bar.rope_free[buf], ((i >> 1) - 1) & 1);
       if (!__all_sync(kFull, ok)) break;
       tc_fence_after();
-      {
-        uint32_t r[16];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          r[4 * e] = rope[e].x;
-          r[4 * e + 1] = rope[e].y;
-          r[4 * e + 2] = rope[e].z;
-          r[4 * e + 3] = rope[e].w;
-        }
-        tmem_st<16>(tb + S::TR + 32 * buf + 16 * hf + ((uint32_t)(32 * quad) << 16), r);
-      }
-      // The scales' last readers, the softmax of tile i - 4, are done: its value products came
-      // after them and have released the entries that tile i - 1 was stored to.
-      if (lane < 16) sc_s[(i & (kScaleTiles - 1)) * kTok + pg * 16 + lane] = sc;
+      tmem_st<32>(tb + S::TR + 32 * buf + ((uint32_t)(32 * quad) << 16), rope);
+      // The scales' last readers, the softmax of tile i - 4, are done: the scores of tile i - 2
+      // that have released this buffer were issued after it.
+      sc_s[(i & (kScaleTiles - 1)) * kTok + tok] = sc;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
-      now = page;
-      valid_now = valid;
-      id = checked(ahead, i + 1);
-      ahead = page_id(i + 2);
-      open_tile(id, i + 1);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        uint4 h[8];
-        convert<MODE>(words[j % S::AHEAD], h);
-        if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
-        if (!__all_sync(kFull, ok)) break;
-        store_chunks<MODE>(h, sm + S::RING + slot * kEntry, pg, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.full[slot]);
-        if (j + S::AHEAD < NB) load_words<MODE, L>(now, j + S::AHEAD, lane, valid_now, words[j % S::AHEAD]);
-        else load_words<MODE, L>(page, j + S::AHEAD - NB, lane, valid, words[j % S::AHEAD]);  // of tile i + 1
-        if (++slot == S::SLOTS) {
-          slot = 0;
-          ++round;
-        }
-      }
+      load(i + 1, ahead);
+      ahead = page_id(i + 2, tok >> 4);
     }
   } else if (warp >= kIssueWarp) {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::RI));
+    set_registers<S::RI>();
     if (warp == kIssueWarp && n > 0) {
       constexpr uint32_t kIdescS = umma_idesc_f16(128, N), kIdescO = umma_idesc_f16(128, N) | (1u << 15) | (1u << 16);
       const uint64_t dq = umma_sdesc(smem_u32(sm + S::Q), kLbo, S::QSBO);
-      const uint64_t dk = umma_sdesc(smem_u32(sm + S::RING), kLbo, kSbo);      // tokens x channels
-      const uint64_t dv = umma_sdesc(smem_u32(sm + S::RING), kSbo, kLbo);      // channels x tokens: the same bytes, MN-major
+      const uint64_t dk = umma_sdesc(smem_u32(sm + S::RING), 16, kGroup) | kSwizzle128;     // tokens x channels
+      const uint64_t dv = umma_sdesc(smem_u32(sm + S::RING), kHalf, kGroup) | kSwizzle128;  // channels x tokens: the same bytes
       const uint64_t dp = umma_sdesc(smem_u32(sm + S::P), N * 16, 128);        // rows x tokens, MN-major
+      // The fence between the warps' stores and the tensor core's reads stands here, after the
+      // wait for them: once for all of the warps that have arrived.
       int kslot = 0, kround = 0, vslot = 0;
       auto scores = [&](int i, int j) {  // of 128 channels
         if (ok) ok = wait(&bar.full[kslot], kround & 1);
         if (!ok) return;
+        fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
           const uint32_t D = tb + (S::SB == 2 ? (i & 1) * 2 * N : 0);
           const uint64_t A = dk + (uint64_t)kslot * (kEntry >> 4), B = dq + (uint64_t)j * ((16 * kLbo) >> 4);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            umma_f16_ss(D, A + e * ((2 * kLbo) >> 4), B + e * ((2 * kLbo) >> 4), kIdescS, (j > 0 || e > 0) ? 1u : 0u);
+            umma_f16_ss(D, A + (e >> 2) * (kHalf >> 4) + (e & 3) * (32 >> 4), B + e * ((2 * kLbo) >> 4), kIdescS,
+                        (j > 0 || e > 0) ? 1u : 0u);
         }
         __syncwarp();
         if (++kslot == S::SLOTS) {
@@ -379,14 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
         }
         if (ok) ok = wait(&bar.p_full, i & 1);
         if (!ok) break;
+        fence_proxy_async_smem();
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < NB; ++j) {
           if (elect_one()) {
             const uint64_t A = dv + (uint64_t)vslot * (kEntry >> 4);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              umma_f16_ss(tb + S::TO + j * N, A + e * ((2 * kSbo) >> 4), dp + e * ((2 * N * 16) >> 4), kIdescO,
+              umma_f16_ss(tb + S::TO + j * N, A + e * ((2 * kGroup) >> 4), dp + e * ((2 * N * 16) >> 4), kIdescO,
                           (i > 0 || e > 0) ? 1u : 0u);
             tc_commit(&bar.free[vslot]);
             if (j == NB - 1) tc_commit(&bar.p_free);
@@ -403,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::RS));
+    set_registers<S::RS>();
     const long long row0 = latent_row(a, t, 0, t.r0);  // rows of a tile lie one after the other
     // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows
     constexpr int QN = (N * S::QCH + kSoftmax - 1) / kSoftmax;
@@ -568,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       } else {
         *reinterpret_cast<uint2*>(prow) = make_uint2(p[0], p[1]);
       }
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full);
