@@ -475,6 +475,7 @@ cudaError_t launch_latent_attention(const kvq_latent* c, const LatentPlan& p, La
 cudaError_t launch_latent_prompt(const kvq_latent* c, LatentArgs& a, cudaStream_t s) {
   a.num_splits = 1;
   spans(a, kLatentHead);
+  if (on_umma(c, a.out_f32)) return launch_latent_prompt_umma(c, a, s);
   return c->cfg.io_dtype == KVQ_F32 ? launch_plain<0, float, kLatentHead>(a, s) : launch_plain<0, __half, kLatentHead>(a, s);
 }
 
