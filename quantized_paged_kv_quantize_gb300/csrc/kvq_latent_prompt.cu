@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
     const uint32_t base = smem_u32(sm) + r0 * 128 + ((c ^ (r0 & 7)) << 4);
     const __half* q = static_cast<const __half*>(a.q) + ((long long)(t.q0 + t.r0) * a.Hq + head) * (kLatentHead + kLatentRope) + 8 * c;
 #pragma unroll 1
-    for (int u = 0; u < kKeyUnits * (last + 1); ++u) {
+    for (int u = 0; u < (n > 0 ? kKeyUnits * (last + 1) : 0); ++u) {  // (rows that see nothing: no one waits for these)
       const int b = u / kKeyUnits, part = u % kKeyUnits;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

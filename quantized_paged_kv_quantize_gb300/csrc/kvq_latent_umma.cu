@@ -23,14 +23,14 @@
 // port.  The rotary part goes through tensor memory instead (32 cycles at N = 64), which
 // also leaves room for P.
 //
-// Roles (32 warps, one CTA per SM):
+// Roles (28 warps, one CTA per SM):
 //  warps 0-15   softmax: thread = token of the tile and a quarter of the rows;
 //  warps 16-23  dequantization, in teams: 128 channels of the tile are one entry of a ring,
 //               and a team takes every second or fourth entry.  A warp's loads in flight are
 //               those of its next entry alone: a wait for some of a warp's loads would wait
-//               for later ones too;
-//  warps 24-27  the tokens' rotary parts (into tensor memory) and scales, one tile ahead;
-//  warp 28      issues the products (29-31 only fill its warpgroup).
+//               for later ones too.  With a tile's first entry a warp stores the rotary parts
+//               of 16 tokens (into tensor memory) and their scales;
+//  warp 24      issues the products (25-27 only fill its warpgroup).
 // The ring's entries are released by the value products, 128 channels at a time, so the
 // next tile is dequantized and its scores begin while these run.  Where ring and tensor
 // memory hold more than a tile (fewer rows, L = 256), its first scores go before them.
@@ -45,8 +45,8 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128;
-constexpr int kThreads = 1024, kSoftmax = 512;
-constexpr int kDequantWarp = 16, kRopeWarp = 24, kIssueWarp = 28;
+constexpr int kThreads = 896, kSoftmax = 512;
+constexpr int kDequantWarp = 16, kIssueWarp = 24;
 constexpr int kEntry = kTok * 128 * 2;     // one ring entry: 128 tokens x 128 channels of fp16
 // An entry holds its 64-channel halves one after the other, each as 128-byte rows of tokens
 // with the 16-byte chunks of row t at chunk ^ (t % 8): the 128-byte swizzle of both a
@@ -62,10 +62,9 @@ struct Shape {
   // fewer the loads are what there is to wait for, and a whole tile is in flight.
   static constexpr int TEAMS = N == 64 ? 2 : L / 128;
   static constexpr int WARPS = 8 / TEAMS, PAGES = TEAMS;  // of a team; of a warp
-  // Registers a thread (the launch gives 64).
-  static constexpr int RS = N == 64 ? 72 : TEAMS == 2 ? 64 : 48, RD = N == 64 ? 72 : TEAMS == 2 ? 80 : 112,
-                       RR = N == 64 ? 40 : TEAMS == 2 ? 56 : 48, RI = N == 64 ? 40 : TEAMS == 2 ? 40 : 48;
-  static_assert(512 * RS + 256 * RD + 128 * RR + 128 * RI <= 1024 * 64, "registers");
+  // Registers a thread (the launch gives 72).
+  static constexpr int RS = N == 64 ? 72 : TEAMS == 2 ? 64 : 56, RD = N == 64 ? 88 : TEAMS == 2 ? 96 : 112, RI = N == 64 ? 40 : 56;
+  static_assert(512 * RS + 256 * RD + 128 * RI <= 896 * 72, "registers");
   static constexpr int NB = L / 128;                   // ring entries of a tile
   static constexpr int C = N / 4;                      // rows of a softmax thread
   static constexpr int QCH = (L + kLatentRope) / 8;    // 16-byte chunks of a query row
@@ -135,8 +134,8 @@ __device__ __forceinline__ void load32_once(const void* p, uint32_t* r) {
                : "l"(p));
 }
 template <int R>
-__device__ __forceinline__ void set_registers() {  // (the launch gives 64)
-  if constexpr (R > 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+__device__ __forceinline__ void set_registers() {  // (the launch gives 72)
+  if constexpr (R > 72) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
@@ -169,43 +168,58 @@ __device__ __forceinline__ void load_words(const uint8_t* page, int j, int lane,
     }
   }
 }
-// The words as fp16: eight chunks of 16 bytes, in the order that store_chunks takes.
+// As fp16: eight chunks of 16 bytes, in the order of store_chunks.  The eight lanes of a
+// store's phase have one token (E2M1: two) and every second chunk of both halves (one in
+// four); the second half's lanes take their chunks in another order, so that the eight differ.
 template <int MODE>
-__device__ __forceinline__ void convert(const Words<MODE>& x, uint4* out) {
+__device__ __forceinline__ int second_half(int lane) { return kLatentFour<MODE> ? (lane >> 1) & 1 : (lane >> 2) & 1; }
+template <int MODE>
+__device__ __forceinline__ void convert(const Words<MODE>& x, int lane, uint4* out) {
+  const int half = second_half<MODE>(lane);
 #pragma unroll
   for (int r = 0; r < Words<MODE>::N; ++r) {
     const uint32_t in[4] = {x.w[r].x, x.w[r].y, x.w[r].z, x.w[r].w};
-    constexpr int HALVES = kLatentFour<MODE> ? 2 : 1;  // sixteen codes each
+    uint32_t h[8];
+    if constexpr (kLatentFour<MODE>) {
 #pragma unroll
-    for (int u = 0; u < HALVES; ++u) {
-      uint32_t h[8];
-      latent_codes16<MODE>(in + 2 * u, kLatentFour<MODE> ? x.s[r] >> (8 * u) : 0u, h);
-      out[2 * (HALVES * r + u)] = make_uint4(h[0], h[1], h[2], h[3]);
-      out[2 * (HALVES * r + u) + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+      for (int u = 0; u < 2; ++u) {  // the second half's lanes begin with their last sixteen codes
+        const uint32_t from[2] = {half ? in[2 * (u ^ 1)] : in[2 * u], half ? in[2 * (u ^ 1) + 1] : in[2 * u + 1]};
+        latent_codes16<MODE>(from, x.s[r] >> (8 * (half ? u ^ 1 : u)), h);
+        out[4 * r + 2 * u] = make_uint4(h[0], h[1], h[2], h[3]);
+        out[4 * r + 2 * u + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+    } else {  // with their last eight
+      const uint32_t from[4] = {half ? in[2] : in[0], half ? in[3] : in[1], half ? in[0] : in[2], half ? in[1] : in[3]};
+      latent_codes16<MODE>(from, 0u, h);
+      out[2 * r] = make_uint4(h[0], h[1], h[2], h[3]);
+      out[2 * r + 1] = make_uint4(h[4], h[5], h[6], h[7]);
     }
   }
 }
-// Into the ring entry at `op`, page `pg` of the tile.  The eight lanes of a store's phase
-// have one token (E2M1: two) and every second chunk of both halves (one in four); the
-// second half's lanes take their chunks in another order, so that the eight differ.
+// Into the ring entry at `op`, page `pg` of the tile.
 template <int MODE>
 __device__ __forceinline__ void store_chunks(const uint4* x, uint8_t* op, int pg, int lane) {
   constexpr bool FOUR = kLatentFour<MODE>;
-  const int half = FOUR ? (lane >> 1) & 1 : (lane >> 2) & 1;
-  const int chunk = FOUR ? 4 * (lane & 1) : 2 * (lane & 3);  // the lane's first
-  uint8_t* p = op + half * kHalf + 2 * pg * kGroup;
+  const int half = second_half<MODE>(lane);
+  const int chunk = FOUR ? (4 * (lane & 1)) ^ (2 * half) : (2 * (lane & 3)) ^ half;  // the lane's first
+  const int row = FOUR ? lane >> 2 : lane >> 3;                                      // its first token
+  uint8_t* p = op + half * kHalf + 2 * pg * kGroup + row * 128;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if constexpr (FOUR) {
-      const int tok = (lane >> 2) + 8 * (i >> 2), k = (i & 3) ^ (2 * half);
-      const uint4 v = half ? x[i ^ 2] : x[i];
-      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + (tok & 7) * 128 + (((chunk + k) ^ (tok & 7)) << 4)) = v;
-    } else {
-      const int tok = (lane >> 3) + 4 * (i >> 1), k = (i & 1) ^ half;
-      const uint4 v = half ? x[i ^ 1] : x[i];
-      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + (tok & 7) * 128 + (((chunk + k) ^ (tok & 7)) << 4)) = v;
-    }
+    if constexpr (FOUR)  // tokens row + 8 r: the same place in the group
+      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + ((chunk ^ row ^ (i & 3)) << 4)) = x[i];
+    else  // tokens row + 4 r: the row's bit 2 changes with r
+      *reinterpret_cast<uint4*>(p + (i >> 2) * kGroup + ((i >> 1) & 1) * 512 + ((chunk ^ row ^ (i & 1) ^ (4 * ((i >> 1) & 1))) << 4)) = x[i];
   }
+}
+// 16 rows of tensor memory x 32 columns: lane's row lane / 4, r[4 k] and r[4 k + 1] columns
+// 8 k + 2 (lane % 4) and the next; r[4 k + 2] and r[4 k + 3] the row eight further on.
+__device__ __forceinline__ void tmem_st_16x256b(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 struct Bars {
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
         mbar_init(&bar.free[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar.rope_full[i], 4);
+        mbar_init(&bar.rope_full[i], 8);
         mbar_init(&bar.rope_free[i], 1);
         mbar_init(&bar.s_full[i], 2);
       }
@@ -273,41 +287,84 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   const uint32_t tb = tmem_s;
   bool ok = true;
 
-  // page id of the tile's page pg; -1 past the last token, or where it lies outside the pool
-  auto page_id = [&](int i, int pg) -> int {
-    const int page = (i0 + i) * 8 + pg;
-    return i < n && page * 16 < most ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page) : -1;
-  };
-  auto page_at = [&](int id) { return a.pool + kHeaderBytes + (size_t)max(id, 0) * a.block_bytes; };
-  auto outside = [&](int id) { return id < 0 || id >= a.num_pages; };
-
-  if (warp >= kDequantWarp && warp < kRopeWarp) {
+  if (warp >= kDequantWarp && warp < kIssueWarp) {
     // ------------------------------------------------------------ dequantization
     set_registers<S::RD>();
-    const int team = (warp - kDequantWarp) / S::WARPS, first = (warp - kDequantWarp) % S::WARPS;
+    const int w = warp - kDequantWarp, team = w / S::WARPS, first = w % S::WARPS;
+    // rotary parts and scales: of the page whose tokens' lanes of tensor memory the warp reaches
+    const int mine = 2 * (warp & 3) + (w >> 2);
     Words<MODE> words[S::PAGES];  // of pages first, first + WARPS, ..
-    int ids = page_id(0, lane & 7), ahead = page_id(1, lane & 7);  // the tile's eight, lane by lane, and the next tile's
-    auto load = [&](int id8, int i, int j) {
+    uint32_t rope[16];
+    float sc;  // of token lane of page `mine` (lanes 0-15); -1 where it is not there
+    // the tile's eight page ids, lane by lane; -1 past the last token
+    auto page_ids = [&](int i) -> int {
+      const int page = (i0 + i) * 8 + (lane & 7);
+      return i < n && page * 16 < most ? __ldg(a.block_table + (long long)t.seq * a.max_pages + page) : -1;
+    };
+    auto page_at = [&](int ids, int i, int pg, int& valid) -> const uint8_t* {
+      const int id = __shfl_sync(kFull, ids, pg);
+      const bool in = id >= 0 && id < a.num_pages;
+      valid = in ? min(16, most - ((i0 + i) * 8 + pg) * 16) : 0;
+      return a.pool + kHeaderBytes + (size_t)(in ? id : 0) * a.block_bytes;
+    };
+    auto load = [&](int ids, int i, int j) {
 #pragma unroll
       for (int u = 0; u < S::PAGES; ++u) {
-        const int pg = first + S::WARPS * u, id = __shfl_sync(kFull, id8, pg);
-        const int valid = outside(id) ? 0 : min(16, most - ((i0 + i) * 8 + pg) * 16);
-        load_words<MODE, L>(page_at(valid > 0 ? id : 0), j, lane, valid, words[u]);
+        int valid;
+        const uint8_t* page = page_at(ids, i, first + S::WARPS * u, valid);
+        load_words<MODE, L>(page, j, lane, valid, words[u]);
       }
     };
+    // Four lanes have a row: its 32 bytes from 32 (lane % 4) in the columns 8 k + 2 (lane % 4),
+    // + 1 of the four steps k; the queries' rotary channels are in the same order.
+    auto load_rope = [&](int ids, int i) {
+      int valid;
+      const uint8_t* page = page_at(ids, i, mine, valid);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t x[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        const int tok = (lane >> 2) + 8 * g;
+        if (tok < valid) load32_once(page + PG::ROPE + tok * kLatentRope * 2 + 32 * (lane & 3), x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          rope[4 * k + 2 * g] = x[2 * k];
+          rope[4 * k + 2 * g + 1] = x[2 * k + 1];
+        }
+      }
+      sc = -1.0f;
+      if (lane < valid) sc = PT ? __ldg(reinterpret_cast<const float*>(page + PG::SCALES) + lane) : 1.0f;
+      if (i < n && valid == 0 && ((i0 + i) * 8 + mine) * 16 < most && lane == 0)
+        set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
+    };
+    int ids = page_ids(0), ahead = page_ids(1);
     load(ids, 0, team);
+    load_rope(ids, 0);
     int slot = team, round = 0;
     for (int i = 0; i < n; ++i) {
+      const int buf = i & 1;
+      if (i >= 2 && ok) ok = wait(&bar.rope_free[buf], ((i >> 1) - 1) & 1);
+      if (!__all_sync(kFull, ok)) break;
+      tc_fence_after();
+      tmem_st_16x256b(tb + S::TR + 32 * buf + ((uint32_t)(16 * mine) << 16), rope);
+      // The scales' last readers, the softmax of tile i - 4, are done: the scores of tile i - 2
+      // that have released this buffer were issued after it.
+      if (lane < 16) sc_s[(i & (kScaleTiles - 1)) * kTok + 16 * mine + lane] = sc;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
 #pragma unroll
       for (int j0 = 0; j0 < NB; j0 += S::TEAMS) {
+        // (one page is converted before the wait where registers allow it)
+        constexpr int EARLY = S::TEAMS == 2 ? 1 : 0;
         uint4 h[8];
-        convert<MODE>(words[0], h);
+        if (EARLY) convert<MODE>(words[0], lane, h);
         if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
         if (!__all_sync(kFull, ok)) break;
         uint8_t* op = sm + S::RING + slot * kEntry;
 #pragma unroll
         for (int u = 0; u < S::PAGES; ++u) {
-          if (u > 0) convert<MODE>(words[u], h);
+          if (u >= EARLY) convert<MODE>(words[u], lane, h);
           store_chunks<MODE>(h, op, first + S::WARPS * u, lane);
         }
         __syncwarp();
@@ -316,8 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
           load(ids, i, j0 + S::TEAMS + team);
         } else {
           load(ahead, i + 1, team);
+          load_rope(ahead, i + 1);
           ids = ahead;
-          ahead = page_id(i + 2, lane & 7);
+          ahead = page_ids(i + 2);
         }
         slot += S::TEAMS;
         if (slot >= S::SLOTS) {
@@ -325,44 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
           ++round;
         }
       }
-    }
-  } else if (warp >= kRopeWarp && warp < kIssueWarp) {
-    // ------------------------------------------------------------ rotary parts and scales
-    set_registers<S::RR>();
-    // thread = token of the tile, whose lane of tensor memory its warp reaches
-    const int quad = warp & 3, tok = 32 * quad + lane;
-    uint32_t rope[32];
-    float sc = -1.0f;  // the token's scale, -1 where it is not there
-    auto load = [&](int i, int id) {
-      const bool seen = i < n && (i0 + i) * kTok + tok < most, there = seen && !outside(id);
-      if (seen && !there && (lane & 15) == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
-      const uint8_t* page = page_at(there ? id : 0);
-      const uint8_t* row = page + PG::ROPE + (tok & 15) * kLatentRope * 2;
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) rope[e + k] = 0u;
-        if (there) load32_once(row + 4 * e, rope + e);
-      }
-      sc = !there ? -1.0f : PT ? __ldg(reinterpret_cast<const float*>(page + PG::SCALES) + (tok & 15)) : 1.0f;
-    };
-    int ahead = page_id(1, tok >> 4);
-    load(0, page_id(0, tok >> 4));
-    for (int i = 0; i < n; ++i) {
-      const int buf = i & 1;
-      if (i >= 2 && ok) ok = wait(&bar.rope_free[buf], ((i >> 1) - 1) & 1);
-      if (!__all_sync(kFull, ok)) break;
-      tc_fence_after();
-      tmem_st<32>(tb + S::TR + 32 * buf + ((uint32_t)(32 * quad) << 16), rope);
-      // The scales' last readers, the softmax of tile i - 4, are done: the scores of tile i - 2
-      // that have released this buffer were issued after it.
-      sc_s[(i & (kScaleTiles - 1)) * kTok + tok] = sc;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
-      load(i + 1, ahead);
-      ahead = page_id(i + 2, tok >> 4);
     }
   } else if (warp >= kIssueWarp) {
     // ------------------------------------------------------------ products
@@ -450,7 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     // ------------------------------------------------------------ softmax
     set_registers<S::RS>();
     const long long row0 = latent_row(a, t, 0, t.r0);  // rows of a tile lie one after the other
-    // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows
+    // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows.
+    // Rotary channels in the order of the keys' tensor memory: channels 16 m + 4 k .. + 3 are
+    // the m-th eight bytes of step k's 32.
     constexpr int QN = (N * S::QCH + kSoftmax - 1) / kSoftmax;
     {
       uint4 x[QN];  // (all loads in flight at once)
@@ -463,7 +485,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
 #pragma unroll
       for (int u = 0; u < QN; ++u) {
         const int it = tid + u * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
-        if (r < N) *reinterpret_cast<uint4*>(sm + S::Q + (r & 7) * 16 + c * kLbo + (r >> 3) * S::QSBO) = x[u];
+        uint8_t* row = sm + S::Q + (r & 7) * 16 + (r >> 3) * S::QSBO;
+        if (r >= N) continue;
+        if (c < L / 8) {
+          *reinterpret_cast<uint4*>(row + c * kLbo) = x[u];
+        } else {
+          const int d = 2 * (c - L / 8), m = d >> 2, k = d & 3;  // eight bytes each: d and d + 1 (of the same m)
+          *reinterpret_cast<uint2*>(row + (L / 8 + 2 * k + (m >> 1)) * kLbo + 8 * (m & 1)) = make_uint2(x[u].x, x[u].y);
+          *reinterpret_cast<uint2*>(row + (L / 8 + 2 * (k + 1) + (m >> 1)) * kLbo + 8 * (m & 1)) = make_uint2(x[u].z, x[u].w);
+        }
       }
     }
     if (tid < N) {
@@ -491,18 +521,23 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       float2 y[C / 2];
       const float sc = sc_s[(i & (kScaleTiles - 1)) * kTok + tok];
       {
-        uint32_t xc[C], xr[C];
-        tmem_ld<C>(tb + sb * 2 * N + col + lanes, xc);
-        tmem_ld<C>(tb + sb * 2 * N + N + col + lanes, xr);
+        // (the rotary scores first, then the others over the same registers)
+        const float ks = one * (PT ? sc : tensor);
+        uint32_t x[C];
+        tmem_ld<C>(tb + sb * 2 * N + N + col + lanes, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(xc[c]), "+r"(xr[c]));  // (no use before the wait)
-        const float2 ks = make_float2(one * (PT ? sc : tensor), one * (PT ? sc : tensor)), one2 = make_float2(one, one);
+        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(x[c]));  // (no use before the wait)
 #pragma unroll
-        for (int c = 0; c < C; c += 2) {
-          const float2 r = __fmul2_rn(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), one2);
-          y[c / 2] = __ffma2_rn(make_float2(__uint_as_float(xc[c]), __uint_as_float(xc[c + 1])), ks, r);
-        }
+        for (int c = 0; c < C; c += 2)
+          y[c / 2] = __fmul2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), make_float2(one, one));
+        tmem_ld<C>(tb + sb * 2 * N + col + lanes, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(x[c]));
+#pragma unroll
+        for (int c = 0; c < C; c += 2)
+          y[c / 2] = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), make_float2(ks, ks), y[c / 2]);
       }
       const int tk = (i0 + i) * kTok + tok;
       const bool masked = (i0 + i + 1) * kTok > fewest;

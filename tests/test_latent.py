@@ -508,3 +508,12 @@ def test_prompt_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), want)
+
+
+def test_prompt_rows_that_see_nothing():
+    """Tiles of rows without a key beside tiles with many: their zeros are not written over by copies in flight."""
+    p = Prompt([2, 300] * 20, [0, 300] * 20, 8, seed=6)
+    for _ in range(5):
+        out, lse = p.run()
+        none = torch.cat([torch.arange(302 * i, 302 * i + 2) for i in range(20)])
+        assert bool((out[none] == 0).all()) and bool((lse[none] == -math.inf).all())
