@@ -59,6 +59,10 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd
       : "memory");
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, 1u << 20); }
+// For the issuing warp: a wait whose result, and a number, that the compiler knows to be the
+// same in all lanes, so that a product's operands are in uniform registers.
+__device__ __forceinline__ bool wait_uniform(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -187,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
     if (warp == kIssueWarp && n > 0) {
       const uint64_t dq = umma_sdesc(smem_u32(sm + Smem::Q), 16, 1024) | kSwizzle128;
       const uint64_t dr = umma_sdesc(smem_u32(sm + Smem::RING), 16, 1024) | kSwizzle128;  // keys: K-major; values: MN-major, 64 channels
-      ok = wait(&bar.q_full, 0);
+      const uint32_t tm = uniform(tb);
+      ok = wait_uniform(&bar.q_full, 0);
       fence_proxy_async_smem();
       // O += P V of a block's last tile, then S of its next (over that P), the blocks in turn.
       // The fences between the copies and the tensor core's reads stand after the waits.
@@ -195,20 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
 #pragma unroll 1
         for (int b = 0; b <= last && ok; ++b) {
           const int nb = b ? n1 : n0;
+          const uint32_t s = uniform(tm + 128 * b);
           if (i > 0 && i <= nb) {
-            ok = wait(&bar.p_full[b], (i - 1) & 1);
+            ok = wait_uniform(&bar.p_full[b], (i - 1) & 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int unit = kTileUnits * (i - 1) + kKeyUnits + h, slot = unit & (kUnits - 1);
-              if (ok) ok = wait(&bar.full[slot], (unit / kUnits) & 1);
+              if (ok) ok = wait_uniform(&bar.full[slot], (unit / kUnits) & 1);
               if (!ok) break;
               fence_proxy_async_smem();
               tc_fence_after();
+              const uint64_t B = dr + uniform(slot * (kUnit >> 4));
+              const uint32_t after = uniform(i - 1);
               if (elect_one()) {
-                const uint64_t B = dr + (uint64_t)slot * (kUnit >> 4);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  umma_f16_ts(tb + 256 + 128 * b + 64 * h, tb + 128 * b + 8 * e, B + e * (2048 >> 4), kIdescPV, (i > 1 || e > 0) ? 1u : 0u);
+                for (int e = 0; e < 8; ++e) umma_f16_ts(s + 256 + 64 * h, s + 8 * e, B + e * (2048 >> 4), kIdescPV, e > 0 ? 1u : after);
                 if (b == last) tc_commit(&bar.free[slot]);
                 if (h == 1 && i == nb) tc_commit(&bar.o_full[b]);
               }
@@ -219,15 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
 #pragma unroll
             for (int p = 0; p < kKeyUnits; ++p) {
               const int unit = kTileUnits * i + p, slot = unit & (kUnits - 1);
-              if (ok) ok = wait(&bar.full[slot], (unit / kUnits) & 1);
+              if (ok) ok = wait_uniform(&bar.full[slot], (unit / kUnits) & 1);
               if (!ok) break;
               fence_proxy_async_smem();
               tc_fence_after();
+              const uint64_t A = dq + uniform((kKeyUnits * b + p) * (kUnit >> 4)), B = dr + uniform(slot * (kUnit >> 4));
               if (elect_one()) {
-                const uint64_t A = dq + (uint64_t)(kKeyUnits * b + p) * (kUnit >> 4), B = dr + (uint64_t)slot * (kUnit >> 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  umma_f16_ss(tb + 128 * b, A + e * (32 >> 4), B + e * (32 >> 4), kIdescQK, (p > 0 || e > 0) ? 1u : 0u);
+                  umma_f16_ss(s, A + e * (32 >> 4), B + e * (32 >> 4), kIdescQK, (p > 0 || e > 0) ? 1u : 0u);
                 if (b == last) tc_commit(&bar.free[slot]);
                 if (p == kKeyUnits - 1) tc_commit(&bar.s_full[b]);
               }

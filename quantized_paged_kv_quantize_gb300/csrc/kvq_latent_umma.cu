@@ -25,14 +25,18 @@
 //
 // Roles (28 warps, one CTA per SM):
 //  warps 0-15   softmax: thread = token of the tile and a quarter of the rows;
-//  warps 16-23  dequantization, in teams: 128 channels of the tile are one entry of a ring,
-//               and a team takes every second or fourth entry.  A warp's loads in flight are
-//               those of its next entry alone: a wait for some of a warp's loads would wait
-//               for later ones too.  With a tile's first entry a warp stores the rotary parts
-//               of 16 tokens (into tensor memory) and their scales;
+//  warps 16-23  dequantization: 256 channels of the tile are one entry of a ring; with few
+//               rows two teams of four warps take the entries in turn.  A warp's loads in
+//               flight are those of its next entry alone: a wait for some of a warp's loads
+//               would wait for later ones too.  With a tile's first entry a warp stores the
+//               rotary parts of 16 tokens (into tensor memory) and their scales;
 //  warp 24      issues the products (25-27 only fill its warpgroup).
-// The ring's entries are released by the value products, 128 channels at a time, so the
-// next tile is dequantized and its scores begin while these run.  Where ring and tensor
+// The ring's entries are released by the value products, 256 channels at a time, so the
+// next tile is dequantized and its scores begin while these run.  The tensor core takes no
+// product ahead of the one it works on: what the issuing warp does between two (a wait takes
+// 110 cycles, a fence 30, a release 35) is lost, so an entry is sixteen products each way
+// (with eight, measured alone: 76 instead of 49 cycles a product).  Warps that poll a barrier
+// slow it further (104 cycles): of the softmax warps one polls, the others wait for it.  Where ring and tensor
 // memory hold more than a tile (fewer rows, L = 256), its first scores go before them.
 #include <cuda_fp16.h>
 
@@ -47,25 +51,26 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128;
 constexpr int kThreads = 896, kSoftmax = 512;
 constexpr int kDequantWarp = 16, kIssueWarp = 24;
-constexpr int kEntry = kTok * 128 * 2;     // one ring entry: 128 tokens x 128 channels of fp16
-// An entry holds its 64-channel halves one after the other, each as 128-byte rows of tokens
+constexpr int kEntry = kTok * 256 * 2;     // one ring entry: 128 tokens x 256 channels of fp16
+// An entry holds 64 channels after 64, each part as 128-byte rows of tokens
 // with the 16-byte chunks of row t at chunk ^ (t % 8): the 128-byte swizzle of both a
 // K-major (tokens x channels) and an MN-major (channels x tokens) operand.
-constexpr int kHalf = kEntry / 2, kGroup = 1024;  // bytes of a half; of 8 tokens in it
+constexpr int kPart = kEntry / 4, kGroup = 1024;  // bytes of a part; of 8 tokens in it
 constexpr int kLbo = 128;                  // Q, unswizzled core matrices (8 rows x 16 bytes): along channels
 constexpr int kScaleTiles = 4;             // tiles whose scales are kept
 constexpr float kTop = 6.0f, kSlack = 8.0f;
 
 template <int L, int N>
 struct Shape {
-  // Teams of dequantizing warps: with 64 rows the products take longer than the loads, with
-  // fewer the loads are what there is to wait for, and a whole tile is in flight.
-  static constexpr int TEAMS = N == 64 ? 2 : L / 128;
+  // Teams of dequantizing warps take the entries in turn, so that a whole tile's loads are in
+  // flight.  With 64 rows registers do not allow it: there a warp takes every entry, and the
+  // codes of a tile's second one wait in tensor memory (E2M1: in registers).
+  static constexpr int TEAMS = N == 64 ? 1 : L / 256;
   static constexpr int WARPS = 8 / TEAMS, PAGES = TEAMS;  // of a team; of a warp
   // Registers a thread (the launch gives 72).
-  static constexpr int RS = N == 64 ? 72 : TEAMS == 2 ? 64 : 56, RD = N == 64 ? 88 : TEAMS == 2 ? 96 : 112, RI = N == 64 ? 40 : 56;
+  static constexpr int RS = N == 64 ? 72 : 56, RD = N == 64 ? 80 : 112, RI = 56;
   static_assert(512 * RS + 256 * RD + 128 * RI <= 896 * 72, "registers");
-  static constexpr int NB = L / 128;                   // ring entries of a tile
+  static constexpr int NB = L / 256;                   // ring entries of a tile
   static constexpr int C = N / 4;                      // rows of a softmax thread
   static constexpr int QCH = (L + kLatentRope) / 8;    // 16-byte chunks of a query row
   static constexpr int QSBO = QCH * 128;               // Q: 8 rows of a chunk together, chunks 128 bytes apart
@@ -79,13 +84,13 @@ struct Shape {
   static constexpr int F = UP + N * 4;                 // [N] the factor that goes with it; at the end, the output's
   static constexpr int REST = (F + N * 4 + 1023) / 1024 * 1024;
   static constexpr int FIT = (227 * 1024 - 1024 - 1024 - REST) / kEntry;
-  static constexpr int SLOTS = FIT < 6 ? FIT : 6;
+  static constexpr int SLOTS = FIT < 3 ? FIT : 3;
   static constexpr int RING = REST;
   static constexpr int BYTES = RING + SLOTS * kEntry;
   static constexpr size_t dynamic() { return BYTES + 1024; }
   // tensor memory: score buffers (latent, rotary), O^T by 128 channels, rotary operands of two tiles
-  static constexpr int SB = NB * N + 64 + 4 * N <= 512 ? 2 : 1;
-  static constexpr int TO = SB * 2 * N, TR = TO + NB * N;
+  static constexpr int SB = L / 128 * N + 64 + 4 * N <= 512 ? 2 : 1;
+  static constexpr int TO = SB * 2 * N, TR = TO + L / 128 * N, TP = TR + 64;  // TP: parked codes, 64 columns
   // entries of the next tile whose scores go before this tile's value products
   static constexpr int PRE = SB == 2 ? (SLOTS - NB < NB ? SLOTS - NB : NB) : 0;
   static_assert(SLOTS >= NB && TR + 64 <= 512, "fits");
@@ -100,6 +105,11 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd
       : "memory");
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, 1u << 20); }
+// For the issuing warp: a wait whose result, and a number, that the compiler knows to be the
+// same in all lanes.  Operands of a product in uniform registers cost nothing to issue;
+// moved there from others they cost some 80 cycles a product.
+__device__ __forceinline__ bool wait_uniform(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -139,7 +149,7 @@ __device__ __forceinline__ void set_registers() {  // (the launch gives 72)
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// A lane's packed words of one ring entry (a page's 16 tokens x 128 channels): one-byte
+// A lane's packed words of half a ring entry (a page's 16 tokens x 128 channels): one-byte
 // codes in four loads, token (lane >> 3) + 4 r, channels 16 (lane & 7) ..; E2M1 codes in
 // two, token (lane >> 2) + 8 r, channels 32 (lane & 3) .., with the two block scales as
 // bytes 0 and 1.
@@ -203,7 +213,7 @@ __device__ __forceinline__ void store_chunks(const uint4* x, uint8_t* op, int pg
   const int half = second_half<MODE>(lane);
   const int chunk = FOUR ? (4 * (lane & 1)) ^ (2 * half) : (2 * (lane & 3)) ^ half;  // the lane's first
   const int row = FOUR ? lane >> 2 : lane >> 3;                                      // its first token
-  uint8_t* p = op + half * kHalf + 2 * pg * kGroup + row * 128;
+  uint8_t* p = op + half * kPart + 2 * pg * kGroup + row * 128;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (FOUR)  // tokens row + 8 r: the same place in the group
@@ -223,7 +233,7 @@ __device__ __forceinline__ void tmem_st_16x256b(uint32_t t, const uint32_t* r) {
 }
 
 struct Bars {
-  uint64_t q_full, full[6], free[6], rope_full[2], rope_free[2], s_full[2], p_full, p_free;
+  uint64_t q_full, full[3], free[3], rope_full[2], rope_free[2], s_full[2], p_full, p_free;
 };
 
 template <int MODE, int L, int N>
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     if (lane == 0) tile_s = t;
   } else if (warp == 1) {
     if (elect_one()) {
-      for (int i = 0; i < 6; ++i) {
+      for (int i = 0; i < 3; ++i) {
         mbar_init(&bar.full[i], S::WARPS);
         mbar_init(&bar.free[i], 1);
       }
@@ -293,7 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     const int w = warp - kDequantWarp, team = w / S::WARPS, first = w % S::WARPS;
     // rotary parts and scales: of the page whose tokens' lanes of tensor memory the warp reaches
     const int mine = 2 * (warp & 3) + (w >> 2);
-    Words<MODE> words[S::PAGES];  // of pages first, first + WARPS, ..
+    constexpr bool TWO = S::TEAMS == 1 && NB == 2;                      // entries of a tile held at once,
+    constexpr bool PARK = TWO && !kLatentFour<MODE>;                  // the second in tensor memory
+    constexpr int HELD = TWO && !PARK ? 2 : 1;
+    static_assert(!PARK || S::TP + 64 <= 512, "fits");
+    Words<MODE> words[HELD][S::PAGES][2];  // of pages first, first + WARPS, ..
+    const uint32_t parked = tb + S::TP + 32 * (w >> 2) + ((uint32_t)(32 * (warp & 3)) << 16);
     uint32_t rope[16];
     float sc;  // of token lane of page `mine` (lanes 0-15); -1 where it is not there
     // the tile's eight page ids, lane by lane; -1 past the last token
@@ -307,12 +322,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       valid = in ? min(16, most - ((i0 + i) * 8 + pg) * 16) : 0;
       return a.pool + kHeaderBytes + (size_t)(in ? id : 0) * a.block_bytes;
     };
-    auto load = [&](int ids, int i, int j) {
+    auto load = [&](int ids, int i, int j, int held) {
 #pragma unroll
       for (int u = 0; u < S::PAGES; ++u) {
         int valid;
         const uint8_t* page = page_at(ids, i, first + S::WARPS * u, valid);
-        load_words<MODE, L>(page, j, lane, valid, words[u]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) load_words<MODE, L>(page, 2 * j + e, lane, valid, words[held][u][e]);
       }
     };
     // Four lanes have a row: its 32 bytes from 32 (lane % 4) in the columns 8 k + 2 (lane % 4),
@@ -336,9 +352,39 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       if (i < n && valid == 0 && ((i0 + i) * 8 + mine) * 16 < most && lane == 0)
         set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_PAGE_RANGE);
     };
-    int ids = page_ids(0), ahead = page_ids(1);
-    load(ids, 0, team);
-    load_rope(ids, 0);
+    int ahead = page_ids(1);
+    auto load_tile = [&](int ids, int i) {  // the first entry, or both
+      if constexpr (PARK) {
+        load(ids, i, 1, 0);
+        uint32_t r[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = words[0][0][e >> 2].w[e & 3];
+          r[4 * e] = x.x;
+          r[4 * e + 1] = x.y;
+          r[4 * e + 2] = x.z;
+          r[4 * e + 3] = x.w;
+        }
+        tmem_st<32>(parked, r);
+        tmem_wait_st();
+      }
+      load(ids, i, team, 0);
+      if constexpr (HELD == 2) load(ids, i, 1, HELD - 1);
+      load_rope(ids, i);
+    };
+    auto unpark = [&]() {
+      if constexpr (PARK) {
+        uint32_t r[32];
+        tmem_ld<32>(parked, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          asm volatile("" : "+r"(r[4 * e]), "+r"(r[4 * e + 1]), "+r"(r[4 * e + 2]), "+r"(r[4 * e + 3]));
+          words[0][0][e >> 2].w[e & 3] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+        }
+      }
+    };
+    load_tile(page_ids(0), 0);
     int slot = team, round = 0;
     for (int i = 0; i < n; ++i) {
       const int buf = i & 1;
@@ -355,26 +401,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&bar.rope_full[buf]);
 #pragma unroll
       for (int j0 = 0; j0 < NB; j0 += S::TEAMS) {
-        // (one page is converted before the wait where registers allow it)
-        constexpr int EARLY = S::TEAMS == 2 ? 1 : 0;
-        uint4 h[8];
-        if (EARLY) convert<MODE>(words[0], lane, h);
+        const int held = HELD == 2 ? j0 : 0;
+        if (j0 > 0) unpark();
         if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
         if (!__all_sync(kFull, ok)) break;
         uint8_t* op = sm + S::RING + slot * kEntry;
 #pragma unroll
-        for (int u = 0; u < S::PAGES; ++u) {
-          if (u >= EARLY) convert<MODE>(words[u], lane, h);
-          store_chunks<MODE>(h, op, first + S::WARPS * u, lane);
+        for (int u = 0; u < 2 * S::PAGES; ++u) {
+          uint4 h[8];
+          convert<MODE>(words[held][u >> 1][u & 1], lane, h);
+          store_chunks<MODE>(h, op + (u & 1) * 2 * kPart, first + S::WARPS * (u >> 1), lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.full[slot]);
-        if (j0 + S::TEAMS < NB) {
-          load(ids, i, j0 + S::TEAMS + team);
-        } else {
-          load(ahead, i + 1, team);
-          load_rope(ahead, i + 1);
-          ids = ahead;
+        if (j0 + S::TEAMS == NB) {
+          load_tile(ahead, i + 1);
           ahead = page_ids(i + 2);
         }
         slot += S::TEAMS;
@@ -391,23 +432,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       constexpr uint32_t kIdescS = umma_idesc_f16(128, N), kIdescO = umma_idesc_f16(128, N) | (1u << 15) | (1u << 16);
       const uint64_t dq = umma_sdesc(smem_u32(sm + S::Q), kLbo, S::QSBO);
       const uint64_t dk = umma_sdesc(smem_u32(sm + S::RING), 16, kGroup) | kSwizzle128;     // tokens x channels
-      const uint64_t dv = umma_sdesc(smem_u32(sm + S::RING), kHalf, kGroup) | kSwizzle128;  // channels x tokens: the same bytes
+      const uint64_t dv = umma_sdesc(smem_u32(sm + S::RING), kPart, kGroup) | kSwizzle128;  // channels x tokens: the same bytes
       const uint64_t dp = umma_sdesc(smem_u32(sm + S::P), N * 16, 128);        // rows x tokens, MN-major
       // The fence between the warps' stores and the tensor core's reads stands here, after the
       // wait for them: once for all of the warps that have arrived.
+      const uint32_t tm = uniform(tb);
       int kslot = 0, kround = 0, vslot = 0;
-      auto scores = [&](int i, int j) {  // of 128 channels
-        if (ok) ok = wait(&bar.full[kslot], kround & 1);
+      auto scores = [&](int i, int j) {  // of 256 channels
+        if (ok) ok = wait_uniform(&bar.full[kslot], kround & 1);
         if (!ok) return;
         fence_proxy_async_smem();
         tc_fence_after();
+        const uint32_t D = uniform(tm + (S::SB == 2 ? (i & 1) * 2 * N : 0)), more = uniform(j);
+        const uint64_t A = dk + uniform(kslot * (kEntry >> 4)), B = dq + uniform(j * ((32 * kLbo) >> 4));
         if (elect_one()) {
-          const uint32_t D = tb + (S::SB == 2 ? (i & 1) * 2 * N : 0);
-          const uint64_t A = dk + (uint64_t)kslot * (kEntry >> 4), B = dq + (uint64_t)j * ((16 * kLbo) >> 4);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            umma_f16_ss(D, A + (e >> 2) * (kHalf >> 4) + (e & 3) * (32 >> 4), B + e * ((2 * kLbo) >> 4), kIdescS,
-                        (j > 0 || e > 0) ? 1u : 0u);
+          for (int e = 0; e < 16; ++e)
+            umma_f16_ss(D, A + (e >> 2) * (kPart >> 4) + (e & 3) * (32 >> 4), B + e * ((2 * kLbo) >> 4), kIdescS, e > 0 ? 1u : more);
+          if (j == NB - 1) tc_commit(&bar.s_full[S::SB == 2 ? i & 1 : 0]);
         }
         __syncwarp();
         if (++kslot == S::SLOTS) {
@@ -417,52 +459,53 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       };
       auto rotary = [&](int i) {
         const int buf = i & 1, sb = S::SB == 2 ? i & 1 : 0;
-        if (ok) ok = wait(&bar.rope_full[buf], (i >> 1) & 1);
+        if (ok) ok = wait_uniform(&bar.rope_full[buf], (i >> 1) & 1);
         if (!ok) return;
         tc_fence_after();
+        const uint32_t D = uniform(tm + sb * 2 * N + N), A = uniform(tm + S::TR + 32 * buf);
         if (elect_one()) {
-          const uint64_t B = dq + (uint64_t)NB * ((16 * kLbo) >> 4);
+          const uint64_t B = dq + (uint64_t)NB * ((32 * kLbo) >> 4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            umma_f16_ts(tb + sb * 2 * N + N, tb + S::TR + 32 * buf + 8 * e, B + e * ((2 * kLbo) >> 4), kIdescS, e > 0 ? 1u : 0u);
+          for (int e = 0; e < 4; ++e) umma_f16_ts(D, A + 8 * e, B + e * ((2 * kLbo) >> 4), kIdescS, e > 0 ? 1u : 0u);
           tc_commit(&bar.rope_free[buf]);
-          tc_commit(&bar.s_full[sb]);
           mbar_arrive(&bar.s_full[sb]);  // passes on the scales that came with the rotary rows
         }
         __syncwarp();
       };
-      ok = wait(&bar.q_full, 0);
-      for (int j = 0; j < NB; ++j) scores(0, j);
+      ok = wait_uniform(&bar.q_full, 0);
       rotary(0);
+      for (int j = 0; j < NB; ++j) scores(0, j);
       for (int i = 0; i < n && ok; ++i) {
         const bool more = i + 1 < n;
-        if (more) {
+        if (more && S::PRE > 0) {
+          rotary(i + 1);
 #pragma unroll 1
           for (int j = 0; j < S::PRE; ++j) scores(i + 1, j);
-          if (S::PRE == NB) rotary(i + 1);
         }
-        if (ok) ok = wait(&bar.p_full, i & 1);
+        if (ok) ok = wait_uniform(&bar.p_full, i & 1);
         if (!ok) break;
         fence_proxy_async_smem();
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
+          const uint64_t A = dv + uniform(vslot * (kEntry >> 4));
+          const uint32_t after = uniform(i);
+          uint64_t* done = &bar.free[uniform(vslot)];
           if (elect_one()) {
-            const uint64_t A = dv + (uint64_t)vslot * (kEntry >> 4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              umma_f16_ss(tb + S::TO + j * N, A + e * ((2 * kGroup) >> 4), dp + e * ((2 * N * 16) >> 4), kIdescO,
-                          (i > 0 || e > 0) ? 1u : 0u);
-            tc_commit(&bar.free[vslot]);
+            for (int e = 0; e < 16; ++e)  // 128 channels after 128
+              umma_f16_ss(tm + S::TO + (2 * j + (e >> 3)) * N, A + (e >> 3) * (2 * kPart >> 4) + (e & 7) * (2 * kGroup >> 4),
+                          dp + (e & 7) * ((2 * N * 16) >> 4), kIdescO, (e & 7) > 0 ? 1u : after);
+            tc_commit(done);
             if (j == NB - 1) tc_commit(&bar.p_free);
           }
           __syncwarp();
           if (++vslot == S::SLOTS) vslot = 0;
         }
         if (more) {
+          if (S::PRE == 0) rotary(i + 1);
 #pragma unroll 1
           for (int j = S::PRE; j < NB; ++j) scores(i + 1, j);
-          if (S::PRE < NB) rotary(i + 1);
         }
       }
     }
@@ -473,18 +516,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     // Q: chunk c of row r at (r % 8) 16 + c kLbo + (r / 8) QSBO; zero past the tile's rows.
     // Rotary channels in the order of the keys' tensor memory: channels 16 m + 4 k .. + 3 are
     // the m-th eight bytes of step k's 32.
-    constexpr int QN = (N * S::QCH + kSoftmax - 1) / kSoftmax;
-    {
-      uint4 x[QN];  // (all loads in flight at once)
+    constexpr int QN = (N * S::QCH + kSoftmax - 1) / kSoftmax, QF = QN < 3 ? QN : 3;
+#pragma unroll 1
+    for (int u0 = 0; u0 < QN; u0 += QF) {
+      uint4 x[QF];  // (in flight at once)
 #pragma unroll
-      for (int u = 0; u < QN; ++u) {
-        const int it = tid + u * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
+      for (int u = 0; u < QF; ++u) {
+        const int it = tid + (u0 + u) * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
         x[u] = make_uint4(0u, 0u, 0u, 0u);
         if (r < t.count) x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + (row0 + r) * (L + kLatentRope)) + c);
       }
 #pragma unroll
-      for (int u = 0; u < QN; ++u) {
-        const int it = tid + u * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
+      for (int u = 0; u < QF; ++u) {
+        const int it = tid + (u0 + u) * kSoftmax, r = (it & 7) + it / (8 * S::QCH) * 8, c = (it >> 3) % S::QCH;
         uint8_t* row = sm + S::Q + (r & 7) * 16 + (r >> 3) * S::QSBO;
         if (r >= N) continue;
         if (c < L / 8) {
@@ -515,29 +559,34 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     uint32_t fresh = (1u << C) - 1;  // this thread's rows that have met no score yet: their reference is 0
     for (int i = 0; i < n; ++i) {
       const int sb = S::SB == 2 ? i & 1 : 0;
-      if (ok) ok = wait(&bar.s_full[sb], (S::SB == 2 ? i >> 1 : i) & 1);
-      ok = __all_sync(kFull, ok);
+      // Where the scores of tile i come after all value products of tile i - 1, these are done
+      // too: P of the last tile, and O, are free.
+      if (warp == 0 && ok) {
+        ok = wait(&bar.s_full[sb], (S::SB == 2 ? i >> 1 : i) & 1);
+        if (S::PRE == NB && i > 0 && ok) ok = wait(&bar.p_free, (i - 1) & 1);
+      }
+      ok = !softmax_any(!ok);
       tc_fence_after();
       float2 y[C / 2];
       const float sc = sc_s[(i & (kScaleTiles - 1)) * kTok + tok];
       {
-        // (the rotary scores first, then the others over the same registers)
+        // (eight columns of each at a time: registers)
         const float ks = one * (PT ? sc : tensor);
-        uint32_t x[C];
-        tmem_ld<C>(tb + sb * 2 * N + N + col + lanes, x);
-        tmem_wait_ld();
+        constexpr int W = C < 8 ? C : 8;
 #pragma unroll
-        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(x[c]));  // (no use before the wait)
+        for (int c0 = 0; c0 < C; c0 += W) {
+          uint32_t xc[W], xr[W];
+          tmem_ld<W>(tb + sb * 2 * N + col + c0 + lanes, xc);
+          tmem_ld<W>(tb + sb * 2 * N + N + col + c0 + lanes, xr);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < C; c += 2)
-          y[c / 2] = __fmul2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), make_float2(one, one));
-        tmem_ld<C>(tb + sb * 2 * N + col + lanes, x);
-        tmem_wait_ld();
+          for (int c = 0; c < W; ++c) asm volatile("" : "+r"(xc[c]), "+r"(xr[c]));  // (no use before the wait)
 #pragma unroll
-        for (int c = 0; c < C; ++c) asm volatile("" : "+r"(x[c]));
-#pragma unroll
-        for (int c = 0; c < C; c += 2)
-          y[c / 2] = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), make_float2(ks, ks), y[c / 2]);
+          for (int c = 0; c < W; c += 2) {
+            const float2 r = __fmul2_rn(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), make_float2(one, one));
+            y[(c0 + c) / 2] = __ffma2_rn(make_float2(__uint_as_float(xc[c]), __uint_as_float(xc[c + 1])), make_float2(ks, ks), r);
+          }
+        }
       }
       const int tk = (i0 + i) * kTok + tok;
       const bool masked = (i0 + i + 1) * kTok > fewest;
@@ -568,10 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < C; ++c) moves |= ((fresh >> c) & 1u) && (c & 1 ? y[c / 2].y : y[c / 2].x) > -INFINITY;
       }
-      // P of the last tile, and O, are free once its value products are done
-      if (i > 0 && ok) ok = wait(&bar.p_free, (i - 1) & 1);
-      ok = __all_sync(kFull, ok);
-      tc_fence_after();
       if (softmax_any(moves)) {
         // References move: to each row's largest y + ex of the tile, over its 128 tokens.
 #pragma unroll
@@ -596,33 +641,32 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
         }
         softmax_sync();
         fresh = (fresh_s[col >> 5] >> (col & 31)) & ((1u << C) - 1);
-        float2 f[C / 2];
         bool any = false;
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
           const float4 u = *reinterpret_cast<const float4*>(up_s + col + c), g = *reinterpret_cast<const float4*>(f_s + col + c);
           y[c / 2] = __fadd2_rn(y[c / 2], make_float2(-u.x, -u.y));
           y[c / 2 + 1] = __fadd2_rn(y[c / 2 + 1], make_float2(-u.z, -u.w));
-          f[c / 2] = make_float2(g.x, g.y);
-          f[c / 2 + 1] = make_float2(g.z, g.w);
+          l[c / 2] = __fmul2_rn(l[c / 2], make_float2(g.x, g.y));
+          l[c / 2 + 1] = __fmul2_rn(l[c / 2 + 1], make_float2(g.z, g.w));
           any |= g.x != 1.0f || g.y != 1.0f || g.z != 1.0f || g.w != 1.0f;
         }
         if (i > 0 && any) {  // (the same for all tokens)
-#pragma unroll
-          for (int c = 0; c < C / 2; ++c) l[c] = __fmul2_rn(l[c], f[c]);
 #pragma unroll 1
-          for (int j = 0; j < NB; ++j) {
-            uint32_t v[C];
-            tmem_ld<C>(tb + S::TO + j * N + col + lanes, v);
-            tmem_wait_ld();
+          for (int j = 0; j < L / 128; ++j) {
 #pragma unroll
-            for (int c = 0; c < C; c += 2) {
-              asm volatile("" : "+r"(v[c]), "+r"(v[c + 1]));
-              const float2 o = __fmul2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f[c / 2]);
-              v[c] = __float_as_uint(o.x);
-              v[c + 1] = __float_as_uint(o.y);
+            for (int c0 = 0; c0 < C; c0 += 4) {
+              const float4 g = *reinterpret_cast<const float4*>(f_s + col + c0);
+              uint32_t v[4];
+              tmem_ld<4>(tb + S::TO + j * N + col + c0 + lanes, v);
+              tmem_wait_ld();
+              asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]));
+              v[0] = __float_as_uint(__uint_as_float(v[0]) * g.x);
+              v[1] = __float_as_uint(__uint_as_float(v[1]) * g.y);
+              v[2] = __float_as_uint(__uint_as_float(v[2]) * g.z);
+              v[3] = __float_as_uint(__uint_as_float(v[3]) * g.w);
+              tmem_st<4>(tb + S::TO + j * N + col + c0 + lanes, v);
             }
-            tmem_st<C>(tb + S::TO + j * N + col + lanes, v);
           }
           tmem_wait_st();
         }
@@ -687,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
       constexpr int OROW = L * 2 + 16;
       uint8_t* stage = sm + S::RING;
 #pragma unroll 1
-      for (int j = 0; j < NB; ++j) {
+      for (int j = 0; j < L / 128; ++j) {
         uint32_t v[C];
         if (n > 0) {
           tmem_ld<C>(tb + S::TO + j * N + col + lanes, v);
