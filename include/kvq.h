@@ -477,6 +477,8 @@ kvq_status kvq_latent_read(const kvq_latent* cache, const int32_t* slot_mapping,
  *  lse          device fp32 [total_q][num_q_heads]: log(sum exp(s_t)), or NULL
  * A query that sees no token: out 0, lse -infinity.  Rows of no sequence are neither
  * read nor written.  A page id outside the pool drops its tokens (KVQ_DEVERR_PAGE_RANGE).
+ * A plan's num_splits is the most parts that a sequence's token range may be split into
+ * (for outputs of io_dtype; how many it is goes by the lengths, on the device).
  * The workspace of the plan (0 bytes where no range is split) belongs to one call at a
  * time; for batches of several sizes it is the largest of their plans.  total_q *
  * num_q_heads < 2^31.

@@ -65,6 +65,11 @@ __device__ __forceinline__ void latent_codes16(const uint32_t* w, uint32_t sb, u
 // head (Hkv = 1, G = Hq); expanded, each has its own (Hkv = Hq, G = 1).
 struct LatentArgs : ChunkArgs {
   int causal;
+  // The tcgen05 kernel's CTAs where row tiles are split: CTA c leaves its rows' partials at
+  // ws_o [c][rows][L] and ws_ml [c][rows][2], and (first CTA, parts) of row tile i is at map[i].
+  // 0: a CTA takes a whole row tile.
+  int ctas;
+  int2* map;
   float* lse;  // [total_q][Hq] or null
   Span lse_span;
   // expanded
@@ -101,8 +106,89 @@ __device__ __forceinline__ long long latent_row(const LatentArgs& a, const RowTi
   return (long long)(t.q0 + rr / a.G) * a.Hq + kvh * a.G + rr % a.G;
 }
 
+// A CTA's part of a row tile.
+struct LatentPart {
+  RowTile t;
+  int tile;         // the row tile's number, as find_tile counts
+  int part, parts;  // of its token range
+  int first;        // the CTA of its part 0
+};
+// CTA `cta` of a.ctas: each sequence's range is cut into parts of at most T tiles of 128 tokens,
+// with the smallest T for which the batch has no more parts than CTAs.  (The host has bounds
+// of the lengths only; equal counts of parts, for any lengths, left CTAs with a few tiles
+// beside others with many.)  One warp; seqs: shared memory for (row tiles, token tiles) of
+// kLatentSeqs sequences.
+constexpr int kLatentSeqs = 512;
+__device__ __forceinline__ LatentPart latent_part(const LatentArgs& a, int cta, int rows, bool flag, int2* seqs) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int lim = (int)min((long long)a.max_seq_len, (long long)a.max_pages * 16);
+  LatentPart p{{-1, 0, 0, 0, 0, 0, 0}, 0, 0, 1, 0};
+  int most = 1;
+  for (int b = lane; b < a.B; b += 32) {
+    const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1), n = __ldg(a.seq_lens + b);
+    int2 s = make_int2(0, 1);
+    if (q0 < 0 || q1 < q0 || q1 > a.total_q || q1 - q0 > a.max_q_len) {
+      if (flag) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_QUERY_RANGE);
+    } else if (q1 > q0) {
+      if (flag && (n > lim || n < 0)) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_SEQ_LEN);
+      s.x = (int)(((long long)(q1 - q0) * a.G + rows - 1) / rows);
+      s.y = max(1, (max(0, min(n, lim)) + 127) / 128);
+      most = max(most, s.y);
+    }
+    seqs[b] = s;
+  }
+  __syncwarp();
+  const int cap = a.ctas + 1;
+  auto parts = [&](int2 s, int T) { return min(cap, (s.y + T - 1) / T); };
+  int lo = 1, hi = __reduce_max_sync(kAll, most);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int sum = 0;
+    for (int b = lane; b < a.B; b += 32) sum += seqs[b].x * parts(seqs[b], mid);
+    if (__reduce_add_sync(kAll, sum) <= a.ctas) hi = mid;
+    else lo = mid + 1;
+  }
+  int before = 0, tiles_before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int2 s = b < a.B ? seqs[b] : make_int2(0, 1);
+    const int n = parts(s, lo);
+    int upto = s.x * n, tiles = s.x;  // inclusive prefix sums over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, upto, o), y = __shfl_up_sync(kAll, tiles, o);
+      if (lane >= o) {
+        upto += x;
+        tiles += y;
+      }
+    }
+    const uint32_t who = __ballot_sync(kAll, cta >= before + upto - s.x * n && cta < before + upto);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      const int R = __shfl_sync(kAll, s.x, src), start = before + __shfl_sync(kAll, upto, src);
+      p.parts = __shfl_sync(kAll, n, src);
+      const int at = cta - (start - R * p.parts), k = at / p.parts;  // row tiles from the chunk's last rows
+      p.part = at % p.parts;
+      p.first = cta - p.part;
+      p.tile = tiles_before + __shfl_sync(kAll, tiles, src) - R + k;
+      p.t.seq = b0 + src;
+      p.t.q0 = __ldg(a.cu_q + p.t.seq);
+      p.t.m = __ldg(a.cu_q + p.t.seq + 1) - p.t.q0;
+      p.t.n = max(0, min(__ldg(a.seq_lens + p.t.seq), lim));
+      p.t.r0 = (R - 1 - k) * rows;
+      p.t.count = (int)min((long long)rows, (long long)p.t.m * a.G - p.t.r0);
+      break;
+    }
+    before += __shfl_sync(kAll, upto, 31);
+    tiles_before += __shfl_sync(kAll, tiles, 31);
+  }
+  return p;
+}
+
 struct LatentPlan {
-  int num_splits = 1;
+  int num_splits = 1;  // at most so many parts of a row tile
+  int ctas = 0;        // of the tcgen05 kernel, where it splits
   size_t workspace_bytes = 0;
 };
 // rows: query rows of a CTA of the tcgen05 kernel, from the largest chunk

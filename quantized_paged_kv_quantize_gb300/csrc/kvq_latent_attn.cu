@@ -321,7 +321,7 @@ cudaError_t launch_plain_mode(int mode, const LatentArgs& a, cudaStream_t s) {
 // out = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s.  A part without tokens has m = -inf
 // and is not read.  Bound by the partials' way through memory, eight loads of 16 bytes
 // in flight a lane.
-constexpr int kMaxParts = 128;
+constexpr int kMaxParts = 512;
 template <int L>
 __global__ void __launch_bounds__(kThreads) latent_combine_kernel(const __grid_constant__ LatentArgs a, int rows) {
   constexpr int N4 = L / 128;  // 16-byte groups of a lane
@@ -335,17 +335,26 @@ __global__ void __launch_bounds__(kThreads) latent_combine_kernel(const __grid_c
   }
   __syncthreads();
   const RowTile t = tile_s;
-  if (t.seq < 0) return;
   const int r = blockIdx.y * (kThreads / 32) + warp;
-  if (r >= t.count) return;
+  if (t.seq < 0 || r >= t.count) return;
   const long long row = latent_row(a, t, 0, t.r0 + r);
-  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
+  // part s of this row is partial first + s step
+  long long first = row * a.num_splits;
+  int parts = a.num_splits, step = 1;
+  if (a.ctas) {
+    const int2 m = a.map[blockIdx.x];
+    if (m.y == 1) return;  // (written whole)
+    first = (long long)m.x * rows + r;
+    parts = m.y;
+    step = rows;
+  }
+  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + first;
   float M = -INFINITY;
-  for (int s = lane; s < a.num_splits; s += 32) M = fmaxf(M, ml[s].x);
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, ml[(long long)s * step].x);
   M = warp_max_xor(M, 1, 16);
   float sum = 0.0f;
-  for (int s = lane; s < a.num_splits; s += 32) {
-    const float2 v = ml[s];
+  for (int s = lane; s < parts; s += 32) {
+    const float2 v = ml[(long long)s * step];
     const float w = v.x == -INFINITY ? 0.0f : exp2f(v.x - M);  // (a NaN stays)
     w_s[warp][s] = w;
     sum += w * v.y;
@@ -357,13 +366,13 @@ __global__ void __launch_bounds__(kThreads) latent_combine_kernel(const __grid_c
 #pragma unroll
   for (int c = 0; c < N4; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   constexpr int U = 8 / N4;
-  for (int s0 = 0; s0 < a.num_splits; s0 += U) {
+  for (int s0 = 0; s0 < parts; s0 += U) {
     float4 x[U][N4];
     float w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      w[u] = s0 + u < a.num_splits ? w_s[warp][s0 + u] : 0.0f;
-      const float4* src = reinterpret_cast<const float4*>(a.ws_o + (row * a.num_splits + s0 + u) * L) + lane;
+      w[u] = s0 + u < parts ? w_s[warp][s0 + u] : 0.0f;
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o + (first + (long long)(s0 + u) * step) * L) + lane;
 #pragma unroll
       for (int c = 0; c < N4; ++c) x[u][c] = w[u] != 0.0f ? src[32 * c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
@@ -410,19 +419,18 @@ cudaError_t launch_combine(const kvq_latent* c, const LatentArgs& a, int rows, c
 
 bool on_umma(const kvq_latent* c, bool out_f32) { return c->cfg.io_dtype == KVQ_F16 && !out_f32; }
 
-// Parts of a row tile's token range.  The lengths are on the device: every tile is taken to
-// see max_seq_len tokens.  Both kernels keep one CTA on an SM; a plan of s parts is
+// Parts of a row tile's token range in the fp32 kernel.  The lengths are on the device: every
+// tile is taken to see max_seq_len tokens.  One CTA on an SM; a plan of s parts is
 // estimated at ceil(units s / SMs) waves x (token tiles / s + the cost of a CTA's start
 // and end, in tiles) plus the merge of s partials.
-int latent_parts(bool umma, int Hq, int total_q, int num_seqs, int max_q_len, int max_seq_len) {
-  const int rows = umma ? latent_umma_rows(max_q_len, Hq) : kRows, kt = umma ? 128 : kTok;
+int plain_parts(int Hq, int total_q, int num_seqs, int max_q_len, int max_seq_len) {
   const long long sms = num_sms(), cost_cta = 4;
-  const long long tiles = ((long long)max_seq_len + kt - 1) / kt;
-  const long long per_seq = ((long long)max_q_len * Hq + rows - 1) / rows;
-  const long long units = std::min(((long long)total_q * Hq + rows - 1) / rows + num_seqs / 2, per_seq * num_seqs);
+  const long long tiles = ((long long)max_seq_len + kTok - 1) / kTok;
+  const long long per_seq = ((long long)max_q_len * Hq + kRows - 1) / kRows;
+  const long long units = std::min(((long long)total_q * Hq + kRows - 1) / kRows + num_seqs / 2, per_seq * num_seqs);
   long long best = -1;
   int parts = 1;
-  for (long long s = 1; s <= kMaxParts && s <= std::max(1ll, tiles); ++s) {
+  for (long long s = 1; s <= 128 && s <= std::max(1ll, tiles); ++s) {
     const long long cost = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + cost_cta) * 8 + s;
     if (best < 0 || cost < best) {
       best = cost;
@@ -430,6 +438,16 @@ int latent_parts(bool umma, int Hq, int total_q, int num_seqs, int max_q_len, in
     }
   }
   return parts;
+}
+// CTAs of the tcgen05 kernel: whole waves, for parts of the ranges, unless there are several
+// waves of row tiles or nothing to split.
+constexpr int kSplitWaves = 3;
+int umma_ctas(int Hq, int total_q, int num_seqs, int max_q_len, int max_seq_len) {
+  const int rows = latent_umma_rows(max_q_len, Hq);
+  const long long per_seq = ((long long)max_q_len * Hq + rows - 1) / rows, sms = num_sms();
+  const long long tiles = std::min(chunk_tile_bound(total_q, num_seqs, Hq, rows), per_seq * num_seqs);
+  if (max_seq_len <= 128 || tiles > kSplitWaves * sms || num_seqs > kLatentSeqs) return 0;
+  return (int)std::min((tiles + sms - 1) / sms * sms, (long long)kMaxParts);
 }
 
 void spans(LatentArgs& a, int width) {
@@ -448,28 +466,40 @@ LatentPlan plan_latent(const kvq_latent* c, int total_q, int num_seqs, int num_q
                        int out_dtype) {
   LatentPlan p;
   if (total_q == 0 || num_seqs == 0 || max_q_len == 0) return p;
-  auto parts = [&](int out) {
-    return latent_parts(on_umma(c, out == KVQ_F32), num_q_heads, total_q, num_seqs, max_q_len, max_seq_len);
-  };
-  p.num_splits = parts(out_dtype);
-  const int most = std::max(parts(KVQ_F16), parts(KVQ_F32));
-  if (most > 1) p.workspace_bytes = (size_t)total_q * num_q_heads * most * (c->cfg.latent_dim + 2) * sizeof(float);
+  const int plain = plain_parts(num_q_heads, total_q, num_seqs, max_q_len, max_seq_len);
+  const size_t row = (c->cfg.latent_dim + 2) * sizeof(float);
+  if (plain > 1) p.workspace_bytes = (size_t)total_q * num_q_heads * plain * row;
+  p.num_splits = plain;
+  if (c->cfg.io_dtype == KVQ_F16) {
+    const int rows = latent_umma_rows(max_q_len, num_q_heads);
+    const int ctas = umma_ctas(num_q_heads, total_q, num_seqs, max_q_len, max_seq_len);
+    const size_t tiles = (size_t)chunk_tile_bound(total_q, num_seqs, num_q_heads, rows);
+    if (ctas) p.workspace_bytes = std::max(p.workspace_bytes, (size_t)ctas * rows * row + tiles * sizeof(int2));
+    if (on_umma(c, out_dtype == KVQ_F32)) {
+      p.ctas = ctas;
+      p.num_splits = ctas ? std::min(ctas, (max_seq_len + 127) / 128) : 1;
+    }
+  }
   return p;
 }
 
 cudaError_t launch_latent_attention(const kvq_latent* c, const LatentPlan& p, LatentArgs& a, cudaStream_t s) {
   const int L = c->cfg.latent_dim, mode = c->cfg.mode;
-  a.num_splits = p.num_splits;
-  a.ws_ml = p.num_splits > 1 ? a.ws_o + (size_t)a.total_q * a.Hq * p.num_splits * L : nullptr;
-  spans(a, L);
   const bool umma = on_umma(c, a.out_f32);
+  const int rows = umma ? latent_umma_rows(a.max_q_len, a.Hq) : kRows;
+  a.num_splits = umma ? 1 : p.num_splits;
+  a.ctas = p.ctas;
+  const size_t partials = umma ? (size_t)p.ctas * rows : (size_t)a.total_q * a.Hq * a.num_splits;
+  a.ws_ml = a.ws_o + partials * L;  // (not used where nothing is split)
+  a.map = reinterpret_cast<int2*>(a.ws_ml + 2 * partials);
+  spans(a, L);
   cudaError_t e;
   if (umma) e = launch_latent_umma(c, a, s);
   else if (c->cfg.io_dtype == KVQ_F32)
     e = L == 512 ? launch_plain_mode<float, 512>(mode, a, s) : launch_plain_mode<float, 256>(mode, a, s);
   else e = L == 512 ? launch_plain_mode<__half, 512>(mode, a, s) : launch_plain_mode<__half, 256>(mode, a, s);
-  if (e != cudaSuccess || a.num_splits == 1) return e;
-  return launch_combine(c, a, umma ? latent_umma_rows(a.max_q_len, a.Hq) : kRows, s);
+  if (e != cudaSuccess || (a.num_splits == 1 && !a.ctas)) return e;
+  return launch_combine(c, a, rows, s);
 }
 
 cudaError_t launch_latent_prompt(const kvq_latent* c, LatentArgs& a, cudaStream_t s) {

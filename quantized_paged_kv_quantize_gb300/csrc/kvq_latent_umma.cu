@@ -84,7 +84,7 @@ struct Shape {
   static constexpr int F = UP + N * 4;                 // [N] the factor that goes with it; at the end, the output's
   static constexpr int REST = (F + N * 4 + 1023) / 1024 * 1024;
   static constexpr int FIT = (227 * 1024 - 1024 - 1024 - REST) / kEntry;
-  static constexpr int SLOTS = FIT < 3 ? FIT : 3;
+  static constexpr int SLOTS = 2;
   static constexpr int RING = REST;
   static constexpr int BYTES = RING + SLOTS * kEntry;
   static constexpr size_t dynamic() { return BYTES + 1024; }
@@ -93,7 +93,8 @@ struct Shape {
   static constexpr int TO = SB * 2 * N, TR = TO + L / 128 * N, TP = TR + 64;  // TP: parked codes, 64 columns
   // entries of the next tile whose scores go before this tile's value products
   static constexpr int PRE = SB == 2 ? (SLOTS - NB < NB ? SLOTS - NB : NB) : 0;
-  static_assert(SLOTS >= NB && TR + 64 <= 512, "fits");
+  static_assert(FIT >= SLOTS && SLOTS >= NB && TR + 64 <= 512, "fits");
+  static_assert(kLatentSeqs * 8 <= SLOTS * kEntry, "fits");
 };
 
 constexpr uint64_t kSwizzle128 = 2ull << 61;  // of a shared-memory matrix descriptor
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Bars bar;
   __shared__ uint32_t tmem_s;
-  __shared__ RowTile tile_s;
+  __shared__ LatentPart part_s;
   __shared__ int failed_s;
   __shared__ uint32_t fresh_s[2];  // rows 0-31, 32-63: no score met yet
   float* sc_s = reinterpret_cast<float*>(sm + S::SC);
@@ -256,10 +257,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   float* up_s = reinterpret_cast<float*>(sm + S::UP);
   float* f_s = reinterpret_cast<float*>(sm + S::F);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, split = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
-    const RowTile t = find_tile(a, blockIdx.x, N, blockIdx.x == 0 && split == 0);
-    if (lane == 0) tile_s = t;
+    LatentPart p{{-1, 0, 0, 0, 0, 0, 0}, 0, 0, 1, 0};
+    if (a.ctas) p = latent_part(a, blockIdx.x, N, blockIdx.x == 0, reinterpret_cast<int2*>(sm + S::RING));
+    else p.t = find_tile(a, blockIdx.x, N, blockIdx.x == 0);
+    if (lane == 0) {
+      part_s = p;
+      if (a.ctas && p.t.seq >= 0 && p.part == 0) st_chk(a.map + p.tile, make_int2(p.first, p.parts), a.ws_span, a.pool);
+    }
   } else if (warp == 1) {
     if (elect_one()) {
       for (int i = 0; i < 3; ++i) {
@@ -285,15 +291,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const RowTile t = tile_s;
+  const RowTile t = part_s.t;
+  const int part = part_s.part, parts = part_s.parts;
   if (t.seq < 0) {  // no such tile
     if (warp == kIssueWarp) tmem_dealloc(tmem_s, 512);
     return;
   }
   const int fewest = latent_sees(a, t, t.r0), most = latent_sees(a, t, t.r0 + t.count - 1);
   const int tiles = (most + kTok - 1) / kTok;
-  const int i0 = (int)((long long)tiles * split / a.num_splits);
-  const int n = (int)((long long)tiles * (split + 1) / a.num_splits) - i0;  // this CTA's tiles
+  const int i0 = (int)((long long)tiles * part / parts);
+  const int n = (int)((long long)tiles * (part + 1) / parts) - i0;  // this CTA's tiles
   const uint32_t tb = tmem_s;
   bool ok = true;
 
@@ -713,23 +720,32 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
     if (failed && tid == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_TIMEOUT);
     if (tid < N) {
       const float sum = red_s[tid] + red_s[N + tid] + red_s[2 * N + tid] + red_s[3 * N + tid];
-      f_s[tid] = sum == 0.0f ? 0.0f : a.num_splits > 1 ? tensor : tensor / sum;  // (a NaN score makes its row NaN)
+      f_s[tid] = sum == 0.0f ? 0.0f : parts > 1 ? tensor : tensor / sum;  // (a NaN score makes its row NaN)
       if (tid < t.count && !failed) {
         const long long row = row0 + tid;
-        if (a.num_splits > 1)
-          st_chk(reinterpret_cast<float2*>(a.ws_ml) + row * a.num_splits + split, make_float2(sum == 0.0f ? -INFINITY : m_s[tid], sum),
+        if (parts > 1)
+          st_chk(reinterpret_cast<float2*>(a.ws_ml) + (long long)blockIdx.x * N + tid, make_float2(sum == 0.0f ? -INFINITY : m_s[tid], sum),
                  a.ws_span, a.pool);
         else if (a.lse)
           st_chk(a.lse + row, sum == 0.0f ? -INFINITY : (m_s[tid] + log2f(sum)) * (1.0f / kLog2e), a.lse_span, a.pool);
       }
     }
     softmax_sync();
-    if (!failed && (n > 0 || a.num_splits == 1)) {
+    if (!failed && (n > 0 || parts == 1)) {
       // O^T: a lane has a channel.  Partials leave as 32 neighbouring floats of a row to a
       // warp's store; fp16 rows go through shared memory (the ring is free) and leave 16
       // bytes a lane.
       constexpr int OROW = L * 2 + 16;
       uint8_t* stage = sm + S::RING;
+      float f[C];
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        const float4 g = *reinterpret_cast<const float4*>(f_s + col + c);
+        f[c] = g.x;
+        f[c + 1] = g.y;
+        f[c + 2] = g.z;
+        f[c + 3] = g.w;
+      }
 #pragma unroll 1
       for (int j = 0; j < L / 128; ++j) {
         uint32_t v[C];
@@ -740,20 +756,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_umma_kernel(const __grid_c
           for (int c = 0; c < C; ++c) asm volatile("" : "+r"(v[c]));
         }
         const int ch = 128 * j + tok;
-        float* po = a.ws_o + ((row0 + col) * a.num_splits + split) * L + ch;
+        float* po = a.ws_o + ((long long)blockIdx.x * N + col) * L + ch;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const float f = f_s[col + c];
-          const float x = n > 0 && f != 0.0f ? __uint_as_float(v[c]) * f : 0.0f;
-          if (a.num_splits == 1) {
+          const float x = n > 0 && f[c] != 0.0f ? __uint_as_float(v[c]) * f[c] : 0.0f;
+          if (parts == 1) {
             *reinterpret_cast<__half*>(stage + (col + c) * OROW + 2 * ch) = __float2half_rn(x);
           } else if (col + c < t.count) {
-            st_chk(po, x, a.ws_span, a.pool);
-            po += (long long)a.num_splits * L;
+            st_chk(po + c * L, x, a.ws_span, a.pool);
           }
         }
       }
-      if (a.num_splits == 1) {
+      if (parts == 1) {
         softmax_sync();
         __half* out = static_cast<__half*>(a.out) + row0 * L;
 #pragma unroll 4
@@ -774,7 +788,7 @@ cudaError_t launch(const LatentArgs& a, cudaStream_t s) {
   constexpr size_t smem = Shape<L, N>::dynamic();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)chunk_tile_bound(a.total_q, a.B, a.G, N), a.num_splits), kThreads, smem, s>>>(a);
+  kern<<<(unsigned)(a.ctas ? a.ctas : chunk_tile_bound(a.total_q, a.B, a.G, N)), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <int L, int N>
