@@ -9,16 +9,19 @@
 // so far less kTop, moved (O and l with it, exactly) only when a score passes it by more
 // than 2^(kTop + kSlack).
 //
-// Roles (16 warps, one CTA per SM; registers are shared out between the warpgroups):
-//  warps 0-3, 4-7  softmax of two blocks of 128 rows, thread = row; the tensor cores run one
-//                  block's products during the other's softmax;
-//  warps 8-11      copy queries, keys, rotary parts and values into shared memory, 16 bytes a
-//                  copy, rows past the sequence's end as zeros;
-//  warp 12         issues the products (13-15 only fill its warpgroup).
+// Roles (24 warps, one CTA per SM; registers are shared out between the warpgroups):
+//  warps 0-7, 8-15  softmax of two blocks of 128 rows; the tensor cores run one block's
+//                   products during the other's softmax.  Two threads share a row, 64 tokens
+//                   of a tile each (with one thread a row, eight warps, 2048 queries of 128
+//                   heads over 8192 keys took 1.13 ms, as long as their softmax);
+//  warps 16-19      copy queries, keys, rotary parts and values into shared memory, 16 bytes a
+//                   copy, rows past the sequence's end as zeros;
+//  warp 20          issues the products (21-23 only fill its warpgroup).
 // Both blocks use the same keys and values.  These go through a ring of eight units of 16 KB
 // (128 tokens x 64 channels in the 128-byte swizzle): a tile is three units of keys and two
 // of values, so that the copies run 0.6 tiles ahead beside the 96 KB of queries.
-// Tensor memory: S_0 S_1 O_0 O_1, 128 columns each; P goes over the first half of its S.
+// Tensor memory: S_0 S_1 O_0 O_1, 128 columns each; P of 64 tokens goes over the first 32 of
+// their scores' 64 columns.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -30,10 +33,10 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128, kRows = 256;
-constexpr int kThreads = 512;
-constexpr int kCopyWarp = 8, kIssueWarp = 12;
-// Registers a thread (the launch gives 128): 256 x 184 + 128 x 80 + 128 x 56 <= 512 x 128.
-constexpr int kRegsSoftmax = 184, kRegsCopy = 80, kRegsIssue = 56;
+constexpr int kThreads = 768;
+constexpr int kCopyWarp = 16, kIssueWarp = 20;
+// Registers a thread (the launch gives 80): 512 x 88 + 128 x 72 + 128 x 56 <= 768 x 80.
+constexpr int kRegsSoftmax = 88, kRegsCopy = 72, kRegsIssue = 56;
 constexpr int kUnit = 128 * 128;       // 128 rows of 64 channels
 constexpr int kUnits = 8, kKeyUnits = 3, kTileUnits = 5;
 constexpr int kStageRow = 256 + 16;    // an output row in shared memory; the pad spreads the banks
@@ -74,12 +77,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void load64(uint32_t t, uint32_t* x) {  // 64 columns of this thread's lane
+__device__ __forceinline__ void load32(uint32_t t, uint32_t* x) {  // 32 columns of this thread's lane
   tmem_ld<32>(t, x);
-  tmem_ld<32>(t + 32, x + 32);
   tmem_wait_ld();
 #pragma unroll
-  for (int e = 0; e < 64; ++e) asm volatile("" : "+r"(x[e]));  // (no use before the wait)
+  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(x[e]));  // (no use before the wait)
 }
 __device__ __forceinline__ float2 get(const uint32_t* r, int i) {  // registers i, i + 1
   return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
@@ -88,7 +90,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
   return a;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // warps 0-7
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }  // warps 0-15
+// The two warps that share rows (one of eight pairs): whether x holds in either.
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(2 + pair)
+      : "memory");
+  return r != 0;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid_constant__ LatentArgs a) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -97,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
   __shared__ uint32_t tmem_s;
   __shared__ RowTile tile_s;
   __shared__ int failed_s;
+  __shared__ float red_s[kRows];  // what a row's two threads exchange
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.x % a.Hq, index = blockIdx.x / a.Hq;
   if (warp == 0) {
     const RowTile t = latent_tile<true>(a, index, kRows, index == 0 && head == 0);
@@ -109,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bar.s_full[i], 1);
-        mbar_init(&bar.p_full[i], 4);
+        mbar_init(&bar.p_full[i], 8);
         mbar_init(&bar.o_full[i], 1);
       }
       mbar_init(&bar.q_full, 128);
@@ -195,50 +208,67 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
       ok = wait_uniform(&bar.q_full, 0);
       fence_proxy_async_smem();
       // O += P V of a block's last tile, then S of its next (over that P), the blocks in turn.
+      // The tensor core takes no product ahead of the one it works on, so the waits stand
+      // together, before all products of a step, and a tile's units are waited for once.
       // The fences between the copies and the tensor core's reads stand after the waits.
+      int keys = 0, values = 0;  // tiles whose units have been waited for
       for (int i = 0; i <= n && ok; ++i) {
 #pragma unroll 1
         for (int b = 0; b <= last && ok; ++b) {
           const int nb = b ? n1 : n0;
           const uint32_t s = uniform(tm + 128 * b);
           if (i > 0 && i <= nb) {
-            ok = wait_uniform(&bar.p_full[b], (i - 1) & 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int unit = kTileUnits * (i - 1) + kKeyUnits + h, slot = unit & (kUnits - 1);
-              if (ok) ok = wait_uniform(&bar.full[slot], (unit / kUnits) & 1);
-              if (!ok) break;
+            const int unit = kTileUnits * (i - 1) + kKeyUnits, s0 = unit & (kUnits - 1), s1 = (unit + 1) & (kUnits - 1);
+            if (values < i) {
+              ok = wait_uniform(&bar.full[s0], (unit / kUnits) & 1) && wait_uniform(&bar.full[s1], ((unit + 1) / kUnits) & 1);
+              values = i;
               fence_proxy_async_smem();
-              tc_fence_after();
-              const uint64_t B = dr + uniform(slot * (kUnit >> 4));
-              const uint32_t after = uniform(i - 1);
-              if (elect_one()) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) umma_f16_ts(s + 256 + 64 * h, s + 8 * e, B + e * (2048 >> 4), kIdescPV, e > 0 ? 1u : after);
-                if (b == last) tc_commit(&bar.free[slot]);
-                if (h == 1 && i == nb) tc_commit(&bar.o_full[b]);
-              }
-              __syncwarp();
             }
+            if (ok) ok = wait_uniform(&bar.p_full[b], (i - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t B0 = dr + uniform(s0 * (kUnit >> 4)), B1 = dr + uniform(s1 * (kUnit >> 4));
+            const uint32_t after = uniform(i - 1), free = uniform(b == last), end = uniform(i == nb);
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                umma_f16_ts(s + 256 + 64 * (e >> 3), s + 64 * ((e >> 2) & 1) + 8 * (e & 3), (e < 8 ? B0 : B1) + (e & 7) * (2048 >> 4), kIdescPV,
+                            (e & 7) > 0 ? 1u : after);
+              if (free) {
+                tc_commit(&bar.free[s0]);
+                tc_commit(&bar.free[s1]);
+              }
+              if (end) tc_commit(&bar.o_full[b]);
+            }
+            __syncwarp();
           }
-          if (i < nb && ok) {
+          if (i < nb) {
+            const int unit = kTileUnits * i;
+            if (keys <= i) {
 #pragma unroll
-            for (int p = 0; p < kKeyUnits; ++p) {
-              const int unit = kTileUnits * i + p, slot = unit & (kUnits - 1);
-              if (ok) ok = wait_uniform(&bar.full[slot], (unit / kUnits) & 1);
+              for (int p = 0; p < kKeyUnits; ++p)
+                if (ok) ok = wait_uniform(&bar.full[(unit + p) & (kUnits - 1)], ((unit + p) / kUnits) & 1);
               if (!ok) break;
+              keys = i + 1;
               fence_proxy_async_smem();
               tc_fence_after();
-              const uint64_t A = dq + uniform((kKeyUnits * b + p) * (kUnit >> 4)), B = dr + uniform(slot * (kUnit >> 4));
-              if (elect_one()) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  umma_f16_ss(s, A + e * (32 >> 4), B + e * (32 >> 4), kIdescQK, (p > 0 || e > 0) ? 1u : 0u);
-                if (b == last) tc_commit(&bar.free[slot]);
-                if (p == kKeyUnits - 1) tc_commit(&bar.s_full[b]);
-              }
-              __syncwarp();
             }
+            const uint64_t A = dq + uniform(kKeyUnits * b * (kUnit >> 4));
+            uint64_t B[kKeyUnits];
+#pragma unroll
+            for (int p = 0; p < kKeyUnits; ++p) B[p] = dr + uniform(((unit + p) & (kUnits - 1)) * (kUnit >> 4));
+            const uint32_t free = uniform(b == last);
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 0; e < 4 * kKeyUnits; ++e)
+                umma_f16_ss(s, A + (e >> 2) * (kUnit >> 4) + (e & 3) * (32 >> 4), B[e >> 2] + (e & 3) * (32 >> 4), kIdescQK, e > 0 ? 1u : 0u);
+              tc_commit(&bar.s_full[b]);
+              if (free) {
+#pragma unroll
+                for (int p = 0; p < kKeyUnits; ++p) tc_commit(&bar.free[(unit + p) & (kUnits - 1)]);
+              }
+            }
+            __syncwarp();
           }
         }
       }
@@ -246,42 +276,45 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int blk = warp >> 2, nb = blk ? n1 : n0;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const bool real = tid < t.count;
-    const int sees = real ? latent_sees(a, t, t.r0 + tid) : 0;
+    const int blk = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, pair = 4 * blk + quad, nb = blk ? n1 : n0;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const int row = 128 * blk + 32 * quad + lane;
+    const bool real = row < t.count;
+    const int sees = real ? latent_sees(a, t, t.r0 + row) : 0;
     const int fewest = latent_sees(a, t, t.r0 + min(128 * blk, t.count - 1));  // of the block's rows
     const float kfac = a.scale * kLog2e;
-    const uint32_t tS = tb + 128 * blk + lanes, tO = tb + 256 + 128 * blk + lanes;
+    const uint32_t tS = tb + 128 * blk + 64 * half + lanes, tO = tb + 256 + 128 * blk + 64 * half + lanes;
     float R = 0.0f, l = 0.0f;
     bool fresh = true;  // the row has met no score yet: its reference is still to be set
     for (int i = 0; i < nb; ++i) {
       if (ok) ok = wait(&bar.s_full[blk], i & 1);
-      if (!__all_sync(kFull, ok)) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(kFull, ok);  // (the pair's barriers are passed all the same)
       tc_fence_after();
       const bool masked = (i + 1) * kTok > fewest;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        uint32_t x[64];
-        load64(tS + 64 * h, x);
+        uint32_t x[32];
+        load32(tS + 32 * h, x);
         if (masked) {
-          const int hi = sees - i * kTok - 64 * h;  // tokens of the half that the row sees
+          const int hi = sees - i * kTok - 64 * half - 32 * h;  // tokens of these that the row sees
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
+          for (int e = 0; e < 32; ++e)
             if (e >= hi) x[e] = 0xff800000u;  // -inf
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; e += 8)
+        for (int e = 0; e < 32; e += 8)
 #pragma unroll
           for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
-        const float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kfac, -R);
-        // The reference moves (and l, O and the first half's weights with it, all by a power of
-        // two) only when a row meets its first score or one passes it by more than the slack.
-        if (__any_sync(kFull, mx > (fresh ? -INFINITY : kTop + kSlack))) {
+        float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kfac, -R);
+        // The reference moves (and l, O and the stored weights of the tile with it, all by a power
+        // of two) only when a row meets its first score or one passes it by more than the slack.
+        if (pair_any(pair, mx > (fresh ? -INFINITY : kTop + kSlack))) {
+          if (half == 0) red_s[row] = mx;
+          pair_any(pair, false);
+          if (half == 1) red_s[row] = mx = fmaxf(mx, red_s[row]);
+          pair_any(pair, false);
+          mx = red_s[row];
           const bool first = fresh && mx > -INFINITY;
           const float to = ceilf(mx) - kTop, up = first ? to : fmaxf(to, 0.0f);
           const float al = first ? 1.0f : up < 127.0f ? __int_as_float((127 - (int)up) << 23) : 0.0f;
@@ -291,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
           tmem_wait_st();  // (the first half may have just rescaled O, and has stored its P: both are read below)
           if (i > 0) {     // every product issued before this S has completed
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t v[16];
               tmem_ld<16>(tO + 16 * c, v);
               tmem_wait_ld();
@@ -304,35 +337,30 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
             }
           }
           if (h) {
+            uint32_t v[16];
+            tmem_ld<16>(tS, v);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[16];
-              tmem_ld<16>(tS + 16 * c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                asm volatile("" : "+r"(v[e]));
-                const float2 w = __half22float2(u32_as_h2(v[e]));
-                v[e] = h2_as_u32(__floats2half2_rn(w.x * al, w.y * al));
-              }
-              tmem_st<16>(tS + 16 * c, v);
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(v[e]));
+              const float2 w = __half22float2(u32_as_h2(v[e]));
+              v[e] = h2_as_u32(__floats2half2_rn(w.x * al, w.y * al));
             }
+            tmem_st<16>(tS, v);
           }
+          pair_any(pair, false);  // (red_s has been read)
         }
         const float2 nR2 = make_float2(-R, -R), kf2 = make_float2(kfac, kfac);
         float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t p[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = __ffma2_rn(get(x, 32 * c + 2 * e), kf2, nR2);
-            const float2 w = make_float2(ex2(y.x), ex2(y.y));
-            l2[e & 1] = __fadd2_rn(l2[e & 1], w);
-            p[e] = h2_as_u32(__floats2half2_rn(w.x, w.y));
-          }
-          tmem_st<16>(tS + 32 * h + 16 * c, p);
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = __ffma2_rn(get(x, 2 * e), kf2, nR2);
+          const float2 w = make_float2(ex2(y.x), ex2(y.y));
+          l2[e & 1] = __fadd2_rn(l2[e & 1], w);
+          p[e] = h2_as_u32(__floats2half2_rn(w.x, w.y));
         }
+        tmem_st<16>(tS + 16 * h, p);
         const float2 ls = __fadd2_rn(l2[0], l2[1]);
         l += ls.x + ls.y;
       }
@@ -346,35 +374,40 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
     if (nb > 0 && ok) ok = wait(&bar.o_full[blk], 0);
     tc_fence_after();
     if (!ok) failed_s = 1;
+    if (half == 0) red_s[row] = l;
+    softmax_sync();
+    if (half == 1) red_s[row] = l = l + red_s[row];
     softmax_sync();  // (the other block's products have read their queries too, whose place the rows take)
     if (failed_s) {
       if (tid == 0) set_error(const_cast<uint8_t*>(a.pool), KVQ_DEVERR_TIMEOUT);
     } else if (128 * blk < t.count) {
+      l = red_s[row];
       const float g = 1.0f / l;
-      uint8_t* stage = sm + Smem::Q + warp * 32 * kStageRow;
+      uint8_t* stage = sm + Smem::Q + pair * 32 * kStageRow;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
-        uint32_t v[64];
-        if (nb > 0) load64(tO + 64 * c, v);
+        uint32_t v[32];
+        if (nb > 0) load32(tO + 32 * c, v);
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
+        for (int e = 0; e < 32; e += 8) {
           uint32_t o[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float2 x = get(v, e + 2 * u);
             o[u] = nb == 0 || l == 0.0f ? 0u : h2_as_u32(__floats2half2_rn(x.x * g, x.y * g));  // (a NaN score makes its row NaN)
           }
-          *reinterpret_cast<uint4*>(stage + lane * kStageRow + 128 * c + 2 * e) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(stage + lane * kStageRow + 128 * half + 64 * c + 2 * e) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      __syncwarp();
-      const long long row0 = (long long)(t.q0 + t.r0 + 32 * warp) * a.Hq + head;
-      const int rows = min(32, t.count - 32 * warp);
+      pair_any(pair, false);
+      const int first_row = 128 * blk + 32 * quad;
+      const long long row0 = (long long)(t.q0 + t.r0 + first_row) * a.Hq + head;
+      const int rows = min(32, t.count - first_row);
 #pragma unroll 4
-      for (int r = lane >> 4; r < rows; r += 2)
+      for (int r = 2 * half + (lane >> 4); r < rows; r += 4)
         st_chk(reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + (row0 + (long long)r * a.Hq) * kLatentHead) + (lane & 15),
                *reinterpret_cast<const uint4*>(stage + r * kStageRow + 16 * (lane & 15)), a.out_span, a.pool);
-      if (real && a.lse)
+      if (real && half == 0 && a.lse)
         st_chk(a.lse + row0 + (long long)lane * a.Hq, l == 0.0f ? -INFINITY : (R + log2f(l)) * (1.0f / kLog2e), a.lse_span, a.pool);
     }
   }
