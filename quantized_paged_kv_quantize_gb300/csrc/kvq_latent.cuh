@@ -66,7 +66,8 @@ __device__ __forceinline__ void latent_codes16(const uint32_t* w, uint32_t sb, u
 struct LatentArgs : ChunkArgs {
   int causal;
   // The tcgen05 kernel's CTAs where row tiles are split: CTA c leaves its rows' partials at
-  // ws_o [c][rows][L] and ws_ml [c][rows][2], and (first CTA, parts) of row tile i is at map[i].
+  // ws_o [c][rows][L] and ws_ml [c][rows][2], and (first CTA, parts) of row tile i < ctas is at
+  // map[i].
   // 0: a CTA takes a whole row tile.
   int ctas;
   int2* map;

@@ -473,8 +473,7 @@ LatentPlan plan_latent(const kvq_latent* c, int total_q, int num_seqs, int num_q
   if (c->cfg.io_dtype == KVQ_F16) {
     const int rows = latent_umma_rows(max_q_len, num_q_heads);
     const int ctas = umma_ctas(num_q_heads, total_q, num_seqs, max_q_len, max_seq_len);
-    const size_t tiles = (size_t)chunk_tile_bound(total_q, num_seqs, num_q_heads, rows);
-    if (ctas) p.workspace_bytes = std::max(p.workspace_bytes, (size_t)ctas * rows * row + tiles * sizeof(int2));
+    if (ctas) p.workspace_bytes = std::max(p.workspace_bytes, (size_t)ctas * (rows * row + sizeof(int2)));
     if (on_umma(c, out_dtype == KVQ_F32)) {
       p.ctas = ctas;
       p.num_splits = ctas ? std::min(ctas, (max_seq_len + 127) / 128) : 1;

@@ -634,6 +634,9 @@ def kvq_latent_set_scale_from_amax(cache: LatentCache, amax: torch.Tensor, strea
 
 def _take_rows(t, name: str, cache, dtype, shape) -> tuple:
     """The data pointer and leading strides (elements) of `t`, whose last dimension is contiguous: slices of wider rows."""
+    strides = t.stride()
+    if t.dtype is dtype and t.shape == shape and strides[-1:] == (1,) and t.get_device() == cache.device and 1 not in shape:
+        return (t.data_ptr(), *strides[:-1])
     have = t.shape
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -641,9 +644,9 @@ def _take_rows(t, name: str, cache, dtype, shape) -> tuple:
         raise ValueError(f"{name}: shape {tuple(have)}, expected {tuple('*' if w is None else w for w in shape)}")
     if t.get_device() != cache.device:
         raise ValueError(f"{name}: on {t.device}, the cache is on {cache.pool.device}")
-    if have[-1] != 1 and t.stride(-1) != 1:
+    if have[-1] != 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (t.data_ptr(), *(0 if n <= 1 else s for n, s in zip(have[:-1], t.stride())))
+    return (t.data_ptr(), *(0 if n <= 1 else s for n, s in zip(have[:-1], strides)))
 
 
 def kvq_latent_write(cache: LatentCache, latent, k_rope, positions, cos_sin, *, slot_mapping=None, q_rope=None,

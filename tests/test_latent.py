@@ -517,3 +517,85 @@ def test_prompt_rows_that_see_nothing():
         out, lse = p.run()
         none = torch.cat([torch.arange(302 * i, 302 * i + 2) for i in range(20)])
         assert bool((out[none] == 0).all()) and bool((lse[none] == -math.inf).all())
+
+
+def test_prompt_without_keys():
+    p = Prompt([3, 2], [0, 0], 2, seed=7)
+    out, lse = p.run()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+# ---------------------------------------------------------------- calls that the documentation allows
+def test_ranges_that_repeat():
+    """Chunk ranges that are no ascending list: the backward ones are flagged, and nothing is written outside the buffers."""
+    K = kvq()
+    b = Batch("fp8_per_token_head", 512, [1] * 60, [300] * 60, 16, seed=15)
+    q, out = b.q[:1].cuda(), guarded((1, 16, 512), F16, fill=float("nan"), name="out")
+    cu = torch.tensor([0, 1] * 30 + [0], dtype=torch.int32).cuda()
+    _, ws = K.kvq_latent_plan(b.cache, 1, 60, 16, max_q_len=1, max_seq_len=300)
+    work = guarded(max(ws, 16), torch.uint8, fill=0xFF, name="workspace")
+    K.kvq_latent_attention(b.cache, q, cu, b.table.cuda(), torch.full((60,), 300, dtype=torch.int32).cuda(), out, max_q_len=1,
+                           max_seq_len=300, softmax_scale=b.scale, workspace=work)
+    torch.cuda.synchronize()
+    assert K.kvq_latent_read_errors(b.cache) == 0x100
+
+
+def test_many_sequences():
+    """More sequences than a plan of parts takes, most of them short, and a batch of one long one."""
+    n = [(37 * b) % 50 for b in range(700)]
+    check(Batch("int8_per_token_head", 256, [1] * 700, n, 2, seed=16))
+    check(Batch("nvfp4", 512, [1], [20000], 3, seed=17))
+
+
+def test_unequal_lengths():
+    """One long sequence among short ones, with and without split ranges: parts of every size."""
+    for heads in (16, 64, 128):
+        check(Batch("fp8_per_token_head", 512, [1, 2, 1, 3, 1], [9000, 5, 130, 700, 1], heads, seed=18))
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond four gigabytes of a pool."""
+    K = kvq()
+    pages = 420000
+    cfg = K.make_latent_config(pages, P, 512, R, "fp8_per_token_head", F16)
+    pool = torch.empty(K.kvq_latent_bytes(cfg), dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 1 << 32
+    cache = K.kvq_latent_alloc(cfg, pool)
+    n = 200
+    table = torch.arange(pages - 13, pages, dtype=torch.int32)[None]
+    slots = (table[0, torch.arange(n) // P] * P + torch.arange(n) % P).int().cuda()
+    c, kr = torch.randn(n, 512).half().cuda(), torch.randn(n, R).half().cuda()
+    K.kvq_latent_write(cache, c, kr, torch.zeros(n, dtype=torch.int32).cuda(), identity_table(1), slot_mapping=slots)
+    back, rope = torch.empty_like(c), torch.empty_like(kr)
+    K.kvq_latent_read(cache, slots, back, rope)
+    assert torch.equal(rope, kr)
+    q, out = torch.randn(1, 8, 576).half().cuda(), torch.empty(1, 8, 512).half().cuda()
+    _, ws = K.kvq_latent_plan(cache, 1, 1, 8, max_q_len=1, max_seq_len=n)
+    K.kvq_latent_attention(cache, q, torch.tensor([0, 1]).int().cuda(), table.cuda(), torch.tensor([n]).int().cuda(), out, max_q_len=1,
+                           max_seq_len=n, softmax_scale=0.05, workspace=torch.empty(max(ws, 16), dtype=torch.uint8, device="cuda"))
+    assert K.kvq_latent_read_errors(cache) == 0
+    k = torch.cat([back, rope], 1).double()  # (fp16 rows of fp8 codes times their scales: 2^-11 of each)
+    p = torch.softmax(q.double()[0] @ k.T * 0.05, -1)
+    mass = p @ back.double().abs()
+    assert bool(((out.double()[0] - p @ back.double()).abs() <= 2.0 ** -11 * 4 * mass + 0.05 * 600 * 4 * 2.0 ** -11 * mass).all())
+
+
+def test_python_refusals():
+    K = kvq()
+    b = Batch("fp8_per_token_head", 512, [1], [40], 4, seed=19)
+    args = lambda **kw: dict(dict(q=b.q.cuda(), cu=b.cu.cuda(), table=b.table.cuda(), n=torch.tensor([40]).int().cuda(),  # noqa: E731
+                                  out=torch.empty(1, 4, 512).half().cuda()), **kw)
+    for bad in (dict(q=b.q.float().cuda()), dict(q=b.q.cuda()[..., :512]), dict(cu=b.cu.long().cuda()), dict(cu=b.cu),
+                dict(out=torch.empty(1, 4, 576).half().cuda()), dict(out=torch.empty(1, 4, 512).bfloat16().cuda()),
+                dict(n=torch.tensor([40, 1]).int().cuda()), dict(table=b.table.cuda()[0])):
+        a = args(**bad)
+        with pytest.raises((ValueError, K.KVQError)):
+            K.kvq_latent_attention(b.cache, a["q"], a["cu"], a["table"], a["n"], a["out"], max_q_len=1, max_seq_len=40, softmax_scale=0.1)
+    with pytest.raises(ValueError):
+        K.kvq_latent_read(b.cache, torch.zeros(2, dtype=torch.int32).cuda(), torch.empty(3, 512).half().cuda())
+    with pytest.raises(ValueError):
+        K.kvq_latent_write(b.cache, torch.zeros(512, 2).half().cuda().t(), torch.zeros(2, R).half().cuda(),
+                           torch.zeros(2, dtype=torch.int32).cuda(), identity_table(1))
+    with pytest.raises(AttributeError):
+        K.kvq_decode_attention(b.cache, b.q.cuda(), b.table.cuda(), torch.tensor([40]).int().cuda(), torch.empty(1, 4, 512).half().cuda(),
+                               max_seq_len=40, softmax_scale=0.1)
