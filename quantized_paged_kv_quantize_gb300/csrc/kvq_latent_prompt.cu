@@ -46,7 +46,7 @@ constexpr int kUnit = 128 * 128;       // 128 rows of 64 channels
 constexpr int kUnits = 8, kKeyUnits = 3, kTileUnits = 5;
 constexpr int kStageRow = 256 + 16;    // an output row in shared memory; the pad spreads the banks
 constexpr float kTop = 6.0f, kSlack = 8.0f;
-constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 64);
+constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
 constexpr uint64_t kSwizzle128 = 2ull << 61;  // of a shared-memory matrix descriptor
 
 struct Smem {
@@ -56,7 +56,7 @@ struct Smem {
   static constexpr size_t dynamic() { return BYTES + 1024; }
 };
 struct Bars {
-  uint64_t q_full, full[kUnits], free[kUnits], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2];  // (k, v: by tile % 2)
 };
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
@@ -96,6 +96,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return a;
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }  // warps 0-15
+// The issuing warps' turns: block b's warp waits for the other's products to be issued, and lets it go on.
+__device__ __forceinline__ void turn_wait(int b) { asm volatile("bar.sync %0, 64;" ::"r"(10 + b) : "memory"); }
+__device__ __forceinline__ void turn_over(int b) { asm volatile("bar.arrive %0, 64;" ::"r"(11 - b) : "memory"); }
 // The two warps that share rows (one of eight pairs): whether x holds in either.
 __device__ __forceinline__ bool pair_any(int pair, bool x) {
   uint32_t r;
@@ -121,11 +124,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
     if (lane == 0) tile_s = t;
   } else if (warp == 1) {
     if (elect_one()) {
-      for (int i = 0; i < kUnits; ++i) {
-        mbar_init(&bar.full[i], 128);
-        mbar_init(&bar.free[i], 1);
-      }
       for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.k_full[i], 128);
+        mbar_init(&bar.v_full[i], 128);
+        mbar_init(&bar.k_free[i], 2);
+        mbar_init(&bar.v_free[i], 2);
         mbar_init(&bar.s_full[i], 1);
         mbar_init(&bar.p_full[i], 8);
         mbar_init(&bar.o_full[i], 1);
@@ -178,13 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
     const __half* k = static_cast<const __half*>(a.k) + k0 * a.k_stride + head * a.k_head_stride + 8 * c;
     const __half* v = static_cast<const __half*>(a.v) + k0 * a.v_stride + head * a.v_head_stride + 8 * c;
     const __half* kr = static_cast<const __half*>(a.k_rope) + k0 * a.k_rope_stride + 8 * c;
-    int slot = 0, round = 0;
+    // Tile i's keys take the places of the last key unit and the values of tile i - 2, its values
+    // those of the first key units of tile i - 1.
+    int slot = 0;
     for (int i = 0; i < n && ok; ++i) {
 #pragma unroll 1
       for (int u = 0; u < kTileUnits; ++u) {
-        const __half* src = u < 2 ? k + 64 * u : u == 2 ? kr : v + 64 * (u - kKeyUnits);
+        const bool wraps = slot == (u == kKeyUnits ? kUnits - 1 : 0);  // (of a tile's values: in the ring's last unit and its first)
+        const __half* src = u < 2 ? k + 64 * u : u == 2 ? kr : v + 64 * ((u - kKeyUnits) ^ (wraps ? 1 : 0));
         const long long stride = u < 2 ? a.k_stride : u == 2 ? a.k_rope_stride : a.v_stride;
-        if (round > 0 && ok) ok = wait(&bar.free[slot], (round - 1) & 1);
+        if (u == 1 && i >= 2 && ok) ok = wait(&bar.v_free[i & 1], ((i - 2) >> 1) & 1);
+        if (u == kKeyUnits && i >= 1 && ok) ok = wait(&bar.k_free[(i - 1) & 1], ((i - 1) >> 1) & 1);
         if (!__all_sync(kFull, ok)) {
           ok = false;
           break;
@@ -195,86 +202,70 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
           const bool there = tok < most;
           copy16(base + Smem::RING + slot * kUnit + e * 2048, src + (there ? tok : 0) * stride, there);
         }
-        copy_arrive(&bar.full[slot]);
-        if (++slot == kUnits) {
-          slot = 0;
-          ++round;
-        }
+        if (u == kKeyUnits - 1) copy_arrive(&bar.k_full[i & 1]);
+        if (u == kTileUnits - 1) copy_arrive(&bar.v_full[i & 1]);
+        slot = (slot + 1) & (kUnits - 1);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kIssueWarp) {
     // ------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kIssueWarp && n > 0) {
-      const uint64_t dq = umma_sdesc(smem_u32(sm + Smem::Q), 16, 1024) | kSwizzle128;
-      const uint64_t dr = umma_sdesc(smem_u32(sm + Smem::RING), 16, 1024) | kSwizzle128;  // keys: K-major; values: MN-major, 64 channels
-      const uint32_t tm = uniform(tb);
+    const int b = warp - kIssueWarp, nb = b == 0 ? n0 : b == 1 ? n1 : 0;
+    if (nb > 0) {
+      const int other = b ? n0 : n1;  // tiles from here on are this block's alone
+      const uint64_t Q = umma_sdesc(smem_u32(sm + Smem::Q + b * kKeyUnits * kUnit), 16, 1024) | kSwizzle128;
+      const uint64_t dk = umma_sdesc(smem_u32(sm + Smem::RING), 16, 1024) | kSwizzle128;  // keys: K-major
+      // values: MN-major, 64 channels a unit; in the ring's last unit and its first: those of the first come first
+      const uint64_t dv = umma_sdesc(smem_u32(sm + Smem::RING), kUnit, 1024) | kSwizzle128;
+      const uint64_t dw = umma_sdesc(smem_u32(sm + Smem::RING), (kUnits - 1) * kUnit, 1024) | kSwizzle128;
+      const uint32_t S = uniform(tb + 128 * b), O = uniform(tb + 256 + 128 * b);
       ok = wait_uniform(&bar.q_full, 0);
       fence_proxy_async_smem();
-      // O += P V of a block's last tile, then S of its next (over that P), the blocks in turn.
-      // The tensor core takes no product ahead of the one it works on, so the waits stand
-      // together, before all products of a step, and a tile's units are waited for once.
-      // The fences between the copies and the tensor core's reads stand after the waits.
-      int keys = 0, values = 0;  // tiles whose units have been waited for
-      for (int i = 0; i <= n && ok; ++i) {
-#pragma unroll 1
-        for (int b = 0; b <= last && ok; ++b) {
-          const int nb = b ? n1 : n0;
-          const uint32_t s = uniform(tm + 128 * b);
-          if (i > 0 && i <= nb) {
-            const int unit = kTileUnits * (i - 1) + kKeyUnits, s0 = unit & (kUnits - 1), s1 = (unit + 1) & (kUnits - 1);
-            if (values < i) {
-              ok = wait_uniform(&bar.full[s0], (unit / kUnits) & 1) && wait_uniform(&bar.full[s1], ((unit + 1) / kUnits) & 1);
-              values = i;
-              fence_proxy_async_smem();
-            }
-            if (ok) ok = wait_uniform(&bar.p_full[b], (i - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t B0 = dr + uniform(s0 * (kUnit >> 4)), B1 = dr + uniform(s1 * (kUnit >> 4));
-            const uint32_t after = uniform(i - 1), free = uniform(b == last), end = uniform(i == nb);
-            if (elect_one()) {
+      // A step: O += P V of the last tile, then S of the next (over that P).  The two warps take
+      // turns, so that one's waits and fences pass during the other's products.  The
+      // fences between the copies and the tensor core's reads stand after the waits.  (A warp
+      // whose wait ran out still takes its turns: the other one waits for them.)
+      const int turns = min(n0, n1) > 0 ? min(n0, n1) + 1 : 0;
+      for (int i = 0; i <= nb; ++i) {
+        const int j = i - 1, vu = kTileUnits * j + kKeyUnits, ku = kTileUnits * i;
+        const int s0 = vu & (kUnits - 1), s1 = (vu + 1) & (kUnits - 1);
+        const uint64_t V = s1 ? dv + uniform(s0 * (kUnit >> 4)) : dw;
+        uint64_t K[kKeyUnits];
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                umma_f16_ts(s + 256 + 64 * (e >> 3), s + 64 * ((e >> 2) & 1) + 8 * (e & 3), (e < 8 ? B0 : B1) + (e & 7) * (2048 >> 4), kIdescPV,
-                            (e & 7) > 0 ? 1u : after);
-              if (free) {
-                tc_commit(&bar.free[s0]);
-                tc_commit(&bar.free[s1]);
-              }
-              if (end) tc_commit(&bar.o_full[b]);
-            }
-            __syncwarp();
+        for (int p = 0; p < kKeyUnits; ++p) K[p] = dk + uniform(((ku + p) & (kUnits - 1)) * (kUnit >> 4));
+        const uint32_t after = uniform(j);
+        if (i > 0 && ok) ok = wait_uniform(&bar.v_full[j & 1], (j >> 1) & 1) && wait_uniform(&bar.p_full[b], j & 1);
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (i < turns && i + b > 0) turn_wait(b);
+        if (i > 0) {
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              umma_f16_ts(O, S + 64 * (e >> 2) + 8 * (e & 3), V + e * (2048 >> 4), kIdescPV, e > 0 ? 1u : after);
+            for (int u = 0; u <= (j >= other); ++u) tc_commit(&bar.v_free[j & 1]);
+            if (i == nb) tc_commit(&bar.o_full[b]);
           }
-          if (i < nb) {
-            const int unit = kTileUnits * i;
-            if (keys <= i) {
+          __syncwarp();
+        }
+        if (i < nb) {
+          if (ok) ok = wait_uniform(&bar.k_full[i & 1], (i >> 1) & 1);
+          fence_proxy_async_smem();
+          if (ok && elect_one()) {
 #pragma unroll
-              for (int p = 0; p < kKeyUnits; ++p)
-                if (ok) ok = wait_uniform(&bar.full[(unit + p) & (kUnits - 1)], ((unit + p) / kUnits) & 1);
-              if (!ok) break;
-              keys = i + 1;
-              fence_proxy_async_smem();
-              tc_fence_after();
-            }
-            const uint64_t A = dq + uniform(kKeyUnits * b * (kUnit >> 4));
-            uint64_t B[kKeyUnits];
-#pragma unroll
-            for (int p = 0; p < kKeyUnits; ++p) B[p] = dr + uniform(((unit + p) & (kUnits - 1)) * (kUnit >> 4));
-            const uint32_t free = uniform(b == last);
-            if (elect_one()) {
-#pragma unroll
-              for (int e = 0; e < 4 * kKeyUnits; ++e)
-                umma_f16_ss(s, A + (e >> 2) * (kUnit >> 4) + (e & 3) * (32 >> 4), B[e >> 2] + (e & 3) * (32 >> 4), kIdescQK, e > 0 ? 1u : 0u);
-              tc_commit(&bar.s_full[b]);
-              if (free) {
-#pragma unroll
-                for (int p = 0; p < kKeyUnits; ++p) tc_commit(&bar.free[(unit + p) & (kUnits - 1)]);
-              }
-            }
-            __syncwarp();
+            for (int e = 0; e < 4 * kKeyUnits; ++e)
+              umma_f16_ss(S, Q + (e >> 2) * (kUnit >> 4) + (e & 3) * (32 >> 4), K[e >> 2] + (e & 3) * (32 >> 4), kIdescQK, e > 0 ? 1u : 0u);
+            tc_commit(&bar.s_full[b]);
           }
+          __syncwarp();
+        }
+        if (i + b < turns) turn_over(b);
+        if (i < nb) {
+          if (ok && elect_one()) {
+            for (int u = 0; u <= (i >= other); ++u) tc_commit(&bar.k_free[i & 1]);
+          }
+          __syncwarp();
         }
       }
     }
