@@ -80,6 +80,7 @@ struct LatentArgs : ChunkArgs {
   const void* v;
   long long k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride;
   int total_k;
+  int group;  // heads whose CTAs run together
 };
 
 // The rows of a CTA.  Expanded: a sequence's tokens are its range of cu_k.

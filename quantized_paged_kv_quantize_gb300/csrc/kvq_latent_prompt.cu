@@ -12,21 +12,27 @@
 // Roles (24 warps, one CTA per SM; registers are shared out between the warpgroups):
 //  warps 0-7, 8-15  softmax of two blocks of 128 rows; the tensor cores run one block's
 //                   products during the other's softmax.  Two threads share a row, 64 tokens
-//                   of a tile each (with one thread a row, eight warps, 2048 queries of 128
-//                   heads over 8192 keys took 1.13 ms, as long as their softmax);
+//                   of a tile each, all of them in registers at once (in two halves, with
+//                   two exchanges between the threads: 2000 instead of 1400 cycles a tile);
 //  warps 16-19      copy queries, keys, rotary parts and values into shared memory, 16 bytes a
 //                   copy, rows past the sequence's end as zeros;
-//  warp 20          issues the products (21-23 only fill its warpgroup).
+//  warps 20, 21     issue the products of a block each (22-23 only fill their warpgroup).  They
+//                   take turns: the tensor core takes no product ahead of the one it works on,
+//                   so one's waits and fences pass during the other's products (one warp for
+//                   both blocks: 1.03 instead of 0.89 ms for the first case below; without
+//                   turns the blocks fall into step, 0.99 ms).
 // Both blocks use the same keys and values.  These go through a ring of eight units of 16 KB
 // (128 tokens x 64 channels in the 128-byte swizzle): a tile is three units of keys and two
-// of values, so that the copies run 0.6 tiles ahead beside the 96 KB of queries.
+// of values, so that the copies run 0.6 tiles ahead beside the 96 KB of queries.  A tile's
+// values are one operand of 128 columns (issuing a product takes 75 cycles, twice what one
+// of 64 columns is worth).
 // Tensor memory: S_0 S_1 O_0 O_1, 128 columns each; P of 64 tokens goes over the first 32 of
 // their scores' 64 columns.
 //
-// Bound by the tensor cores and by the waits between a block's products and its softmax: the
-// products are half of the cycles.  Measured: 2048 queries of 128 heads over 8192 keys, causal,
-// 1.07 ms (1120 TFLOP/s); three prompts of 300 to 1500 queries, 32 heads, 72 us (577 TFLOP/s:
-// two and a half waves of CTAs of unequal lengths).
+// Bound by a block's turn: its products (20 of 75 cycles and the wait for the weights) and the
+// softmax between them.  Measured: 2048 queries of 128 heads over 8192 keys, causal, 0.83 ms
+// (1450 TFLOP/s); 4096 queries and keys of 32 heads 0.16 ms (1040); three prompts of 1024, 32
+// heads, 78 us (a CTA's start and end beside 8 tiles).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -40,11 +46,18 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTok = 128, kRows = 256;
 constexpr int kThreads = 768;
 constexpr int kCopyWarp = 16, kIssueWarp = 20;
-// Registers a thread (the launch gives 80): 512 x 88 + 128 x 72 + 128 x 56 <= 768 x 80.
-constexpr int kRegsSoftmax = 88, kRegsCopy = 72, kRegsIssue = 56;
+// Registers a thread (the launch gives 80): 512 x 96 + 128 x 40 + 128 x 56 <= 768 x 80.
+constexpr int kRegsSoftmax = 96, kRegsCopy = 40, kRegsIssue = 56;
+static_assert(512 * kRegsSoftmax + 128 * (kRegsCopy + kRegsIssue) <= kThreads * 80, "registers");
 constexpr int kUnit = 128 * 128;       // 128 rows of 64 channels
 constexpr int kUnits = 8, kKeyUnits = 3, kTileUnits = 5;
 constexpr int kStageRow = 256 + 16;    // an output row in shared memory; the pad spreads the banks
+// CTAs run by groups of heads, a group's row tiles longest first: the row tiles of a head read
+// its keys and values together, of heads whose keys and values are 32 MB at most (a fraction of
+// the L2 cache).  Heads side by side, whatever their lengths: 0.89 instead of 0.83 ms for 2048
+// queries of 128 heads over 8192 keys (4 TB/s of rereads); a head after the other: 0.20 instead
+// of 0.17 ms for 32 heads of 4096 queries and keys (a long tile begins late).
+constexpr long long kGroupBytes = 32ll << 20;
 constexpr float kTop = 6.0f, kSlack = 8.0f;
 constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128), kIdescPV = umma_idesc_f16_bmn(128, 128);
 constexpr uint64_t kSwizzle128 = 2ull << 61;  // of a shared-memory matrix descriptor
@@ -73,6 +86,15 @@ __device__ __forceinline__ bool wait_uniform(uint64_t* bar, uint32_t parity) { r
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return r != 0;
 }
 // 16 bytes global -> shared; zeros where !there (the source is not read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
@@ -118,7 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
   __shared__ RowTile tile_s;
   __shared__ int failed_s;
   __shared__ float red_s[kRows];  // what a row's two threads exchange
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, head = blockIdx.x % a.Hq, index = blockIdx.x / a.Hq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.group * (gridDim.x / a.Hq);
+  const int head0 = blockIdx.x / group * a.group, heads = min(a.group, a.Hq - head0);
+  const int head = head0 + blockIdx.x % group % heads, index = blockIdx.x % group / heads;
   if (warp == 0) {
     const RowTile t = latent_tile<true>(a, index, kRows, index == 0 && head == 0);
     if (lane == 0) tile_s = t;
@@ -231,11 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
         const int j = i - 1, vu = kTileUnits * j + kKeyUnits, ku = kTileUnits * i;
         const int s0 = vu & (kUnits - 1), s1 = (vu + 1) & (kUnits - 1);
         const uint64_t V = s1 ? dv + uniform(s0 * (kUnit >> 4)) : dw;
-        uint64_t K[kKeyUnits];
-#pragma unroll
-        for (int p = 0; p < kKeyUnits; ++p) K[p] = dk + uniform(((ku + p) & (kUnits - 1)) * (kUnit >> 4));
         const uint32_t after = uniform(j);
         if (i > 0 && ok) ok = wait_uniform(&bar.v_full[j & 1], (j >> 1) & 1) && wait_uniform(&bar.p_full[b], j & 1);
+        const bool there = i < nb && ok && __all_sync(kFull, mbar_done(&bar.k_full[i & 1], (i >> 1) & 1));
         fence_proxy_async_smem();
         tc_fence_after();
         if (i < turns && i + b > 0) turn_wait(b);
@@ -250,8 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
           __syncwarp();
         }
         if (i < nb) {
-          if (ok) ok = wait_uniform(&bar.k_full[i & 1], (i >> 1) & 1);
-          fence_proxy_async_smem();
+          if (ok && !there) {
+            ok = wait_uniform(&bar.k_full[i & 1], (i >> 1) & 1);
+            fence_proxy_async_smem();
+          }
+          uint64_t K[kKeyUnits];
+#pragma unroll
+          for (int p = 0; p < kKeyUnits; ++p) K[p] = dk + uniform(((ku + p) & (kUnits - 1)) * (kUnit >> 4));
           if (ok && elect_one()) {
 #pragma unroll
             for (int e = 0; e < 4 * kKeyUnits; ++e)
@@ -287,79 +314,70 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prompt_kernel(const __grid
       ok = __all_sync(kFull, ok);  // (the pair's barriers are passed all the same)
       tc_fence_after();
       const bool masked = (i + 1) * kTok > fewest;
+      uint32_t x[64];
+      tmem_ld<32>(tS, x);
+      tmem_ld<32>(tS + 32, x + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 64; ++e) asm volatile("" : "+r"(x[e]));  // (no use before the wait)
+      if (masked) {
+        const int hi = sees - i * kTok - 64 * half;  // tokens of these that the row sees
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= hi) x[e] = 0xff800000u;  // -inf
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 64; e += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+      float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kfac, -R);
+      // The reference moves (and l and O with it, by a power of two) only when a row meets its
+      // first score or one passes it by more than the slack.
+      if (pair_any(pair, mx > (fresh ? -INFINITY : kTop + kSlack))) {
+        if (half == 0) red_s[row] = mx;
+        pair_any(pair, false);
+        if (half == 1) red_s[row] = mx = fmaxf(mx, red_s[row]);
+        pair_any(pair, false);
+        mx = red_s[row];
+        const bool first = fresh && mx > -INFINITY;
+        const float to = ceilf(mx) - kTop, up = first ? to : fmaxf(to, 0.0f);
+        const float al = first ? 1.0f : up < 127.0f ? __int_as_float((127 - (int)up) << 23) : 0.0f;
+        fresh = fresh && !first;
+        R += up;
+        l *= al;
+        if (i > 0) {  // every product issued before this S has completed
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t x[32];
-        load32(tS + 32 * h, x);
-        if (masked) {
-          const int hi = sees - i * kTok - 64 * half - 32 * h;  // tokens of these that the row sees
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e >= hi) x[e] = 0xff800000u;  // -inf
-        }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) m4[u] = max3(m4[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
-        float mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kfac, -R);
-        // The reference moves (and l, O and the stored weights of the tile with it, all by a power
-        // of two) only when a row meets its first score or one passes it by more than the slack.
-        if (pair_any(pair, mx > (fresh ? -INFINITY : kTop + kSlack))) {
-          if (half == 0) red_s[row] = mx;
-          pair_any(pair, false);
-          if (half == 1) red_s[row] = mx = fmaxf(mx, red_s[row]);
-          pair_any(pair, false);
-          mx = red_s[row];
-          const bool first = fresh && mx > -INFINITY;
-          const float to = ceilf(mx) - kTop, up = first ? to : fmaxf(to, 0.0f);
-          const float al = first ? 1.0f : up < 127.0f ? __int_as_float((127 - (int)up) << 23) : 0.0f;
-          fresh = fresh && !first;
-          R += up;
-          l *= al;
-          tmem_wait_st();  // (the first half may have just rescaled O, and has stored its P: both are read below)
-          if (i > 0) {     // every product issued before this S has completed
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[16];
-              tmem_ld<16>(tO + 16 * c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                asm volatile("" : "+r"(v[e]));
-                v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-              }
-              tmem_st<16>(tO + 16 * c, v);
-            }
-          }
-          if (h) {
-            uint32_t v[16];
-            tmem_ld<16>(tS, v);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[8];
+            tmem_ld<8>(tO + 8 * c, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               asm volatile("" : "+r"(v[e]));
-              const float2 w = __half22float2(u32_as_h2(v[e]));
-              v[e] = h2_as_u32(__floats2half2_rn(w.x * al, w.y * al));
+              v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
             }
-            tmem_st<16>(tS, v);
+            tmem_st<8>(tO + 8 * c, v);
           }
-          pair_any(pair, false);  // (red_s has been read)
         }
-        const float2 nR2 = make_float2(-R, -R), kf2 = make_float2(kfac, kfac);
-        float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        pair_any(pair, false);  // (red_s has been read)
+      }
+      const float2 nR2 = make_float2(-R, -R), kf2 = make_float2(kfac, kfac);
+      float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 y = __ffma2_rn(get(x, 2 * e), kf2, nR2);
+          const float2 y = __ffma2_rn(get(x, 32 * h + 2 * e), kf2, nR2);
           const float2 w = make_float2(ex2(y.x), ex2(y.y));
           l2[e & 1] = __fadd2_rn(l2[e & 1], w);
           p[e] = h2_as_u32(__floats2half2_rn(w.x, w.y));
         }
         tmem_st<16>(tS + 16 * h, p);
-        const float2 ls = __fadd2_rn(l2[0], l2[1]);
-        l += ls.x + ls.y;
       }
+      const float2 ls = __fadd2_rn(l2[0], l2[1]);
+      l += ls.x + ls.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -420,7 +438,9 @@ cudaError_t launch_latent_prompt_umma(const kvq_latent*, const LatentArgs& a, cu
   if (e != cudaSuccess) return e;
   const long long grid = chunk_tile_bound(a.total_q, a.B, 1, kRows) * a.Hq;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  latent_prompt_kernel<<<(unsigned)grid, kThreads, smem, s>>>(a);
+  LatentArgs args = a;
+  args.group = (int)std::min((long long)a.Hq, std::max(1ll, kGroupBytes / (std::max(1ll, (long long)a.max_seq_len) * 2 * kLatentHead * 2)));
+  latent_prompt_kernel<<<(unsigned)grid, kThreads, smem, s>>>(args);
   return cudaGetLastError();
 }
 
