@@ -510,6 +510,13 @@ def test_prompt_streams_and_graphs():
     assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("max_k", [20000, 70000])
+def test_prompt_head_groups(max_k):
+    """Bounds for which heads run in groups (of three and two of five; one by one), over ranges of many tiles."""
+    Prompt([300, 40, 1], [2500, 40, 2200], 5, seed=9, extra=1).check(max_k=max_k)
+    Prompt([300, 40], [1500, 700], 5, seed=10).check(causal=False, max_k=max_k)
+
+
 def test_prompt_rows_that_see_nothing():
     """Tiles of rows without a key beside tiles with many: their zeros are not written over by copies in flight."""
     p = Prompt([2, 300] * 20, [0, 300] * 20, 8, seed=6)
